@@ -20,6 +20,13 @@ Shapes (D = 128):
                    bfloat16), conv_w [L][3*H*D][4], ring [L][3][3*H*D] float32
   conv ring        ring [L][3][C] float32, raw conv input rows [L][T][C]
   batched copy     table = copy_table(srcs, dsts) -> int64 device tensor [2n]
+  packed prompts   R rows of B sequences one after another: q, k, v, g
+                   [R][H][D], beta [R][H], o [R][H][D]; offsets [B+1] int32 on
+                   the device; s_ptrs = state_table([states]) or any int64 [B]
+  linear attention q, k [R][Hk][D], v, o [R][H][D], g [R][H] float32 always
+                   (the step: [L][B][..] in place of [R][..])
+  log probs        logits [t][V], tokens [t], lp and entropy [t] float32,
+                   top_ids [t][n] int32 or uint32, top_lp [t][n] float32
   greedy accept    logits [t][V] (row stride free, elements contiguous),
                    drafts [t-1], vam [t], out2 [2] as int32 or uint32,
                    work = accept_workspace()
@@ -40,6 +47,7 @@ ACCEPT_WORK_BYTES = 12288
 NO_TOKEN = 0xFFFFFFFF
 RING_ROWS = 3
 MAX_PREV_ROUNDS = 4
+TOP_MAX = 32
 
 
 class _PrevRound(ctypes.Structure):
@@ -92,6 +100,17 @@ def load():
     lib.kda_row_ops.argtypes = [p] * 11 + [i, i, i, i, p]
     lib.kda_verify_round_multi.argtypes = [p, p, ctypes.POINTER(_PrevRound), i, p, p, p, p, p,
                                            p, p, i, i, i, i, p]
+    ll = ctypes.c_longlong
+    lib.kda_prompt.argtypes = [p] * 8 + [i] * 4 + [p, ll, p]
+    lib.kda_linear_prompt.argtypes = [p] * 7 + [i] * 5 + [p, ll, p]
+    lib.kda_linear_step.argtypes = [p] * 6 + [i] * 5 + [p]
+    lib.kda_logprobs.argtypes = [p, i, i, ll, i, p, i, p, p, p, p, p, ll, p]
+    for fn in (lib.kda_prompt_work_bytes, lib.kda_linear_prompt_work_bytes,
+               lib.kda_logprobs_work_bytes):
+        fn.argtypes = [i, i, i]
+        fn.restype = ll
+    for fn in (lib.kda_prompt, lib.kda_linear_prompt, lib.kda_linear_step, lib.kda_logprobs):
+        fn.restype = i
     for fn in (lib.kda_scan_rows, lib.kda_snapshot, lib.kda_replay, lib.kda_scan_batched,
                lib.kda_verify_round, lib.kda_accept_greedy, lib.kda_conv_reroll,
                lib.kda_copy_batch, lib.kda_row_ops, lib.kda_verify_round_multi,
@@ -554,6 +573,193 @@ def kda_copy_batch(table, n: int, words: int, stream=None) -> None:
     _check(lib.kda_copy_batch(_dev(table, "table"), int(n), int(words), _stream(stream)))
 
 
+def _work_bytes(fn, *counts) -> int:
+    n = fn(*counts)
+    if n < 0:
+        raise KdaError(2, _lib.kda_last_error().decode())
+    return n
+
+
+def _workspace(n: int, device) -> torch.Tensor:
+    return torch.empty(n, dtype=torch.uint8, device=device if device is not None else "cuda")
+
+
+def prompt_workspace(R: int, B: int, H: int, device=None) -> torch.Tensor:
+    """Scratch for kda_prompt calls of up to R rows, B sequences and H heads (uint8,
+    contents irrelevant).  Calls that may run at the same time need their own."""
+    return _workspace(_work_bytes(load().kda_prompt_work_bytes, R, B, H), device)
+
+
+def linear_workspace(R: int, B: int, H: int, device=None) -> torch.Tensor:
+    """prompt_workspace for kda_linear_prompt."""
+    return _workspace(_work_bytes(load().kda_linear_prompt_work_bytes, R, B, H), device)
+
+
+def logprobs_workspace(t: int, V: int, n_top: int, device=None) -> torch.Tensor:
+    """Scratch for a kda_logprobs call of t rows of V logits with n_top alternatives."""
+    return _workspace(_work_bytes(load().kda_logprobs_work_bytes, t, V, n_top), device)
+
+
+def _ptr(t, name: str, dtype, shape, device):
+    """Address of a contiguous tensor of the given dtype and shape on `device`; None for None."""
+    if t is None:
+        return None
+    if t.dtype != dtype:
+        raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
+    if t.shape != shape:
+        raise ValueError(f"{name} has shape {tuple(t.shape)}, expected {shape}")
+    if t.device != device:
+        raise ValueError(f"{name} is on {t.device}, expected {device}")
+    if not t.is_contiguous():
+        raise ValueError(f"{name} must be contiguous")
+    return t.data_ptr()
+
+
+def _place(t, stream):
+    """The device of a call's first tensor, which has to be the current one, and its stream."""
+    dev = t.device
+    if dev.type != "cuda":
+        raise ValueError("tensors must be device tensors")
+    if dev.index != torch.cuda.current_device():
+        raise ValueError(f"tensors are on {dev}, the current device is cuda:"
+                         f"{torch.cuda.current_device()}")
+    if stream is None:
+        return dev, torch.cuda.current_stream().cuda_stream
+    if not hasattr(stream, "cuda_stream"):
+        return dev, int(stream)
+    if stream.device != dev:
+        raise ValueError(f"stream is on {stream.device}, the tensors on {dev}")
+    return dev, stream.cuda_stream
+
+
+def _row_dtype(t, name: str) -> int:
+    if t.dtype == torch.bfloat16:
+        return KDA_IN_BF16
+    if t.dtype == torch.float32:
+        return KDA_IN_F32
+    raise TypeError(f"{name} must be float32 or bfloat16, got {t.dtype}")
+
+
+def _work(work, device):
+    if work is None:
+        return None, 0
+    if work.dtype != torch.uint8 or work.device != device or not work.is_contiguous():
+        raise ValueError(f"work must be a contiguous uint8 tensor on {device}")
+    return work.data_ptr(), work.numel()
+
+
+def kda_prompt(s_ptrs, offsets, q, k, v, g, beta, o=None, work=None, stream=None) -> None:
+    """Prompt rows of B packed sequences through one KDA layer, states updated in place.
+
+    s_ptrs [B] int64 holds the states' device addresses ([H][D][D] float32 each; 0
+    leaves the sequence out), offsets [B+1] int32 the sequences' first rows.  q, k,
+    v, g are [R][H][D], beta [R][H]; o [R][H][D] float32 receives the outputs.
+    work = prompt_workspace(R, B, H).  The result is kda_scan_rows's to float32
+    rounding, for any number of rows.
+    """
+    lib = load()
+    dev, st = _place(v, stream)
+    if v.dim() != 3 or v.shape[2] != D:
+        raise ValueError(f"v must be [R][H][{D}], got {tuple(v.shape)}")
+    R, H, _ = shape = v.shape
+    B = s_ptrs.shape[0] if s_ptrs.dim() == 1 else -1
+    dt = _row_dtype(v, "v")
+    wp, wn = _work(work, dev)
+    _check(lib.kda_prompt(
+        _ptr(s_ptrs, "s_ptrs", torch.int64, (B,), dev),
+        _ptr(offsets, "offsets", torch.int32, (B + 1,), dev), _ptr(q, "q", v.dtype, shape, dev),
+        _ptr(k, "k", v.dtype, shape, dev), _ptr(v, "v", v.dtype, shape, dev),
+        _ptr(g, "g", v.dtype, shape, dev), _ptr(beta, "beta", v.dtype, (R, H), dev),
+        _ptr(o, "o", torch.float32, shape, dev), R, B, H, dt, wp, wn, st))
+
+
+def kda_linear_prompt(s_ptrs, offsets, q, k, v, g, o=None, work=None, stream=None) -> None:
+    """Prompt rows of B packed sequences through a layer of linear attention with one
+    decay for each head, states updated in place.
+
+    q, k are [R][Hk][D] with Hk a divisor of H, v [R][H][D], g [R][H] float32 (the
+    log-decays); the rest as kda_prompt, with work = linear_workspace(R, B, H).
+    """
+    lib = load()
+    dev, st = _place(v, stream)
+    if v.dim() != 3 or v.shape[2] != D or q.dim() != 3:
+        raise ValueError(f"v must be [R][H][{D}] and q [R][Hk][{D}], got {tuple(v.shape)} and "
+                         f"{tuple(q.shape)}")
+    R, H, _ = shape = v.shape
+    Hk = q.shape[1]
+    B = s_ptrs.shape[0] if s_ptrs.dim() == 1 else -1
+    dt = _row_dtype(v, "v")
+    wp, wn = _work(work, dev)
+    _check(lib.kda_linear_prompt(
+        _ptr(s_ptrs, "s_ptrs", torch.int64, (B,), dev),
+        _ptr(offsets, "offsets", torch.int32, (B + 1,), dev),
+        _ptr(q, "q", v.dtype, (R, Hk, D), dev), _ptr(k, "k", v.dtype, (R, Hk, D), dev),
+        _ptr(v, "v", v.dtype, shape, dev), _ptr(g, "g", torch.float32, (R, H), dev),
+        _ptr(o, "o", torch.float32, shape, dev), R, B, Hk, H, dt, wp, wn, st))
+
+
+def kda_linear_step(s_ptrs, q, k, v, g, o=None, stream=None) -> None:
+    """One token of each of L x B sessions through layers of linear attention with one
+    decay for each head, states updated in place.
+
+    s_ptrs [L*B] int64 as state_table gives it (0 leaves the session out); q, k
+    [L][B][Hk][D], v and o [L][B][H][D], g [L][B][H] float32.
+    """
+    lib = load()
+    dev, st = _place(v, stream)
+    if v.dim() != 4 or v.shape[3] != D or q.dim() != 4:
+        raise ValueError(f"v must be [L][B][H][{D}] and q [L][B][Hk][{D}], got {tuple(v.shape)} "
+                         f"and {tuple(q.shape)}")
+    L, B, H, _ = shape = v.shape
+    Hk = q.shape[2]
+    keys = (L, B, Hk, D)
+    dt = _row_dtype(v, "v")
+    _check(lib.kda_linear_step(
+        _ptr(s_ptrs, "s_ptrs", torch.int64, (L * B,), dev), _ptr(q, "q", v.dtype, keys, dev),
+        _ptr(k, "k", v.dtype, keys, dev), _ptr(v, "v", v.dtype, shape, dev),
+        _ptr(g, "g", torch.float32, (L, B, H), dev), _ptr(o, "o", torch.float32, shape, dev),
+        L, B, Hk, H, dt, st))
+
+
+def _ids(t, name, shape, device):
+    if t is not None and t.dtype not in (torch.int32, torch.uint32):
+        raise TypeError(f"{name} must be int32 or uint32")
+    return _ptr(t, name, None if t is None else t.dtype, shape, device)
+
+
+def kda_logprobs(logits, tokens=None, lp=None, entropy=None, top_ids=None, top_lp=None,
+                 work=None, stream=None) -> None:
+    """Log probabilities of given tokens, entropy and top alternatives of logits rows.
+
+    logits [t][V] float32 or bfloat16, unit element stride (any row stride >= V).
+    tokens [t] int32 or uint32 with lp [t]; entropy [t]; top_ids [t][n] (int32 or
+    uint32) with top_lp [t][n], n <= TOP_MAX: float32 outputs, each optional.
+    work = logprobs_workspace(t, V, n).
+    """
+    lib = load()
+    dev, st = _place(logits, stream)
+    if logits.dim() != 2:
+        raise ValueError("logits must be a [t][V] tensor")
+    t, V = logits.shape
+    dt = _row_dtype(logits, "logits")
+    if V > 1 and logits.stride(1) != 1:
+        raise ValueError("logits rows must be contiguous")
+    if (top_ids is None) != (top_lp is None):
+        raise ValueError("top_ids and top_lp go together")
+    n = 0
+    if top_ids is not None:
+        if top_ids.dim() != 2:
+            raise ValueError("top_ids must be a [t][n] tensor")
+        n = top_ids.shape[1]
+    wp, wn = _work(work, dev)
+    f32 = torch.float32
+    _check(lib.kda_logprobs(
+        logits.data_ptr(), t, V, logits.stride(0) if t > 1 else V, dt,
+        _ids(tokens, "tokens", (t,), dev), n, _ptr(lp, "lp", f32, (t,), dev),
+        _ptr(entropy, "entropy", f32, (t,), dev), _ids(top_ids, "top_ids", (t, n), dev),
+        _ptr(top_lp, "top_lp", f32, (t, n), dev), wp, wn, st))
+
+
 def kda_abi_version() -> int:
     return int(load().kda_abi_version())
 
@@ -568,5 +774,7 @@ __all__ = [
     "kda_last_error", "kda_accept_greedy", "accept_workspace", "ACCEPT_WORK_BYTES", "NO_TOKEN",
     "kda_conv_reroll", "copy_table", "kda_copy_batch", "RING_ROWS", "kda_row_ops",
     "kda_verify_round_multi", "MAX_PREV_ROUNDS", "kda_scan_rows_columns", "kda_scan_rows_stash",
-    "kda_replay_stash", "kda_accept_greedy_noalloc",
+    "kda_replay_stash", "kda_accept_greedy_noalloc", "kda_prompt", "prompt_workspace",
+    "kda_linear_prompt", "linear_workspace", "kda_linear_step", "kda_logprobs",
+    "logprobs_workspace", "TOP_MAX",
 ]

@@ -21,7 +21,9 @@ ROOT = os.path.dirname(PKG)
 CSRC = os.path.join(PKG, "csrc")
 INCLUDE = os.path.join(ROOT, "include")
 LIB = os.path.join(PKG, "libkda.so")
-SOURCES = [os.path.join(CSRC, "kda_kernels.hip"), os.path.join(CSRC, "kda_abi.cpp")]
+SOURCES = [os.path.join(CSRC, n) for n in
+           ("kda_kernels.hip", "kda_prompt.hip", "kda_logprobs.hip", "kda_abi.cpp",
+            "kda_ops_abi.cpp")]
 
 HIPCC = os.environ.get("HIPCC", "/opt/rocm/bin/hipcc")
 

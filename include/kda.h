@@ -52,11 +52,14 @@ extern "C" {
 #define KDA_HEAD_DIM 128   /* d_k = d_v; glm5_spec_ppn_gate.rs fixture head_dim */
 #define KDA_T_MAX 15       /* verify rows per round: K + 1 <= 15 (glm_spec.rs, WALK-REUSE) */
 #define KDA_B_MAX 15       /* batched-decode sessions per step (same knee) */
-#define KDA_ABI_VERSION 10
+#define KDA_ABI_VERSION 11
 #define KDA_ACCEPT_WORK_BYTES 12288   /* workspace of kda_accept_greedy */
 #define KDA_NO_TOKEN 0xFFFFFFFFu      /* argmax slot of a logits row holding a NaN */
 #define KDA_CONV_RING_ROWS 3          /* short-conv history: kernel size 4 keeps 3 raw rows */
 #define KDA_MAX_PREV_ROUNDS 4         /* earlier rounds one kda_verify_round_multi can replay */
+#define KDA_PROMPT_ROWS_MAX 268435456 /* packed rows of one prompt call */
+#define KDA_PROMPT_SEQS_MAX 1048576   /* sequences of one prompt call */
+#define KDA_TOP_MAX 32                /* alternatives kda_logprobs lists for a row */
 
 enum { KDA_IN_F32 = 0, KDA_IN_BF16 = 1 };
 
@@ -399,6 +402,100 @@ int kda_conv_reroll_dev(const float* ring_snap, const void* raw, float* ring_out
  * overlaps a source or another destination.
  */
 int kda_copy_batch(const uint64_t* table, int n, long long words, void* stream);
+
+/*
+ * Prompt rows of B sequences through one KDA layer: the row program of
+ * kda_scan_rows over any number of rows, each sequence against its own state,
+ * updated in place.  It makes the state that the first verify round of a
+ * session starts from; there is no snapshot and no row limit.
+ *   The rows run in chunks (the recurrence is linear in the state, so a chunk
+ *   is a few matrix products), which sums in another order than the row scan:
+ *   results agree with kda_scan_rows to f32 rounding, not bit for bit.  They
+ *   are deterministic, and do not depend on the other sequences of the call.
+ *   s_ptrs      : DEVICE array of B pointers, s_ptrs[b] to sequence b's state
+ *                 [H][128][128] f32 (16-byte aligned; zero it for a fresh
+ *                 sequence).  A NULL entry leaves sequence b out: its rows of
+ *                 o are not written.  Entries must not overlap each other or
+ *                 any argument; the library cannot check them.
+ *   offsets     : DEVICE array of B + 1 int32, 4-byte aligned: sequence b has
+ *                 rows offsets[b] .. offsets[b+1]-1 (none if they are equal:
+ *                 its state stays as it is).  Entries are read as if clamped
+ *                 to 0..R and to be non-decreasing; rows that no sequence
+ *                 covers are not read, and their rows of o not written.
+ *   q, k, v, g  : [R][H][128] in in_dtype, the sequences packed one after the
+ *                 other.  beta: [R][H].
+ *   o           : [R][H][128] f32, or NULL for the state only.
+ *   work        : kda_prompt_work_bytes(R, B, H) bytes (work_bytes says how
+ *                 many there are), 16-byte aligned, in any state on entry;
+ *                 NULL when none are needed.  Calls that can run at the same
+ *                 time need different work buffers.
+ *   0 <= R <= KDA_PROMPT_ROWS_MAX, 1 <= B <= KDA_PROMPT_SEQS_MAX,
+ *   1 <= H <= 65535.  With R = 0 nothing is enqueued.
+ */
+int kda_prompt(float* const* s_ptrs, const int32_t* offsets, const void* q, const void* k,
+               const void* v, const void* g, const void* beta, float* o, int R, int B, int H,
+               int in_dtype, void* work, long long work_bytes, void* stream);
+/* Workspace bytes of kda_prompt (it never shrinks as R, B or H grow); -1 on a bad count. */
+long long kda_prompt_work_bytes(int R, int B, int H);
+
+/*
+ * Linear attention with one decay for each head, over the same states.  One
+ * row of value head h, which reads key head hk = h / (H / Hk):
+ *     S   = exp(min(g_t[h], 0)) S + k_t[hk] v_t[h]^T
+ *     o_t = S^T q_t[hk] / sqrt(128)          (from the updated state)
+ * kda_linear_prompt runs packed prompts in chunks, as kda_prompt;
+ * kda_linear_step one token of each of L x B sessions, as kda_scan_batched.
+ * kda_snapshot and kda_copy_batch serve these states too.
+ *   q, k        : [R][Hk][128] ([L][B][Hk][128] for the step) in in_dtype;
+ *                 Hk >= 1 divides H (Hk = H: a key head for each value head).
+ *   v           : [R][H][128] ([L][B][H][128]) in in_dtype.
+ *   g           : [R][H] ([L][B][H]), the log-decays, f32 whatever in_dtype is:
+ *                 a decay rounded to 8 bits would drift over a long prompt.
+ *                 -inf is allowed (the state restarts at that row); a decay
+ *                 below exp(-104) is 0 in f32.
+ *   o           : [R][H][128] ([L][B][H][128]) f32, or NULL.
+ *   s_ptrs, offsets, work : as kda_prompt; for the step s_ptrs[l*B + b] is
+ *                 session b's layer-l state, and a NULL entry leaves that
+ *                 session out (its row of o is not written).
+ *   The step takes any B >= 1 with L*B*H < 2^31.
+ */
+int kda_linear_prompt(float* const* s_ptrs, const int32_t* offsets, const void* q, const void* k,
+                      const void* v, const float* g, float* o, int R, int B, int Hk, int H,
+                      int in_dtype, void* work, long long work_bytes, void* stream);
+/* Workspace bytes of kda_linear_prompt; -1 on a bad count. */
+long long kda_linear_prompt_work_bytes(int R, int B, int H);
+int kda_linear_step(float* const* s_ptrs, const void* q, const void* k, const void* v,
+                    const float* g, float* o, int L, int B, int Hk, int H, int in_dtype,
+                    void* stream);
+
+/*
+ * Log probabilities of given tokens, entropy and top alternatives of t rows of
+ * logits, laid out as for kda_accept_greedy but any number of them: what a
+ * verify round answers with beside its tokens, or the scores of a prompt.
+ * With p = softmax(x) of a row x:
+ *   tokens  : t u32 token ids, or NULL together with lp.
+ *   lp      : t f32, log p[token].  A token >= V (KDA_NO_TOKEN) gives NaN.
+ *   entropy : t f32, -sum p log p (in nats), or NULL.
+ *   top_ids : [t][n_top] u32, the tokens of highest probability in falling
+ *             order, the lowest index first among equal logits (-0 equals +0).
+ *             Past the last token with a finite logit: KDA_NO_TOKEN.
+ *   top_lp  : [t][n_top] f32, their log probabilities (-inf past the last).
+ *             top_ids and top_lp are needed when n_top > 0 and not read else.
+ *   n_top   : 0..KDA_TOP_MAX.
+ * Logits of -inf are masked tokens (lp = -inf, no share of the entropy).  A row
+ * whose logits are all -inf: lp = -inf, entropy 0, no alternatives.  A row that
+ * holds a NaN or +inf has no distribution: lp, entropy and top_lp are NaN and
+ * top_ids KDA_NO_TOKEN.
+ *   work    : kda_logprobs_work_bytes(t, V, n_top) bytes, 16-byte aligned, in
+ *             any state on entry; NULL when none are needed.  Calls that can
+ *             run at the same time need different work buffers.
+ *   logits, ld, in_dtype as kda_accept_greedy; t, V >= 1, t * ld <= 2^40.
+ */
+int kda_logprobs(const void* logits, int t, int V, long long ld, int in_dtype,
+                 const uint32_t* tokens, int n_top, float* lp, float* entropy, uint32_t* top_ids,
+                 float* top_lp, void* work, long long work_bytes, void* stream);
+/* Workspace bytes of kda_logprobs; -1 on a bad count. */
+long long kda_logprobs_work_bytes(int t, int V, int n_top);
 
 /* Message for the last nonzero status returned on the calling thread. */
 const char* kda_last_error(void);
