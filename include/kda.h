@@ -419,9 +419,10 @@ int kda_copy_batch(const uint64_t* table, int n, long long words, void* stream);
  *                 any argument; the library cannot check them.
  *   offsets     : DEVICE array of B + 1 int32, 4-byte aligned: sequence b has
  *                 rows offsets[b] .. offsets[b+1]-1 (none if they are equal:
- *                 its state stays as it is).  Entries are read as if clamped
- *                 to 0..R and to be non-decreasing; rows that no sequence
- *                 covers are not read, and their rows of o not written.
+ *                 its state stays as it is).  Entries are clamped to 0..R and
+ *                 read with a running maximum (one that decreases counts as
+ *                 the largest before it); rows that no sequence covers are not
+ *                 read, and their rows of o not written.
  *   q, k, v, g  : [R][H][128] in in_dtype, the sequences packed one after the
  *                 other.  beta: [R][H].
  *   o           : [R][H][128] f32, or NULL for the state only.
