@@ -6,10 +6,6 @@
 //   KDA     S' = diag(exp(clamp(g, -5, 0))) S,  e = beta (v - S'^T k)
 //   linear  S' = exp(min(g, 0)) S,              e = v
 //   both    S  = S' + k e^T,  o = S^T q / sqrt(128)
-//
-// Row kernel: a workgroup owns 32 value columns of one (sequence, head) and
-// walks its rows; 8 neighbouring lanes share a column, 16 keys each, and
-// reduce with three lane exchanges.  Rows are staged 16 at a time in LDS.
 
 #include <hip/hip_runtime.h>
 
@@ -84,107 +80,6 @@ __device__ __forceinline__ void sequence(const PromptArgs& a, int b, int& first,
     for (int m = 32; m >= 1; m >>= 1) x = max(x, __shfl_xor(x, m));
     first = __builtin_amdgcn_readfirstlane(x);
     last = min(max(a.offsets[b + 1], first), a.R);
-}
-
-constexpr int kTileRows = 16;
-constexpr int kRowCols = 32;   // value columns of a workgroup
-
-template <bool LINEAR, bool BF16>
-__global__ void __launch_bounds__(256) row_kernel(PromptArgs a) {
-    __shared__ float qs[kTileRows][kD], ks[kTileRows][kD], ds[LINEAR ? 1 : kTileRows][kD];
-    __shared__ float vs[kTileRows][kRowCols], bs[kTileRows];
-    const int tid = threadIdx.x;
-    const int slices = kD / kRowCols;
-    const int slice = blockIdx.x % slices;
-    const int h = blockIdx.x / slices % a.H;
-    const int b = blockIdx.x / slices / a.H;
-    const int hk = h / (a.H / a.Hk);
-    int first, last;
-    sequence(a, b, first, last);
-    float* s = a.s_ptrs[b];
-    if (s == nullptr || first >= last) return;
-    s += static_cast<long long>(h) * kD * kD;
-
-    const int ki = tid & 7;              // keys 4*ki + 32*m + 0..3
-    const int cl = tid >> 3;             // column within the slice
-    const int col = slice * kRowCols + cl;
-    float S[16];
-#pragma unroll
-    for (int m = 0; m < 16; ++m) S[m] = s[(4 * ki + 32 * (m >> 2) + (m & 3)) * kD + col];
-
-    for (int t0 = first; t0 < last; t0 += kTileRows) {
-        const int n = min(kTileRows, last - t0);
-        __syncthreads();
-        for (int x = tid; x < n * kD; x += 256) {
-            const int t = x / kD, c = x % kD;
-            const long long kr = (static_cast<long long>(t0 + t) * a.Hk + hk) * kD + c;
-            qs[t][c] = load<BF16>(a.q, kr);
-            ks[t][c] = load<BF16>(a.k, kr);
-            if constexpr (!LINEAR) {
-                const long long r = (static_cast<long long>(t0 + t) * a.H + h) * kD + c;
-                ds[t][c] = expf(fminf(fmaxf(load<BF16>(a.g, r), kGateLow), 0.f));
-            }
-        }
-        for (int x = tid; x < n * kRowCols; x += 256) {
-            const int t = x / kRowCols, c = x % kRowCols;
-            vs[t][c] = load<BF16>(a.v, (static_cast<long long>(t0 + t) * a.H + h) * kD +
-                                           slice * kRowCols + c);
-        }
-        if (tid < n) {
-            const long long r = static_cast<long long>(t0 + tid) * a.H + h;
-            if constexpr (LINEAR)
-                bs[tid] = expf(fminf(static_cast<const float*>(a.g)[r], 0.f));
-            else
-                bs[tid] = load<BF16>(a.beta, r);
-        }
-        __syncthreads();
-        for (int t = 0; t < n; ++t) {
-            float e = vs[t][cl];
-            if constexpr (LINEAR) {
-                const float d = bs[t];
-#pragma unroll
-                for (int m = 0; m < 16; ++m) S[m] *= d;
-            } else {
-                float u = 0.f;
-#pragma unroll
-                for (int m = 0; m < 16; ++m) {
-                    const int i = 4 * ki + 32 * (m >> 2) + (m & 3);
-                    S[m] *= ds[t][i];
-                    u = fmaf(ks[t][i], S[m], u);
-                }
-                u += __shfl_xor(u, 1);
-                u += __shfl_xor(u, 2);
-                u += __shfl_xor(u, 4);
-                e = bs[t] * (e - u);
-            }
-            float w = 0.f;
-#pragma unroll
-            for (int m = 0; m < 16; ++m) {
-                const int i = 4 * ki + 32 * (m >> 2) + (m & 3);
-                S[m] = fmaf(ks[t][i], e, S[m]);
-                w = fmaf(qs[t][i], S[m], w);
-            }
-            w += __shfl_xor(w, 1);
-            w += __shfl_xor(w, 2);
-            w += __shfl_xor(w, 4);
-            if (a.o != nullptr && ki == 0)
-                a.o[(static_cast<long long>(t0 + t) * a.H + h) * kD + col] = w * kScale;
-        }
-    }
-#pragma unroll
-    for (int m = 0; m < 16; ++m) s[(4 * ki + 32 * (m >> 2) + (m & 3)) * kD + col] = S[m];
-}
-
-template <bool LINEAR>
-hipError_t launch_rows(const PromptArgs& a, bool bf16, hipStream_t stream) {
-    const long long blocks = static_cast<long long>(a.B) * a.H * (kD / kRowCols);
-    if (blocks > 0x7FFFFFFFll) return hipErrorInvalidValue;
-    const dim3 grid(static_cast<unsigned>(blocks));
-    if (bf16)
-        row_kernel<LINEAR, true><<<grid, dim3(256), 0, stream>>>(a);
-    else
-        row_kernel<LINEAR, false><<<grid, dim3(256), 0, stream>>>(a);
-    return hipGetLastError();
 }
 
 // ------------------------------------------------------------------ linear attention, chunks
@@ -310,7 +205,7 @@ struct LinearTile {
 
 // By channel: word x of four rows of one plane.
 template <int NS>
-__device__ __forceinline__ void store_columns(uint16_t (&t)[NS][kD][kColPitch], int cg, int rg,
+__device__ __forceinline__ void store_columns(uint16_t (&t)[NS][kD][kColPitch], int cg, int at,
                                               const uint2 (&w)[4][NS]) {
 #pragma unroll
     for (int s = 0; s < NS; ++s) {
@@ -320,7 +215,7 @@ __device__ __forceinline__ void store_columns(uint16_t (&t)[NS][kD][kColPitch], 
             uint2 y;
             y.x = __builtin_amdgcn_perm(x < 2 ? w[1][s].x : w[1][s].y, x < 2 ? w[0][s].x : w[0][s].y, sel);
             y.y = __builtin_amdgcn_perm(x < 2 ? w[3][s].x : w[3][s].y, x < 2 ? w[2][s].x : w[2][s].y, sel);
-            *reinterpret_cast<uint2*>(&t[s][4 * cg + x][4 * rg]) = y;
+            *reinterpret_cast<uint2*>(&t[s][4 * cg + x][at]) = y;
         }
     }
 }
@@ -431,9 +326,9 @@ __global__ void __launch_bounds__(256, BF16 ? 2 : 1) linear_chunk_kernel(PromptA
             }
             patch_words<BF16>(pk, w);
             if (out) store_rows<NS>(T.k, cg, rg, w);
-            store_columns<NS>(T.kt, cg, rg, w);
+            store_columns<NS>(T.kt, cg, 4 * rg, w);
             patch_words<BF16>(pv, w);
-            store_columns<NS>(T.vt, cg, rg, w);
+            store_columns<NS>(T.vt, cg, 4 * rg, w);
         }
         if (tid < 64) {
             double x = lane < kChunk ? fminf(fmaxf(pg, kGateOff), 0.f) : 0.f;
@@ -598,6 +493,556 @@ __global__ void __launch_bounds__(256) linear_chain_kernel(PromptArgs a, Parts p
     }
 }
 
+// ------------------------------------------------------------------ KDA, chunks
+//
+// Within a chunk of 32 rows, G_t[c] = sum of the clamped gates of channel c up
+// to and with row t, and
+//   A_tj = sum_c k_t[c] k_j[c] e^{G_t[c]-G_j[c]}   (j < t)
+//   B_tj = sum_c q_t[c] k_j[c] e^{G_t[c]-G_j[c]}   (j <= t)
+// the rows' deltas e solve a triangular system, and the chunk is
+//   E   = (I + diag(beta) A)^-1 diag(beta) (V - (k e^G) S_0)  =  M (V - (k e^G) S_0)
+//   O   = [ (q e^G) S_0 + B E ] / sqrt(128)
+//   S_C = diag(e^{G_C}) S_0 + (k e^{G_C-G})^T E
+// M and B need no state: a first launch computes them for all chunks side by
+// side.  A second launch walks the chunks of each sequence.
+
+using f16x8 = __attribute__((ext_vector_type(8))) _Float16;
+using f16x2 = __attribute__((ext_vector_type(2))) _Float16;
+using f32x2 = __attribute__((ext_vector_type(2))) float;
+
+constexpr int kSub = 16;                        // rows of a block of A and B
+constexpr long long kPairBytes = 2ll * 2 * kChunk * kChunk * 2;   // M and B, two f16 words each
+
+// The scales of a chunk's f16 words, powers of two.
+struct ChunkScale {
+    float k, q, m, b;
+};
+
+// A power of two that brings m into [2^13, 2^14): the largest f16 word then
+// keeps 22 bits in two words, and what falls below f16's range is under 2^-38
+// of the largest.  (Held to 2^100: smaller values than 2^-87 keep fewer bits.)
+__device__ __forceinline__ float scale_of(float m) {
+    const int e = static_cast<int>(bits(m) >> 23 & 0xFF);
+    const int x = min(13 + 127 + 127 - e, 127 + 100);
+    return real(static_cast<uint32_t>(max(x, 1)) << 23);
+}
+
+// 1 / s of a power of two from scale_of.
+__device__ __forceinline__ float inverse_of(float s) { return real(0x7F000000u - bits(s)); }
+
+// Two f32 values as two words of two f16 each (22 bits).
+__device__ __forceinline__ void halves2(float x0, float x1, uint32_t& a, uint32_t& b) {
+    const f16x2 h = __builtin_convertvector((f32x2{x0, x1}), f16x2);
+    const f16x2 l = __builtin_convertvector((f32x2{x0 - static_cast<float>(h[0]), x1 - static_cast<float>(h[1])}), f16x2);
+    a = __builtin_bit_cast(uint32_t, h);
+    b = __builtin_bit_cast(uint32_t, l);
+}
+
+__device__ __forceinline__ void halves4(const float (&x)[4], uint2 (&w)[2]) {
+    halves2(x[0], x[1], w[0].x, w[1].x);
+    halves2(x[2], x[3], w[0].y, w[1].y);
+}
+
+__device__ __forceinline__ void halves8(const f32x4& lo, const f32x4& hi, float s, uint4 (&w)[2]) {
+    halves2(lo[0] * s, lo[1] * s, w[0].x, w[1].x);
+    halves2(lo[2] * s, lo[3] * s, w[0].y, w[1].y);
+    halves2(hi[0] * s, hi[1] * s, w[0].z, w[1].z);
+    halves2(hi[2] * s, hi[3] * s, w[0].w, w[1].w);
+}
+
+// a . b over two f16 words each: all products but low x low (under 2^-22).
+__device__ __forceinline__ f32x4 product16(const uint4 (&a)[2], const uint4 (&b)[2], f32x4 c) {
+    const auto m = [](uint4 x, uint4 y, f32x4 z) {
+        return __builtin_amdgcn_mfma_f32_16x16x32_f16(__builtin_bit_cast(f16x8, x),
+                                                      __builtin_bit_cast(f16x8, y), z, 0, 0, 0);
+    };
+    c = m(a[1], b[0], c);
+    c = m(a[0], b[1], c);
+    return m(a[0], b[0], c);
+}
+
+template <bool BF16>
+__device__ __forceinline__ void patch_values(const Patch<BF16>& p, float (&x)[4][4]) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        if constexpr (BF16) {
+            const uint4 r = p.r[i >> 1];
+            const uint32_t u = i & 1 ? r.z : r.x, v = i & 1 ? r.w : r.y;
+            x[i][0] = real(u << 16);
+            x[i][1] = real(u & 0xFFFF0000u);
+            x[i][2] = real(v << 16);
+            x[i][3] = real(v & 0xFFFF0000u);
+        } else {
+            x[i][0] = real(p.r[i].x);
+            x[i][1] = real(p.r[i].y);
+            x[i][2] = real(p.r[i].z);
+            x[i][3] = real(p.r[i].w);
+        }
+    }
+}
+
+__device__ __forceinline__ float decay(float g) { return expf(fminf(fmaxf(g, kGateLow), 0.f)); }
+
+// Eight consecutive elements of a row.
+template <bool BF16>
+__device__ __forceinline__ void load8(const void* src, long long at, float (&x)[8]) {
+    if constexpr (BF16) {
+        const uint4 u = *reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(src) + at);
+        const uint32_t w[4] = {u.x, u.y, u.z, u.w};
+#pragma unroll
+        for (int i = 0; i < 8; ++i) x[i] = real(i & 1 ? w[i >> 1] & 0xFFFF0000u : w[i >> 1] << 16);
+    } else {
+        const float4 u = reinterpret_cast<const float4*>(static_cast<const float*>(src) + at)[0];
+        const float4 v = reinterpret_cast<const float4*>(static_cast<const float*>(src) + at)[1];
+        x[0] = u.x; x[1] = u.y; x[2] = u.z; x[3] = u.w;
+        x[4] = v.x; x[5] = v.y; x[6] = v.z; x[7] = v.w;
+    }
+}
+
+__device__ __forceinline__ float wave_max(float x) {
+#pragma unroll
+    for (int m = 32; m >= 1; m >>= 1) x = fmaxf(x, __shfl_xor(x, m));
+    return x;
+}
+
+// M and B of one chunk of one head.
+//
+// e^{G_t-G_j} does not split into a factor of t and one of j over the chunk's
+// whole range (e^{-5 * 32} leaves f32), so A and B are three blocks of 16 x 16:
+// with f = e^{G - G_mid}, G_mid at the middle of a 16-row block, every factor
+// stays within e^{-40}..e^{40}; the block below the diagonal takes the decay
+// between the two middles with its rows.  The factors are running products of
+// the rows' decays, which do not lose the weak gates behind strong ones as
+// differences of sums would.
+template <bool BF16>
+__global__ void __launch_bounds__(256) kda_pair_kernel(PromptArgs a, char* pairs, ChunkScale* scales) {
+    __shared__ __align__(16) float F[kChunk][kD + 4];
+    __shared__ float between[kD];
+    __shared__ float A[kChunk][kChunk + 1], B[kChunk][kChunk + 1], T[kChunk][kChunk + 1];
+    __shared__ float beta[kChunk], top[4][4];
+    const int tid = threadIdx.x, wave = tid >> 6, lane = tid & 63, g4 = lane >> 4, l16 = lane & 15;
+    const int h = blockIdx.x % a.H, slot = blockIdx.x / a.H;
+    const Part f = find_part(a, kChunk, slot);
+    if (f.b < 0 || a.s_ptrs[f.b] == nullptr) return;
+    const int t0 = f.first + f.index * kChunk;
+    const int n = min(f.last - t0, kChunk);
+    const long long pitch = static_cast<long long>(a.H) * kD, base = t0 * pitch + h * kD;
+
+    {   // factors: a thread has 4 rows x 4 channels, 8 neighbouring lanes a channel's 32 rows
+        const int rg = tid & 7, cg = tid >> 3;
+        Patch<BF16> pg;
+        load_patch<BF16>(pg, a.g, 4 * rg, n - 4 * rg, pitch, base + 4 * cg);
+        float d[4][4];
+        patch_values<BF16>(pg, d);
+        const bool late = rg & 2;   // behind the middle of its block
+#pragma unroll
+        for (int x = 0; x < 4; ++x) {
+            // a late row's f is the product from the middle to it; an early row's
+            // 1/f the product of what lies between it and the middle
+#pragma unroll
+            for (int i = 0; i < 4; ++i) d[i][x] = decay(d[i][x]);
+            const float all = d[0][x] * d[1][x] * (d[2][x] * d[3][x]);
+            const float near = __shfl_xor(all, 1);
+            float u[4];
+            if (late) {
+                u[0] = d[0][x];
+                u[1] = u[0] * d[1][x];
+                u[2] = u[1] * d[2][x];
+                u[3] = u[2] * d[3][x];
+            } else {
+                u[3] = 1.f;
+                u[2] = d[3][x];
+                u[1] = u[2] * d[2][x];
+                u[0] = u[1] * d[1][x];
+            }
+            const bool far = late == static_cast<bool>(rg & 1);
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                const float y = far ? u[i] * near : u[i];
+                F[4 * rg + i][4 * cg + x] = late ? y : 1.f / y;
+            }
+            const float pair = all * near;                  // lanes 2, 3: rows 8..15; 4, 5: 16..23
+            const float c = __shfl(pair, (lane & ~7) | 2) * __shfl(pair, (lane & ~7) | 4);
+            if (rg == 0) between[4 * cg + x] = c;
+        }
+    }
+    if (tid < kChunk)
+        beta[tid] = tid < n ? load<BF16>(a.beta, static_cast<long long>(t0 + tid) * a.H + h) : 0.f;
+    __syncthreads();
+
+    // waves 0, 1: the diagonal blocks; 2 and 3: A and B below it
+    const int tb = wave != 0, jb = wave == 1;
+    const bool low = wave >= 2, wantA = wave != 3, wantB = wave != 2;
+    f32x4 xa{0.f, 0.f, 0.f, 0.f}, xb{0.f, 0.f, 0.f, 0.f};
+    float kmax = 0.f, qmax = 0.f;
+#pragma unroll
+    for (int ks = 0; ks < 4; ++ks) {
+        const int c = 32 * ks + 8 * g4;
+        float x[8], y[8];
+        uint4 kj[3], kt[3], qt[3];
+        const int t = 16 * tb + l16, j = 16 * jb + l16;
+#pragma unroll
+        for (int i = 0; i < 8; ++i) x[i] = y[i] = 0.f;
+        if (j < n) load8<BF16>(a.k, base + j * pitch + c, x);
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+            if (!low) kmax = fmaxf(kmax, fabsf(x[i]));
+            y[i] = x[i] / F[j][c + i];
+        }
+        split8(y, kj);
+        float ft[8];
+#pragma unroll
+        for (int i = 0; i < 8; ++i) ft[i] = F[t][c + i] * (low ? between[c + i] : 1.f);
+        if (wantA) {
+            if (low) {
+#pragma unroll
+                for (int i = 0; i < 8; ++i) x[i] = 0.f;
+                if (t < n) load8<BF16>(a.k, base + t * pitch + c, x);
+            }
+#pragma unroll
+            for (int i = 0; i < 8; ++i) y[i] = x[i] * ft[i];
+            split8(y, kt);
+            xa = product<3, 3>(kt, kj, xa);
+        }
+        if (wantB) {
+#pragma unroll
+            for (int i = 0; i < 8; ++i) x[i] = 0.f;
+            if (t < n) load8<BF16>(a.q, base + t * pitch + c, x);
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+                if (!low) qmax = fmaxf(qmax, fabsf(x[i]));
+                y[i] = x[i] * ft[i];
+            }
+            split8(y, qt);
+            xb = product<3, 3>(qt, kj, xb);
+        }
+    }
+#pragma unroll
+    for (int r = 0; r < 4; ++r) {
+        const int t = 16 * tb + 4 * g4 + r, j = 16 * jb + l16;
+        if (wantA) A[t][j] = j < t ? -beta[t] * xa[r] : 0.f;
+        if (wantB) B[t][j] = j <= t ? xb[r] : 0.f;
+        if (low) (wantA ? A : B)[l16][16 + 4 * g4 + r] = 0.f;
+    }
+    __syncthreads();
+
+    // T = (I - A)^-1: the diagonal blocks column by column, then the one below
+    if (tid < kChunk) {
+        const int o = tid & 16, c = tid & 15;
+        float x[kSub];
+#pragma unroll
+        for (int t = 0; t < kSub; ++t) {
+            float s = t == c ? 1.f : 0.f;
+#pragma unroll
+            for (int j = 0; j < t; ++j) s = fmaf(A[o + t][o + j], x[j], s);
+            x[t] = s;
+            T[o + t][o + c] = s;
+        }
+    }
+    __syncthreads();
+    {
+        const int t = tid >> 4, j = tid & 15;
+        float s = 0.f;
+#pragma unroll
+        for (int i = 0; i < kSub; ++i) s = fmaf(A[16 + t][i], T[i][j], s);
+        A[t][16 + j] = s;    // the upper block is free
+        __syncthreads();
+        s = 0.f;
+#pragma unroll
+        for (int i = 0; i < kSub; ++i) s = fmaf(T[16 + t][16 + i], A[i][16 + j], s);
+        T[16 + t][j] = s;
+        T[t][16 + j] = 0.f;
+    }
+    __syncthreads();
+
+    const int t = tid >> 3, x = tid & 7;
+    float m[4], b[4], mmax = 0.f, bmax = 0.f;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        m[i] = T[t][4 * x + i] * beta[4 * x + i];
+        b[i] = B[t][4 * x + i];
+        mmax = fmaxf(mmax, fabsf(m[i]));
+        bmax = fmaxf(bmax, fabsf(b[i]));
+    }
+    kmax = wave_max(kmax);
+    qmax = wave_max(qmax);
+    mmax = wave_max(mmax);
+    bmax = wave_max(bmax);
+    if (lane == 0) {
+        top[0][wave] = kmax;
+        top[1][wave] = qmax;
+        top[2][wave] = mmax;
+        top[3][wave] = bmax;
+    }
+    __syncthreads();
+    float s[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+        s[i] = scale_of(fmaxf(fmaxf(top[i][0], top[i][1]), fmaxf(top[i][2], top[i][3])));
+    const long long at = static_cast<long long>(slot) * a.H + h;
+    if (tid == 0) scales[at] = ChunkScale{s[0], s[1], s[2], s[3]};
+    // by row, the columns of the 32 in operand order
+    uint2* to = reinterpret_cast<uint2*>(pairs + at * kPairBytes) + t * 8 + 2 * (x & 3) + (x >> 2);
+    uint2 w[2];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        m[i] *= s[2];
+        b[i] *= s[3];
+    }
+    halves4(m, w);
+    to[0] = w[0];
+    to[kChunk * 8] = w[1];
+    halves4(b, w);
+    to[2 * kChunk * 8] = w[0];
+    to[3 * kChunk * 8] = w[1];
+}
+
+struct KdaTile {
+    uint16_t q[2][kChunk][kRowPitch];    // q e^G by row
+    uint16_t k[2][kChunk][kRowPitch];    // k e^G by row
+    uint16_t kt[2][kD][kColPitch];       // k e^{G_C-G} by channel, the rows in operand order
+    float keep[kD];                      // e^{G_C}
+};
+
+constexpr int kKdaCols = 32;   // value columns of a workgroup
+
+// max over the four lanes that share a column
+__device__ __forceinline__ float column_max(float x) {
+    x = fmaxf(x, __shfl_xor(x, 16));
+    return fmaxf(x, __shfl_xor(x, 32));
+}
+
+// The chunks of one sequence and head, 32 value columns.  Waves 4..7 prepare
+// the next chunk's operands in LDS while waves 0..3 take the current one
+// through: wave 2 * half + c has value columns 16 c.. and key channels
+// 64 half.. of the state in 16 registers, and the two halves of a column block
+// exchange their parts of the sums over channels through LDS.
+//
+// Operands are two f16 words of a value scaled by a power of two (3 products,
+// 22 bits): state, right-hand side and deltas by their column's largest,
+// k, q, M and B by the chunk's.
+template <bool BF16, bool OUT>
+__global__ void __launch_bounds__(512) kda_chunk_kernel(PromptArgs a, const char* pairs,
+                                                        const ChunkScale* scales) {
+    __shared__ __align__(16) KdaTile tiles[2];
+    __shared__ f32x4 xr[4][2][64], xo[4][64];
+    const int tid = threadIdx.x, wave = tid >> 6, lane = tid & 63, g4 = lane >> 4, l16 = lane & 15;
+    constexpr int slices = kD / kKdaCols;
+    const int h = blockIdx.x / slices % a.H, b = blockIdx.x / slices / a.H, slice = blockIdx.x % slices;
+    int first, last;
+    sequence(a, b, first, last);
+    float* state = a.s_ptrs[b];
+    if (state == nullptr || first >= last) return;
+    state += static_cast<long long>(h) * kD * kD;
+    const int chunks = (last - first + kChunk - 1) / kChunk;
+    const long long pitch = static_cast<long long>(a.H) * kD;
+    const long long slot0 = (static_cast<long long>(first / kChunk) + b) * a.H + h;
+
+    if (wave >= 4) {
+        const int x = tid - 256, rg = x & 7, cg = x >> 3;
+        Patch<BF16> pq, pk, pg;
+        ChunkScale sc{};
+        const auto fetch = [&](int i) {
+            const int r0 = first + i * kChunk + 4 * rg, n = last - r0;
+            const long long col = static_cast<long long>(h) * kD + 4 * cg;
+            if (OUT) load_patch<BF16>(pq, a.q, r0, n, pitch, col);
+            load_patch<BF16>(pk, a.k, r0, n, pitch, col);
+            load_patch<BF16>(pg, a.g, r0, n, pitch, col);
+            sc = scales[slot0 + static_cast<long long>(i) * a.H];
+        };
+        const auto stage = [&](KdaTile& T) {
+            float d[4][4], k[4][4], pre[4][4], suf[4][4];
+            patch_values<BF16>(pg, d);
+            patch_values<BF16>(pk, k);
+#pragma unroll
+            for (int c = 0; c < 4; ++c) {
+#pragma unroll
+                for (int i = 0; i < 4; ++i) d[i][c] = decay(d[i][c]);
+                pre[0][c] = d[0][c];
+#pragma unroll
+                for (int i = 1; i < 4; ++i) pre[i][c] = pre[i - 1][c] * d[i][c];
+                suf[3][c] = 1.f;
+#pragma unroll
+                for (int i = 2; i >= 0; --i) suf[i][c] = suf[i + 1][c] * d[i + 1][c];
+                // products over the row groups before and behind this one
+                float up = pre[3][c], down = pre[3][c];
+#pragma unroll
+                for (int s = 1; s < 8; s <<= 1) {
+                    const float y = __shfl_up(up, s), z = __shfl_down(down, s);
+                    if (rg >= s) up *= y;
+                    if (rg + s < 8) down *= z;
+                }
+                float before = __shfl_up(up, 1), behind = __shfl_down(down, 1);
+                if (rg == 0) before = 1.f;
+                if (rg == 7) {
+                    behind = 1.f;
+                    T.keep[4 * cg + c] = up;
+                }
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    pre[i][c] *= before;
+                    suf[i][c] *= behind;
+                }
+            }
+            uint2 w[4][2];
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                float y[4];
+#pragma unroll
+                for (int c = 0; c < 4; ++c) y[c] = k[i][c] * pre[i][c] * sc.k;
+                halves4(y, w[i]);
+            }
+            store_rows<2>(T.k, cg, rg, w);
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                float y[4];
+#pragma unroll
+                for (int c = 0; c < 4; ++c) y[c] = k[i][c] * suf[i][c] * sc.k;
+                halves4(y, w[i]);
+            }
+            store_columns<2>(T.kt, cg, 8 * (rg & 3) + 4 * (rg >> 2), w);
+            if (OUT) {
+                patch_values<BF16>(pq, k);
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    float y[4];
+#pragma unroll
+                    for (int c = 0; c < 4; ++c) y[c] = k[i][c] * pre[i][c] * sc.q;
+                    halves4(y, w[i]);
+                }
+                store_rows<2>(T.q, cg, rg, w);
+            }
+        };
+        fetch(0);
+        stage(tiles[0]);
+        if (chunks > 1) fetch(1);
+        for (int i = 0; i < chunks; ++i) {
+            __syncthreads();
+            if (i + 1 < chunks) {
+                stage(tiles[(i + 1) & 1]);
+                if (i + 2 < chunks) fetch(i + 2);
+            }
+            __syncthreads();
+        }
+        return;
+    }
+
+    const int half = wave >> 1, col = kKdaCols * slice + 16 * (wave & 1) + l16;
+    f32x4 S[4];
+    float smax = 0.f;
+#pragma unroll
+    for (int m = 0; m < 4; ++m)
+#pragma unroll
+        for (int r = 0; r < 4; ++r) {
+            S[m][r] = state[(64 * half + 16 * m + 4 * g4 + r) * kD + col];
+            smax = fmaxf(smax, fabsf(S[m][r]));
+        }
+    uint4 mf[2][2], bf[2];
+    float v[2][4];
+    ChunkScale sc{};
+    const auto fetch = [&](int i) {
+        const long long at = slot0 + static_cast<long long>(i) * a.H;
+        const uint4* p = reinterpret_cast<const uint4*>(pairs + at * kPairBytes);
+#pragma unroll
+        for (int s = 0; s < 2; ++s) {
+#pragma unroll
+            for (int tb = 0; tb < 2; ++tb) mf[tb][s] = p[(s * kChunk + 16 * tb + l16) * 4 + g4];
+            if (OUT) bf[s] = p[((2 + s) * kChunk + 16 * half + l16) * 4 + g4];
+        }
+        sc = scales[at];
+        if (half == 0)
+#pragma unroll
+            for (int tb = 0; tb < 2; ++tb)
+#pragma unroll
+                for (int r = 0; r < 4; ++r) {
+                    const int t = first + i * kChunk + 16 * tb + 4 * g4 + r;
+                    v[tb][r] = t < last ? load<BF16>(a.v, t * pitch + h * kD + col) : 0.f;
+                }
+    };
+    fetch(0);
+
+    for (int i = 0; i < chunks; ++i) {
+        const KdaTile& T = tiles[i & 1];
+        const float ss = scale_of(column_max(smax));
+        const float sk = inverse_of(sc.k), sq = inverse_of(sc.q), si = inverse_of(ss);
+        uint4 sf[2][2];
+#pragma unroll
+        for (int ks = 0; ks < 2; ++ks) halves8(S[2 * ks], S[2 * ks + 1], ss, sf[ks]);
+        __syncthreads();
+        f32x4 R[2], Q[2];
+#pragma unroll
+        for (int tb = 0; tb < 2; ++tb) R[tb] = Q[tb] = f32x4{0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+        for (int ks = 0; ks < 2; ++ks)
+#pragma unroll
+            for (int tb = 0; tb < 2; ++tb) {
+                uint4 f[2];
+                read_rows<2>(T.k, 16 * tb + l16, 64 * half + 32 * ks + 8 * g4, f);
+                R[tb] = product16(f, sf[ks], R[tb]);
+                if (OUT) {
+                    read_rows<2>(T.q, 16 * tb + l16, 64 * half + 32 * ks + 8 * g4, f);
+                    Q[tb] = product16(f, sf[ks], Q[tb]);
+                }
+            }
+#pragma unroll
+        for (int tb = 0; tb < 2; ++tb) {
+            R[tb] = R[tb] * sk * si;
+            if (half == 0)
+#pragma unroll
+                for (int r = 0; r < 4; ++r) R[tb][r] -= v[tb][r];
+            xr[wave][tb][lane] = R[tb];
+            Q[tb] = Q[tb] * sq * si;
+        }
+        if (OUT) xo[wave][lane] = half == 0 ? Q[1] : Q[0];
+        __syncthreads();
+        float rmax = 0.f;
+#pragma unroll
+        for (int tb = 0; tb < 2; ++tb) {
+            R[tb] = -(R[tb] + xr[wave ^ 2][tb][lane]);
+#pragma unroll
+            for (int r = 0; r < 4; ++r) rmax = fmaxf(rmax, fabsf(R[tb][r]));
+        }
+        const float sr = scale_of(column_max(rmax)), sm = inverse_of(sc.m);
+        uint4 rf[2], ef[2];
+        halves8(R[0], R[1], sr, rf);
+        f32x4 E[2];
+        float emax = 0.f;
+#pragma unroll
+        for (int tb = 0; tb < 2; ++tb) {
+            E[tb] = product16(mf[tb], rf, f32x4{0.f, 0.f, 0.f, 0.f}) * sm * inverse_of(sr);
+#pragma unroll
+            for (int r = 0; r < 4; ++r) emax = fmaxf(emax, fabsf(E[tb][r]));
+        }
+        const float se = scale_of(column_max(emax)), ei = inverse_of(se);
+        halves8(E[0], E[1], se, ef);
+        if (OUT) {
+            f32x4 O = half == 0 ? Q[0] : Q[1];
+            O = O + xo[wave ^ 2][lane] + product16(bf, ef, f32x4{0.f, 0.f, 0.f, 0.f}) * inverse_of(sc.b) * ei;
+#pragma unroll
+            for (int r = 0; r < 4; ++r) {
+                const int t = first + i * kChunk + 16 * half + 4 * g4 + r;
+                if (t < last) a.o[t * pitch + h * kD + col] = O[r] * kScale;
+            }
+        }
+        if (i + 1 < chunks) fetch(i + 1);
+        smax = 0.f;
+#pragma unroll
+        for (int m = 0; m < 4; ++m) {
+            const int c = 64 * half + 16 * m;
+            uint4 kf[2];
+            read_columns<2, kD>(T.kt, c + l16, 8 * g4, kf);
+            const f32x4 keep = *reinterpret_cast<const f32x4*>(&T.keep[c + 4 * g4]);
+            S[m] = S[m] * keep + product16(kf, ef, f32x4{0.f, 0.f, 0.f, 0.f}) * sk * ei;
+#pragma unroll
+            for (int r = 0; r < 4; ++r) smax = fmaxf(smax, fabsf(S[m][r]));
+        }
+    }
+#pragma unroll
+    for (int m = 0; m < 4; ++m)
+#pragma unroll
+        for (int r = 0; r < 4; ++r) state[(64 * half + 16 * m + 4 * g4 + r) * kD + col] = S[m][r];
+}
+
 // ------------------------------------------------------------------ single token
 //
 // A workgroup owns one (layer, session, head): the head's 64 KiB state is read
@@ -671,7 +1116,6 @@ __global__ void __launch_bounds__(256) linear_step_kernel(StepArgs a) {
 
 }  // namespace
 
-long long prompt_work_bytes(int, int, int) { return 0; }
 
 // Rows of a part: 512, and more where the call has work for the chip without
 // parts that short (each part but a sequence's last reads k and v twice).
@@ -688,8 +1132,28 @@ long long linear_work_bytes(int R, int B, int H) {
     return part_slots(R, B, 512) * H * (kD * kD * 4ll + 8);
 }
 
+long long prompt_work_bytes(int R, int B, int H) {
+    return part_slots(R, B, kChunk) * H * (kPairBytes + static_cast<long long>(sizeof(ChunkScale)));
+}
+
+template <bool BF16>
+static hipError_t launch_kda(const PromptArgs& a, hipStream_t stream) {
+    const long long pairs = part_slots(a.R, a.B, kChunk) * a.H;
+    const long long blocks = static_cast<long long>(a.B) * a.H * (kD / kKdaCols);
+    if (pairs > 0x7FFFFFFFll || blocks > 0x7FFFFFFFll) return hipErrorInvalidValue;
+    char* const words = static_cast<char*>(a.work);
+    ChunkScale* const scales = reinterpret_cast<ChunkScale*>(words + pairs * kPairBytes);
+    kda_pair_kernel<BF16><<<dim3(static_cast<unsigned>(pairs)), dim3(256), 0, stream>>>(a, words, scales);
+    const dim3 grid(static_cast<unsigned>(blocks));
+    if (a.o)
+        kda_chunk_kernel<BF16, true><<<grid, dim3(512), 0, stream>>>(a, words, scales);
+    else
+        kda_chunk_kernel<BF16, false><<<grid, dim3(512), 0, stream>>>(a, words, scales);
+    return hipGetLastError();
+}
+
 hipError_t launch_prompt(const PromptArgs& a, bool bf16, hipStream_t stream) {
-    return launch_rows<false>(a, bf16, stream);
+    return bf16 ? launch_kda<true>(a, stream) : launch_kda<false>(a, stream);
 }
 
 template <bool BF16>
