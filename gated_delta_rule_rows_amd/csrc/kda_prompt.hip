@@ -106,6 +106,7 @@ __device__ __forceinline__ void sequence(const PromptArgs& a, int b, int& first,
 
 using bf16x8 = __attribute__((ext_vector_type(8))) __bf16;
 using f32x4 = __attribute__((ext_vector_type(4))) float;
+using u32x4 = __attribute__((ext_vector_type(4))) uint32_t;
 
 __device__ __forceinline__ uint32_t bits(float x) { return __builtin_bit_cast(uint32_t, x); }
 __device__ __forceinline__ float real(uint32_t x) { return __builtin_bit_cast(float, x); }
@@ -152,6 +153,20 @@ constexpr int kRowPitch = kD + 8;      // q and k by row: 16 rows of a 16-byte r
 constexpr int kColPitch = kChunk + 8;  // k, v by channel and the chunk's weights: the same
 constexpr float kGateOff = -104.0f;    // exp of it is 0 in f32
 
+// Up to 32 rows of one head as a buffer: reads past the last row give 0 and
+// writes there are dropped, so that the row loops need no branches.
+struct Rows {
+    __amdgpu_buffer_rsrc_t buffer;
+    int pitch;   // bytes from row to row
+};
+
+__device__ __forceinline__ Rows rows_of(const void* p, int es, long long row, int rows, int heads, int head) {
+    const int pitch = heads * kD * es;
+    char* at = static_cast<char*>(const_cast<void*>(p)) + row * pitch + static_cast<long long>(head) * kD * es;
+    const int n = rows > 0 ? (min(rows, kChunk) - 1) * pitch + kD * es : 0;
+    return Rows{__builtin_amdgcn_make_buffer_rsrc(at, 0, n, 0x00020000), pitch};
+}
+
 // Four rows x four channels of one thread, as they come from memory.
 template <bool BF16>
 struct Patch {
@@ -159,22 +174,31 @@ struct Patch {
 };
 
 template <bool BF16>
-__device__ __forceinline__ void load_patch(Patch<BF16>& p, const void* src, long long row0, int rows,
-                                           long long pitch, long long col) {
+__device__ __forceinline__ void load_patch(Patch<BF16>& p, const Rows& x, int row, int col) {
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
-        const long long at = (row0 + i) * pitch + col;
+        const int at = (row + i) * x.pitch + col * (BF16 ? 2 : 4);
         if constexpr (BF16) {
-            uint2 x = make_uint2(0, 0);
-            if (i < rows) x = *reinterpret_cast<const uint2*>(static_cast<const uint16_t*>(src) + at);
-            if (i & 1) { p.r[i >> 1].z = x.x; p.r[i >> 1].w = x.y; }
-            else       { p.r[i >> 1].x = x.x; p.r[i >> 1].y = x.y; }
+            const uint2 y = __builtin_bit_cast(uint2, __builtin_amdgcn_raw_buffer_load_b64(x.buffer, at, 0, 0));
+            if (i & 1) { p.r[i >> 1].z = y.x; p.r[i >> 1].w = y.y; }
+            else       { p.r[i >> 1].x = y.x; p.r[i >> 1].y = y.y; }
         } else {
-            p.r[i] = make_uint4(0, 0, 0, 0);
-            if (i < rows) p.r[i] = *reinterpret_cast<const uint4*>(static_cast<const float*>(src) + at);
+            p.r[i] = __builtin_bit_cast(uint4, __builtin_amdgcn_raw_buffer_load_b128(x.buffer, at, 0, 0));
         }
     }
 }
+
+// One element, raw; element() makes it a number.
+template <bool BF16>
+__device__ __forceinline__ uint32_t load_raw(const Rows& x, int row, int col) {
+    if constexpr (BF16)
+        return __builtin_amdgcn_raw_buffer_load_b16(x.buffer, row * x.pitch + col * 2, 0, 0);
+    else
+        return __builtin_amdgcn_raw_buffer_load_b32(x.buffer, row * x.pitch + col * 4, 0, 0);
+}
+
+template <bool BF16>
+__device__ __forceinline__ float element(uint32_t u) { return real(BF16 ? u << 16 : u); }
 
 // The patch's four rows as bf16 words, plane by plane.
 template <bool BF16>
@@ -258,7 +282,7 @@ template <bool BF16, bool STATES>
 __global__ void __launch_bounds__(256, BF16 ? 2 : 1) linear_chunk_kernel(PromptArgs a, Parts parts) {
     constexpr int NS = BF16 ? 1 : 3;
     __shared__ __align__(16) LinearTile<NS> T;
-    const int tid = threadIdx.x, wave = tid >> 6, lane = tid & 63, g4 = lane >> 4, l16 = lane & 15;
+    const int tid = threadIdx.x, wave = __builtin_amdgcn_readfirstlane(tid >> 6), lane = tid & 63, g4 = lane >> 4, l16 = lane & 15;
     const int h = blockIdx.x % a.H, slot = blockIdx.x / a.H;
     const int hk = h / (a.H / a.Hk);
     const Part f = find_part(a, parts.rows, slot);
@@ -302,14 +326,14 @@ __global__ void __launch_bounds__(256, BF16 ? 2 : 1) linear_chunk_kernel(PromptA
     }
 
     const int rg = tid & 7, cg = tid >> 3;
-    const long long kpitch = static_cast<long long>(a.Hk) * kD, vpitch = static_cast<long long>(a.H) * kD;
+    constexpr int es = BF16 ? 2 : 4;
     Patch<BF16> pq, pk, pv;
     float pg = 0.f;
     const auto fetch = [&](int t0) {
-        const int r0 = t0 + 4 * rg, n = end - r0;
-        if (out) load_patch<BF16>(pq, a.q, r0, n, kpitch, hk * kD + 4 * cg);
-        load_patch<BF16>(pk, a.k, r0, n, kpitch, hk * kD + 4 * cg);
-        load_patch<BF16>(pv, a.v, r0, n, vpitch, h * kD + 4 * cg);
+        const int n = end - t0;
+        if (out) load_patch<BF16>(pq, rows_of(a.q, es, t0, n, a.Hk, hk), 4 * rg, 4 * cg);
+        load_patch<BF16>(pk, rows_of(a.k, es, t0, n, a.Hk, hk), 4 * rg, 4 * cg);
+        load_patch<BF16>(pv, rows_of(a.v, es, t0, n, a.H, h), 4 * rg, 4 * cg);
         if (tid < kChunk)
             pg = t0 + tid < end ? static_cast<const float*>(a.g)[static_cast<long long>(t0 + tid) * a.H + h] : 0.f;
     };
@@ -374,6 +398,7 @@ __global__ void __launch_bounds__(256, BF16 ? 2 : 1) linear_chunk_kernel(PromptA
                 for (int s = 0; s < 3; ++s)
                     *reinterpret_cast<uint2*>(&T.p[s][t][16 * jb + 4 * g4]) = w[s];
             }
+            const Rows o = rows_of(a.o, 4, t0, end - t0, a.H, h);
             f32x4 O[2][2];
 #pragma unroll
             for (int c = 0; c < 2; ++c)
@@ -408,10 +433,10 @@ __global__ void __launch_bounds__(256, BF16 ? 2 : 1) linear_chunk_kernel(PromptA
                     read_columns<NS, kD>(T.vt, 32 * wave + 16 * c + l16, 8 * g4, vf);
                     O[c][tb] *= e;
                     O[c][tb] = product<NS, 3>(vf, pf, O[c][tb]);
-                    const int t = t0 + 16 * tb + l16;
-                    if (t < end)
-                        *reinterpret_cast<f32x4*>(a.o + (static_cast<long long>(t) * a.H + h) * kD +
-                                                  32 * wave + 16 * c + 4 * g4) = O[c][tb] * kScale;
+                    const f32x4 y = O[c][tb] * kScale;
+                    __builtin_amdgcn_raw_buffer_store_b128(__builtin_bit_cast(u32x4, y), o.buffer,
+                                                           (16 * tb + l16) * o.pitch +
+                                                               4 * (32 * wave + 16 * c + 4 * g4), 0, 0);
                 }
             }
         }
@@ -581,21 +606,39 @@ __device__ __forceinline__ void patch_values(const Patch<BF16>& p, float (&x)[4]
     }
 }
 
-__device__ __forceinline__ float decay(float g) { return expf(fminf(fmaxf(g, kGateLow), 0.f)); }
+// e^clamp(g): the rounding of g log2(e) is carried over to the result.
+__device__ __forceinline__ float decay(float g) {
+    constexpr float log2e = 1.44269504088896340736f, ln2 = 0.693147180559945309417f;
+    g = fminf(fmaxf(g, kGateLow), 0.f);
+    const float x = g * log2e;
+    const float y = __builtin_amdgcn_exp2f(x);
+    return fmaf(y, fmaf(g, log2e, -x) * ln2, y);
+}
 
 // Eight consecutive elements of a row.
 template <bool BF16>
-__device__ __forceinline__ void load8(const void* src, long long at, float (&x)[8]) {
+struct Eight {
+    uint4 r[BF16 ? 1 : 2];
+};
+
+template <bool BF16>
+__device__ __forceinline__ void load_eight(Eight<BF16>& p, const Rows& x, int row, int col) {
+#pragma unroll
+    for (int i = 0; i < (BF16 ? 1 : 2); ++i)
+        p.r[i] = __builtin_bit_cast(uint4, __builtin_amdgcn_raw_buffer_load_b128(
+                                               x.buffer, row * x.pitch + col * (BF16 ? 2 : 4) + 16 * i, 0, 0));
+}
+
+template <bool BF16>
+__device__ __forceinline__ void eight_values(const Eight<BF16>& p, float (&x)[8]) {
     if constexpr (BF16) {
-        const uint4 u = *reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(src) + at);
-        const uint32_t w[4] = {u.x, u.y, u.z, u.w};
+        const uint32_t w[4] = {p.r[0].x, p.r[0].y, p.r[0].z, p.r[0].w};
 #pragma unroll
         for (int i = 0; i < 8; ++i) x[i] = real(i & 1 ? w[i >> 1] & 0xFFFF0000u : w[i >> 1] << 16);
     } else {
-        const float4 u = reinterpret_cast<const float4*>(static_cast<const float*>(src) + at)[0];
-        const float4 v = reinterpret_cast<const float4*>(static_cast<const float*>(src) + at)[1];
-        x[0] = u.x; x[1] = u.y; x[2] = u.z; x[3] = u.w;
-        x[4] = v.x; x[5] = v.y; x[6] = v.z; x[7] = v.w;
+        const uint32_t w[8] = {p.r[0].x, p.r[0].y, p.r[0].z, p.r[0].w, p.r[1].x, p.r[1].y, p.r[1].z, p.r[1].w};
+#pragma unroll
+        for (int i = 0; i < 8; ++i) x[i] = real(w[i]);
     }
 }
 
@@ -620,18 +663,33 @@ __global__ void __launch_bounds__(256) kda_pair_kernel(PromptArgs a, char* pairs
     __shared__ float between[kD];
     __shared__ float A[kChunk][kChunk + 1], B[kChunk][kChunk + 1], T[kChunk][kChunk + 1];
     __shared__ float beta[kChunk], top[4][4];
-    const int tid = threadIdx.x, wave = tid >> 6, lane = tid & 63, g4 = lane >> 4, l16 = lane & 15;
+    const int tid = threadIdx.x, wave = __builtin_amdgcn_readfirstlane(tid >> 6), lane = tid & 63, g4 = lane >> 4, l16 = lane & 15;
     const int h = blockIdx.x % a.H, slot = blockIdx.x / a.H;
     const Part f = find_part(a, kChunk, slot);
     if (f.b < 0 || a.s_ptrs[f.b] == nullptr) return;
     const int t0 = f.first + f.index * kChunk;
     const int n = min(f.last - t0, kChunk);
-    const long long pitch = static_cast<long long>(a.H) * kD, base = t0 * pitch + h * kD;
+    constexpr int es = BF16 ? 2 : 4;
+
+    // waves 0, 1: the diagonal blocks; 2 and 3: A and B below it
+    const int tb = wave != 0, jb = wave == 1;
+    const bool low = wave >= 2, wantA = wave != 3, wantB = wave != 2;
+    const int tr = 16 * tb + l16, jr = 16 * jb + l16;
+    Eight<BF16> ek[4], et[4], eq[4];
+    {
+        const Rows rk = rows_of(a.k, es, t0, n, a.H, h), rq = rows_of(a.q, es, t0, n, a.H, h);
+#pragma unroll
+        for (int ks = 0; ks < 4; ++ks) {
+            load_eight<BF16>(ek[ks], rk, jr, 32 * ks + 8 * g4);
+            if (low && wantA) load_eight<BF16>(et[ks], rk, tr, 32 * ks + 8 * g4);
+            if (wantB) load_eight<BF16>(eq[ks], rq, tr, 32 * ks + 8 * g4);
+        }
+    }
 
     {   // factors: a thread has 4 rows x 4 channels, 8 neighbouring lanes a channel's 32 rows
         const int rg = tid & 7, cg = tid >> 3;
         Patch<BF16> pg;
-        load_patch<BF16>(pg, a.g, 4 * rg, n - 4 * rg, pitch, base + 4 * cg);
+        load_patch<BF16>(pg, rows_of(a.g, es, t0, n, a.H, h), 4 * rg, 4 * cg);
         float d[4][4];
         patch_values<BF16>(pg, d);
         const bool late = rg & 2;   // behind the middle of its block
@@ -659,7 +717,7 @@ __global__ void __launch_bounds__(256) kda_pair_kernel(PromptArgs a, char* pairs
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
                 const float y = far ? u[i] * near : u[i];
-                F[4 * rg + i][4 * cg + x] = late ? y : 1.f / y;
+                F[4 * rg + i][4 * cg + x] = late ? y : __builtin_amdgcn_rcpf(y);
             }
             const float pair = all * near;                  // lanes 2, 3: rows 8..15; 4, 5: 16..23
             const float c = __shfl(pair, (lane & ~7) | 2) * __shfl(pair, (lane & ~7) | 4);
@@ -670,51 +728,38 @@ __global__ void __launch_bounds__(256) kda_pair_kernel(PromptArgs a, char* pairs
         beta[tid] = tid < n ? load<BF16>(a.beta, static_cast<long long>(t0 + tid) * a.H + h) : 0.f;
     __syncthreads();
 
-    // waves 0, 1: the diagonal blocks; 2 and 3: A and B below it
-    const int tb = wave != 0, jb = wave == 1;
-    const bool low = wave >= 2, wantA = wave != 3, wantB = wave != 2;
     f32x4 xa{0.f, 0.f, 0.f, 0.f}, xb{0.f, 0.f, 0.f, 0.f};
     float kmax = 0.f, qmax = 0.f;
 #pragma unroll
     for (int ks = 0; ks < 4; ++ks) {
         const int c = 32 * ks + 8 * g4;
-        float x[8], y[8];
-        uint4 kj[3], kt[3], qt[3];
-        const int t = 16 * tb + l16, j = 16 * jb + l16;
-#pragma unroll
-        for (int i = 0; i < 8; ++i) x[i] = y[i] = 0.f;
-        if (j < n) load8<BF16>(a.k, base + j * pitch + c, x);
+        float x[8], y[8], ft[8];
+        uint4 kj[3], w[3];
+        eight_values<BF16>(ek[ks], x);
 #pragma unroll
         for (int i = 0; i < 8; ++i) {
-            if (!low) kmax = fmaxf(kmax, fabsf(x[i]));
-            y[i] = x[i] / F[j][c + i];
+            kmax = fmaxf(kmax, fabsf(x[i]));
+            y[i] = x[i] * __builtin_amdgcn_rcpf(F[jr][c + i]);
         }
         split8(y, kj);
-        float ft[8];
 #pragma unroll
-        for (int i = 0; i < 8; ++i) ft[i] = F[t][c + i] * (low ? between[c + i] : 1.f);
+        for (int i = 0; i < 8; ++i) ft[i] = F[tr][c + i] * (low ? between[c + i] : 1.f);
         if (wantA) {
-            if (low) {
-#pragma unroll
-                for (int i = 0; i < 8; ++i) x[i] = 0.f;
-                if (t < n) load8<BF16>(a.k, base + t * pitch + c, x);
-            }
+            if (low) eight_values<BF16>(et[ks], x);
 #pragma unroll
             for (int i = 0; i < 8; ++i) y[i] = x[i] * ft[i];
-            split8(y, kt);
-            xa = product<3, 3>(kt, kj, xa);
+            split8(y, w);
+            xa = product<3, 3>(w, kj, xa);
         }
         if (wantB) {
-#pragma unroll
-            for (int i = 0; i < 8; ++i) x[i] = 0.f;
-            if (t < n) load8<BF16>(a.q, base + t * pitch + c, x);
+            eight_values<BF16>(eq[ks], x);
 #pragma unroll
             for (int i = 0; i < 8; ++i) {
-                if (!low) qmax = fmaxf(qmax, fabsf(x[i]));
+                qmax = fmaxf(qmax, fabsf(x[i]));
                 y[i] = x[i] * ft[i];
             }
-            split8(y, qt);
-            xb = product<3, 3>(qt, kj, xb);
+            split8(y, w);
+            xb = product<3, 3>(w, kj, xb);
         }
     }
 #pragma unroll
@@ -826,7 +871,7 @@ __global__ void __launch_bounds__(512) kda_chunk_kernel(PromptArgs a, const char
                                                         const ChunkScale* scales) {
     __shared__ __align__(16) KdaTile tiles[2];
     __shared__ f32x4 xr[4][2][64], xo[4][64];
-    const int tid = threadIdx.x, wave = tid >> 6, lane = tid & 63, g4 = lane >> 4, l16 = lane & 15;
+    const int tid = threadIdx.x, wave = __builtin_amdgcn_readfirstlane(tid >> 6), lane = tid & 63, g4 = lane >> 4, l16 = lane & 15;
     constexpr int slices = kD / kKdaCols;
     const int h = blockIdx.x / slices % a.H, b = blockIdx.x / slices / a.H, slice = blockIdx.x % slices;
     int first, last;
@@ -835,7 +880,7 @@ __global__ void __launch_bounds__(512) kda_chunk_kernel(PromptArgs a, const char
     if (state == nullptr || first >= last) return;
     state += static_cast<long long>(h) * kD * kD;
     const int chunks = (last - first + kChunk - 1) / kChunk;
-    const long long pitch = static_cast<long long>(a.H) * kD;
+    constexpr int es = BF16 ? 2 : 4;
     const long long slot0 = (static_cast<long long>(first / kChunk) + b) * a.H + h;
 
     if (wave >= 4) {
@@ -843,17 +888,23 @@ __global__ void __launch_bounds__(512) kda_chunk_kernel(PromptArgs a, const char
         Patch<BF16> pq, pk, pg;
         ChunkScale sc{};
         const auto fetch = [&](int i) {
-            const int r0 = first + i * kChunk + 4 * rg, n = last - r0;
-            const long long col = static_cast<long long>(h) * kD + 4 * cg;
-            if (OUT) load_patch<BF16>(pq, a.q, r0, n, pitch, col);
-            load_patch<BF16>(pk, a.k, r0, n, pitch, col);
-            load_patch<BF16>(pg, a.g, r0, n, pitch, col);
+            const int t0 = first + i * kChunk, n = last - t0;
+            if (OUT) load_patch<BF16>(pq, rows_of(a.q, es, t0, n, a.H, h), 4 * rg, 4 * cg);
+            load_patch<BF16>(pk, rows_of(a.k, es, t0, n, a.H, h), 4 * rg, 4 * cg);
+            load_patch<BF16>(pg, rows_of(a.g, es, t0, n, a.H, h), 4 * rg, 4 * cg);
             sc = scales[slot0 + static_cast<long long>(i) * a.H];
         };
-        const auto stage = [&](KdaTile& T) {
-            float d[4][4], k[4][4], pre[4][4], suf[4][4];
+        float k[4][4], q[4][4], pre[4][4], suf[4][4], keep[4];
+        float sk = 1.f, sq = 1.f;
+        // the next chunk's decays, and the loads of the one behind it
+        const auto decays = [&](int next) {
+            float d[4][4];
             patch_values<BF16>(pg, d);
             patch_values<BF16>(pk, k);
+            if (OUT) patch_values<BF16>(pq, q);
+            sk = sc.k;
+            sq = sc.q;
+            if (next < chunks) fetch(next);
 #pragma unroll
             for (int c = 0; c < 4; ++c) {
 #pragma unroll
@@ -874,22 +925,23 @@ __global__ void __launch_bounds__(512) kda_chunk_kernel(PromptArgs a, const char
                 }
                 float before = __shfl_up(up, 1), behind = __shfl_down(down, 1);
                 if (rg == 0) before = 1.f;
-                if (rg == 7) {
-                    behind = 1.f;
-                    T.keep[4 * cg + c] = up;
-                }
+                if (rg == 7) behind = 1.f;
+                keep[c] = up;
 #pragma unroll
                 for (int i = 0; i < 4; ++i) {
                     pre[i][c] *= before;
                     suf[i][c] *= behind;
                 }
             }
+        };
+        const auto stage = [&](KdaTile& T) {
+            if (rg == 7) *reinterpret_cast<float4*>(&T.keep[4 * cg]) = make_float4(keep[0], keep[1], keep[2], keep[3]);
             uint2 w[4][2];
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
                 float y[4];
 #pragma unroll
-                for (int c = 0; c < 4; ++c) y[c] = k[i][c] * pre[i][c] * sc.k;
+                for (int c = 0; c < 4; ++c) y[c] = k[i][c] * pre[i][c] * sk;
                 halves4(y, w[i]);
             }
             store_rows<2>(T.k, cg, rg, w);
@@ -897,32 +949,29 @@ __global__ void __launch_bounds__(512) kda_chunk_kernel(PromptArgs a, const char
             for (int i = 0; i < 4; ++i) {
                 float y[4];
 #pragma unroll
-                for (int c = 0; c < 4; ++c) y[c] = k[i][c] * suf[i][c] * sc.k;
+                for (int c = 0; c < 4; ++c) y[c] = k[i][c] * suf[i][c] * sk;
                 halves4(y, w[i]);
             }
             store_columns<2>(T.kt, cg, 8 * (rg & 3) + 4 * (rg >> 2), w);
             if (OUT) {
-                patch_values<BF16>(pq, k);
 #pragma unroll
                 for (int i = 0; i < 4; ++i) {
                     float y[4];
 #pragma unroll
-                    for (int c = 0; c < 4; ++c) y[c] = k[i][c] * pre[i][c] * sc.q;
+                    for (int c = 0; c < 4; ++c) y[c] = q[i][c] * pre[i][c] * sq;
                     halves4(y, w[i]);
                 }
                 store_rows<2>(T.q, cg, rg, w);
             }
         };
         fetch(0);
+        decays(1);
         stage(tiles[0]);
-        if (chunks > 1) fetch(1);
         for (int i = 0; i < chunks; ++i) {
             __syncthreads();
-            if (i + 1 < chunks) {
-                stage(tiles[(i + 1) & 1]);
-                if (i + 2 < chunks) fetch(i + 2);
-            }
+            if (i + 1 < chunks) decays(i + 2);
             __syncthreads();
+            if (i + 1 < chunks) stage(tiles[(i + 1) & 1]);
         }
         return;
     }
@@ -938,7 +987,7 @@ __global__ void __launch_bounds__(512) kda_chunk_kernel(PromptArgs a, const char
             smax = fmaxf(smax, fabsf(S[m][r]));
         }
     uint4 mf[2][2], bf[2];
-    float v[2][4];
+    uint32_t v[2][4];
     ChunkScale sc{};
     const auto fetch = [&](int i) {
         const long long at = slot0 + static_cast<long long>(i) * a.H;
@@ -950,14 +999,14 @@ __global__ void __launch_bounds__(512) kda_chunk_kernel(PromptArgs a, const char
             if (OUT) bf[s] = p[((2 + s) * kChunk + 16 * half + l16) * 4 + g4];
         }
         sc = scales[at];
-        if (half == 0)
+        if (half == 0) {
+            const int t0 = first + i * kChunk;
+            const Rows rv = rows_of(a.v, es, t0, last - t0, a.H, h);
 #pragma unroll
             for (int tb = 0; tb < 2; ++tb)
 #pragma unroll
-                for (int r = 0; r < 4; ++r) {
-                    const int t = first + i * kChunk + 16 * tb + 4 * g4 + r;
-                    v[tb][r] = t < last ? load<BF16>(a.v, t * pitch + h * kD + col) : 0.f;
-                }
+                for (int r = 0; r < 4; ++r) v[tb][r] = load_raw<BF16>(rv, 16 * tb + 4 * g4 + r, col);
+        }
     };
     fetch(0);
 
@@ -989,7 +1038,7 @@ __global__ void __launch_bounds__(512) kda_chunk_kernel(PromptArgs a, const char
             R[tb] = R[tb] * sk * si;
             if (half == 0)
 #pragma unroll
-                for (int r = 0; r < 4; ++r) R[tb][r] -= v[tb][r];
+                for (int r = 0; r < 4; ++r) R[tb][r] -= element<BF16>(v[tb][r]);
             xr[wave][tb][lane] = R[tb];
             Q[tb] = Q[tb] * sq * si;
         }
@@ -1018,11 +1067,12 @@ __global__ void __launch_bounds__(512) kda_chunk_kernel(PromptArgs a, const char
         if (OUT) {
             f32x4 O = half == 0 ? Q[0] : Q[1];
             O = O + xo[wave ^ 2][lane] + product16(bf, ef, f32x4{0.f, 0.f, 0.f, 0.f}) * inverse_of(sc.b) * ei;
+            const int t0 = first + i * kChunk;
+            const Rows ro = rows_of(a.o, 4, t0, last - t0, a.H, h);
 #pragma unroll
-            for (int r = 0; r < 4; ++r) {
-                const int t = first + i * kChunk + 16 * half + 4 * g4 + r;
-                if (t < last) a.o[t * pitch + h * kD + col] = O[r] * kScale;
-            }
+            for (int r = 0; r < 4; ++r)
+                __builtin_amdgcn_raw_buffer_store_b32(bits(O[r] * kScale), ro.buffer,
+                                                      (16 * half + 4 * g4 + r) * ro.pitch + 4 * col, 0, 0);
         }
         if (i + 1 < chunks) fetch(i + 1);
         smax = 0.f;
