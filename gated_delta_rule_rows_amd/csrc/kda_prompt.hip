@@ -528,20 +528,34 @@ __global__ void __launch_bounds__(256) linear_chain_kernel(PromptArgs a, Parts p
 //   E   = (I + diag(beta) A)^-1 diag(beta) (V - (k e^G) S_0)  =  M (V - (k e^G) S_0)
 //   O   = [ (q e^G) S_0 + B E ] / sqrt(128)
 //   S_C = diag(e^{G_C}) S_0 + (k e^{G_C-G})^T E
-// M and B need no state: a first launch computes them for all chunks side by
-// side.  A second launch walks the chunks of each sequence.
+// Nothing but S_0 ties one chunk to the next: a first launch prepares all chunks
+// side by side (M, B, k e^G, q e^G, k e^{G_C-G}, e^{G_C}), and a second walks the
+// chunks of each sequence, where only the products are left.
 
 using f16x8 = __attribute__((ext_vector_type(8))) _Float16;
 using f16x2 = __attribute__((ext_vector_type(2))) _Float16;
 using f32x2 = __attribute__((ext_vector_type(2))) float;
 
 constexpr int kSub = 16;                        // rows of a block of A and B
-constexpr long long kPairBytes = 2ll * 2 * kChunk * kChunk * 2;   // M and B, two f16 words each
 
 // The scales of a chunk's f16 words, powers of two.
 struct ChunkScale {
     float k, q, m, b;
 };
+
+// One chunk of one head, ready for the products: 16-byte operands of 64 lanes,
+// two f16 words each, the contracted index in the order of an accumulator.
+struct KdaBlock {
+    uint4 k[2][4][2][64];    // k e^G: 16-row block, 32-channel block, word, lane
+    uint4 q[2][4][2][64];    // q e^G
+    uint4 kt[8][2][64];      // k e^{G_C-G}: 16-channel block, word, lane
+    uint4 m[2][2][64];       // M: 16-row block, word, lane
+    uint4 b[2][2][64];       // B
+    float keep[kD];          // e^{G_C}
+    ChunkScale scale;
+    float unused[124];
+};
+static_assert(sizeof(KdaBlock) == 57 * 1024, "whole kilobytes");
 
 // A power of two that brings m into [2^13, 2^14): the largest f16 word then
 // keeps 22 bits in two words, and what falls below f16's range is under 2^-38
@@ -555,24 +569,35 @@ __device__ __forceinline__ float scale_of(float m) {
 // 1 / s of a power of two from scale_of.
 __device__ __forceinline__ float inverse_of(float s) { return real(0x7F000000u - bits(s)); }
 
-// Two f32 values as two words of two f16 each (22 bits).
-__device__ __forceinline__ void halves2(float x0, float x1, uint32_t& a, uint32_t& b) {
-    const f16x2 h = __builtin_convertvector((f32x2{x0, x1}), f16x2);
-    const f16x2 l = __builtin_convertvector((f32x2{x0 - static_cast<float>(h[0]), x1 - static_cast<float>(h[1])}), f16x2);
+// x0 s0 and x1 s1 as two words of two f16 each (22 bits).  The products are
+// formed inside the two roundings: the second word holds what the first left of
+// the exact product.
+__device__ __forceinline__ void halves2(float x0, float s0, float x1, float s1, uint32_t& a, uint32_t& b) {
+    const f16x2 h{static_cast<_Float16>(fmaf(x0, s0, 0.f)), static_cast<_Float16>(fmaf(x1, s1, 0.f))};
+    const f16x2 l{static_cast<_Float16>(fmaf(x0, s0, -static_cast<float>(h[0]))),
+                  static_cast<_Float16>(fmaf(x1, s1, -static_cast<float>(h[1])))};
     a = __builtin_bit_cast(uint32_t, h);
     b = __builtin_bit_cast(uint32_t, l);
 }
 
-__device__ __forceinline__ void halves4(const float (&x)[4], uint2 (&w)[2]) {
-    halves2(x[0], x[1], w[0].x, w[1].x);
-    halves2(x[2], x[3], w[0].y, w[1].y);
+__device__ __forceinline__ void halves4(const float (&x)[4], const float (&s)[4], uint2 (&w)[2]) {
+    halves2(x[0], s[0], x[1], s[1], w[0].x, w[1].x);
+    halves2(x[2], s[2], x[3], s[3], w[0].y, w[1].y);
 }
 
 __device__ __forceinline__ void halves8(const f32x4& lo, const f32x4& hi, float s, uint4 (&w)[2]) {
-    halves2(lo[0] * s, lo[1] * s, w[0].x, w[1].x);
-    halves2(lo[2] * s, lo[3] * s, w[0].y, w[1].y);
-    halves2(hi[0] * s, hi[1] * s, w[0].z, w[1].z);
-    halves2(hi[2] * s, hi[3] * s, w[0].w, w[1].w);
+    halves2(lo[0], s, lo[1], s, w[0].x, w[1].x);
+    halves2(lo[2], s, lo[3], s, w[0].y, w[1].y);
+    halves2(hi[0], s, hi[1], s, w[0].z, w[1].z);
+    halves2(hi[2], s, hi[3], s, w[0].w, w[1].w);
+}
+
+__device__ __forceinline__ float abs_max(float a, float b, float c) {
+    return fmaxf(fmaxf(fabsf(a), fabsf(b)), c);
+}
+
+__device__ __forceinline__ float abs_max(const f32x4& x, float c) {
+    return abs_max(x[0], x[1], abs_max(x[2], x[3], c));
 }
 
 // a . b over two f16 words each: all products but low x low (under 2^-22).
@@ -648,7 +673,27 @@ __device__ __forceinline__ float wave_max(float x) {
     return x;
 }
 
-// M and B of one chunk of one head.
+// max over the four lanes that share a column.  (Written as asm: the swap
+// builtins return the first register for both results.  The s_nop covers the
+// wait states between a VALU write and a swap that reads it.)
+__device__ __forceinline__ float column_max(float x) {
+    float y = x;
+    asm volatile("s_nop 1\n\tv_permlane32_swap_b32 %0, %1" : "+v"(x), "+v"(y));
+    x = abs_max(x, y, 0.f);
+    y = x;
+    asm volatile("s_nop 1\n\tv_permlane16_swap_b32 %0, %1" : "+v"(x), "+v"(y));
+    return abs_max(x, y, 0.f);
+}
+
+// x of the lane N before (or behind) this one, 0 where there is none in its row of 16.
+template <int CTRL>
+__device__ __forceinline__ float neighbour(float x) {
+    return real(__builtin_amdgcn_update_dpp(0, bits(x), CTRL, 0xF, 0xF, true));
+}
+template <int N> __device__ __forceinline__ float lane_before(float x) { return neighbour<0x110 + N>(x); }
+template <int N> __device__ __forceinline__ float lane_behind(float x) { return neighbour<0x100 + N>(x); }
+
+// Prepares one chunk of one head.
 //
 // e^{G_t-G_j} does not split into a factor of t and one of j over the chunk's
 // whole range (e^{-5 * 32} leaves f32), so A and B are three blocks of 16 x 16:
@@ -658,74 +703,94 @@ __device__ __forceinline__ float wave_max(float x) {
 // the rows' decays, which do not lose the weak gates behind strong ones as
 // differences of sums would.
 template <bool BF16>
-__global__ void __launch_bounds__(256) kda_pair_kernel(PromptArgs a, char* pairs, ChunkScale* scales) {
-    __shared__ __align__(16) float F[kChunk][kD + 4];
-    __shared__ float between[kD];
+__global__ void __launch_bounds__(256) kda_prepare_kernel(PromptArgs a, KdaBlock* blocks, int slot0) {
+    struct Factors {
+        float F[kChunk][kD + 4];
+        float between[kD];
+    };
+    __shared__ __align__(16) union {
+        Factors f;
+        uint4 words[3 * 16 * 64];   // k, q and kt of the block
+    } U;
     __shared__ float A[kChunk][kChunk + 1], B[kChunk][kChunk + 1], T[kChunk][kChunk + 1];
     __shared__ float beta[kChunk], top[4][4];
     const int tid = threadIdx.x, wave = __builtin_amdgcn_readfirstlane(tid >> 6), lane = tid & 63, g4 = lane >> 4, l16 = lane & 15;
-    const int h = blockIdx.x % a.H, slot = blockIdx.x / a.H;
+    const int h = blockIdx.x % a.H, slot = slot0 + blockIdx.x / a.H;
     const Part f = find_part(a, kChunk, slot);
     if (f.b < 0 || a.s_ptrs[f.b] == nullptr) return;
     const int t0 = f.first + f.index * kChunk;
     const int n = min(f.last - t0, kChunk);
     constexpr int es = BF16 ? 2 : 4;
 
+    // a thread has 4 rows x 4 channels, 8 neighbouring lanes a channel's 32 rows
+    const int rg = tid & 7, cg = tid >> 3;
+    const Rows rk = rows_of(a.k, es, t0, n, a.H, h), rq = rows_of(a.q, es, t0, n, a.H, h);
+    Patch<BF16> pg, pk, pq;
+    load_patch<BF16>(pg, rows_of(a.g, es, t0, n, a.H, h), 4 * rg, 4 * cg);
     // waves 0, 1: the diagonal blocks; 2 and 3: A and B below it
     const int tb = wave != 0, jb = wave == 1;
     const bool low = wave >= 2, wantA = wave != 3, wantB = wave != 2;
     const int tr = 16 * tb + l16, jr = 16 * jb + l16;
     Eight<BF16> ek[4], et[4], eq[4];
-    {
-        const Rows rk = rows_of(a.k, es, t0, n, a.H, h), rq = rows_of(a.q, es, t0, n, a.H, h);
 #pragma unroll
-        for (int ks = 0; ks < 4; ++ks) {
-            load_eight<BF16>(ek[ks], rk, jr, 32 * ks + 8 * g4);
-            if (low && wantA) load_eight<BF16>(et[ks], rk, tr, 32 * ks + 8 * g4);
-            if (wantB) load_eight<BF16>(eq[ks], rq, tr, 32 * ks + 8 * g4);
-        }
+    for (int ks = 0; ks < 4; ++ks) {
+        load_eight<BF16>(ek[ks], rk, jr, 32 * ks + 8 * g4);
+        if (low && wantA) load_eight<BF16>(et[ks], rk, tr, 32 * ks + 8 * g4);
+        if (wantB) load_eight<BF16>(eq[ks], rq, tr, 32 * ks + 8 * g4);
     }
+    load_patch<BF16>(pk, rk, 4 * rg, 4 * cg);
+    load_patch<BF16>(pq, rq, 4 * rg, 4 * cg);
+    if (tid < kChunk)
+        beta[tid] = tid < n ? load<BF16>(a.beta, static_cast<long long>(t0 + tid) * a.H + h) : 0.f;
 
-    {   // factors: a thread has 4 rows x 4 channels, 8 neighbouring lanes a channel's 32 rows
-        const int rg = tid & 7, cg = tid >> 3;
-        Patch<BF16> pg;
-        load_patch<BF16>(pg, rows_of(a.g, es, t0, n, a.H, h), 4 * rg, 4 * cg);
+    float pre[4][4], suf[4][4], keep[4];   // e^{G_t} and e^{G_C-G_t} of the thread's elements
+    {
         float d[4][4];
         patch_values<BF16>(pg, d);
         const bool late = rg & 2;   // behind the middle of its block
 #pragma unroll
-        for (int x = 0; x < 4; ++x) {
+        for (int c = 0; c < 4; ++c) {
+#pragma unroll
+            for (int i = 0; i < 4; ++i) d[i][c] = decay(d[i][c]);
+            pre[0][c] = d[0][c];
+#pragma unroll
+            for (int i = 1; i < 4; ++i) pre[i][c] = pre[i - 1][c] * d[i][c];
+            suf[3][c] = 1.f;
+#pragma unroll
+            for (int i = 2; i >= 0; --i) suf[i][c] = suf[i + 1][c] * d[i + 1][c];
+            const float all = pre[3][c];
+            const float near = real(__builtin_amdgcn_update_dpp(0, bits(all), 0xB1, 0xF, 0xF, true));   // lane ^ 1
             // a late row's f is the product from the middle to it; an early row's
             // 1/f the product of what lies between it and the middle
-#pragma unroll
-            for (int i = 0; i < 4; ++i) d[i][x] = decay(d[i][x]);
-            const float all = d[0][x] * d[1][x] * (d[2][x] * d[3][x]);
-            const float near = __shfl_xor(all, 1);
-            float u[4];
-            if (late) {
-                u[0] = d[0][x];
-                u[1] = u[0] * d[1][x];
-                u[2] = u[1] * d[2][x];
-                u[3] = u[2] * d[3][x];
-            } else {
-                u[3] = 1.f;
-                u[2] = d[3][x];
-                u[1] = u[2] * d[2][x];
-                u[0] = u[1] * d[1][x];
-            }
-            const bool far = late == static_cast<bool>(rg & 1);
+            const float beyond = late == static_cast<bool>(rg & 1) ? near : 1.f;
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
-                const float y = far ? u[i] * near : u[i];
-                F[4 * rg + i][4 * cg + x] = late ? y : __builtin_amdgcn_rcpf(y);
+                const float y = (late ? pre[i][c] : suf[i][c]) * beyond;
+                U.f.F[4 * rg + i][4 * cg + c] = late ? y : __builtin_amdgcn_rcpf(y);
             }
-            const float pair = all * near;                  // lanes 2, 3: rows 8..15; 4, 5: 16..23
-            const float c = __shfl(pair, (lane & ~7) | 2) * __shfl(pair, (lane & ~7) | 4);
-            if (rg == 0) between[4 * cg + x] = c;
+            // between the middles: row groups 2, 3 and 4, 5
+            const float pair = all * near, next = lane_behind<2>(pair);
+            if (rg == 2) U.f.between[4 * cg + c] = pair * next;
+            // products over the row groups before and behind this one
+            float up = all, down = all;
+            float y = lane_before<1>(up), z = lane_behind<1>(down);
+            up *= rg >= 1 ? y : 1.f;
+            down *= rg < 7 ? z : 1.f;
+            y = lane_before<2>(up), z = lane_behind<2>(down);
+            up *= rg >= 2 ? y : 1.f;
+            down *= rg < 6 ? z : 1.f;
+            y = lane_before<4>(up), z = lane_behind<4>(down);
+            up *= rg >= 4 ? y : 1.f;
+            down *= rg < 4 ? z : 1.f;
+            y = lane_before<1>(up), z = lane_behind<1>(down);
+            keep[c] = up;
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                pre[i][c] *= rg >= 1 ? y : 1.f;
+                suf[i][c] *= rg < 7 ? z : 1.f;
+            }
         }
     }
-    if (tid < kChunk)
-        beta[tid] = tid < n ? load<BF16>(a.beta, static_cast<long long>(t0 + tid) * a.H + h) : 0.f;
     __syncthreads();
 
     f32x4 xa{0.f, 0.f, 0.f, 0.f}, xb{0.f, 0.f, 0.f, 0.f};
@@ -739,11 +804,11 @@ __global__ void __launch_bounds__(256) kda_pair_kernel(PromptArgs a, char* pairs
 #pragma unroll
         for (int i = 0; i < 8; ++i) {
             kmax = fmaxf(kmax, fabsf(x[i]));
-            y[i] = x[i] * __builtin_amdgcn_rcpf(F[jr][c + i]);
+            y[i] = x[i] * __builtin_amdgcn_rcpf(U.f.F[jr][c + i]);
         }
         split8(y, kj);
 #pragma unroll
-        for (int i = 0; i < 8; ++i) ft[i] = F[tr][c + i] * (low ? between[c + i] : 1.f);
+        for (int i = 0; i < 8; ++i) ft[i] = U.f.F[tr][c + i] * (low ? U.f.between[c + i] : 1.f);
         if (wantA) {
             if (low) eight_values<BF16>(et[ks], x);
 #pragma unroll
@@ -762,6 +827,12 @@ __global__ void __launch_bounds__(256) kda_pair_kernel(PromptArgs a, char* pairs
             xb = product<3, 3>(w, kj, xb);
         }
     }
+    kmax = wave_max(kmax);
+    qmax = wave_max(qmax);
+    if (lane == 0) {
+        top[0][wave] = kmax;
+        top[1][wave] = qmax;
+    }
 #pragma unroll
     for (int r = 0; r < 4; ++r) {
         const int t = 16 * tb + 4 * g4 + r, j = 16 * jb + l16;
@@ -771,7 +842,7 @@ __global__ void __launch_bounds__(256) kda_pair_kernel(PromptArgs a, char* pairs
     }
     __syncthreads();
 
-    // T = (I - A)^-1: the diagonal blocks column by column, then the one below
+    // T = (I - A)^-1: the diagonal blocks column by column by the first wave ...
     if (tid < kChunk) {
         const int o = tid & 16, c = tid & 15;
         float x[kSub];
@@ -784,8 +855,59 @@ __global__ void __launch_bounds__(256) kda_pair_kernel(PromptArgs a, char* pairs
             T[o + t][o + c] = s;
         }
     }
+    // ... and beside it the operands; the factors' memory is free
+    const float sk = scale_of(fmaxf(fmaxf(top[0][0], top[0][1]), fmaxf(top[0][2], top[0][3])));
+    const float sq = scale_of(fmaxf(fmaxf(top[1][0], top[1][1]), fmaxf(top[1][2], top[1][3])));
+    {
+        float x[4][4];
+        uint2 w[4][2];
+        uint2* const to = reinterpret_cast<uint2*>(U.words);
+        const int at = (cg >> 3) * 2 * 128 + (cg & 3) * 32 + (cg >> 2 & 1);   // channel part of a row operand
+        patch_values<BF16>(pk, x);
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+#pragma unroll
+            for (int c = 0; c < 4; ++c) x[i][c] *= sk;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            halves4(x[i], pre[i], w[i]);
+            const int t = 4 * rg + i;
+#pragma unroll
+            for (int s = 0; s < 2; ++s) to[(t >> 4) * 8 * 128 + s * 128 + at + 2 * (t & 15)] = w[i][s];
+        }
+#pragma unroll
+        for (int i = 0; i < 4; ++i) halves4(x[i], suf[i], w[i]);
+#pragma unroll
+        for (int s = 0; s < 2; ++s)
+#pragma unroll
+            for (int c = 0; c < 4; ++c) {
+                const uint32_t sel = c & 1 ? 0x07060302u : 0x05040100u;
+                uint2 y;
+                y.x = __builtin_amdgcn_perm(c < 2 ? w[1][s].x : w[1][s].y, c < 2 ? w[0][s].x : w[0][s].y, sel);
+                y.y = __builtin_amdgcn_perm(c < 2 ? w[3][s].x : w[3][s].y, c < 2 ? w[2][s].x : w[2][s].y, sel);
+                to[32 * 128 + ((cg >> 2) * 2 + s) * 128 + (rg & 3) * 32 + 2 * (4 * (cg & 3) + c) + (rg >> 2)] = y;
+            }
+        patch_values<BF16>(pq, x);
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+#pragma unroll
+            for (int c = 0; c < 4; ++c) x[i][c] *= sq;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            halves4(x[i], pre[i], w[i]);
+            const int t = 4 * rg + i;
+#pragma unroll
+            for (int s = 0; s < 2; ++s) to[16 * 128 + (t >> 4) * 8 * 128 + s * 128 + at + 2 * (t & 15)] = w[i][s];
+        }
+    }
+    KdaBlock& out = blocks[blockIdx.x];
+    if (rg == 7) *reinterpret_cast<float4*>(&out.keep[4 * cg]) = make_float4(keep[0], keep[1], keep[2], keep[3]);
     __syncthreads();
     {
+        uint4* to = &out.k[0][0][0][0];
+#pragma unroll
+        for (int i = 0; i < 12; ++i) to[256 * i + tid] = U.words[256 * i + tid];
+        // the block of T below the diagonal
         const int t = tid >> 4, j = tid & 15;
         float s = 0.f;
 #pragma unroll
@@ -809,283 +931,195 @@ __global__ void __launch_bounds__(256) kda_pair_kernel(PromptArgs a, char* pairs
         mmax = fmaxf(mmax, fabsf(m[i]));
         bmax = fmaxf(bmax, fabsf(b[i]));
     }
-    kmax = wave_max(kmax);
-    qmax = wave_max(qmax);
     mmax = wave_max(mmax);
     bmax = wave_max(bmax);
     if (lane == 0) {
-        top[0][wave] = kmax;
-        top[1][wave] = qmax;
         top[2][wave] = mmax;
         top[3][wave] = bmax;
     }
     __syncthreads();
-    float s[4];
-#pragma unroll
-    for (int i = 0; i < 4; ++i)
-        s[i] = scale_of(fmaxf(fmaxf(top[i][0], top[i][1]), fmaxf(top[i][2], top[i][3])));
-    const long long at = static_cast<long long>(slot) * a.H + h;
-    if (tid == 0) scales[at] = ChunkScale{s[0], s[1], s[2], s[3]};
-    // by row, the columns of the 32 in operand order
-    uint2* to = reinterpret_cast<uint2*>(pairs + at * kPairBytes) + t * 8 + 2 * (x & 3) + (x >> 2);
+    const float sm = scale_of(fmaxf(fmaxf(top[2][0], top[2][1]), fmaxf(top[2][2], top[2][3])));
+    const float sb = scale_of(fmaxf(fmaxf(top[3][0], top[3][1]), fmaxf(top[3][2], top[3][3])));
+    if (tid == 0) out.scale = ChunkScale{sk, sq, sm, sb};
+    const float am[4] = {sm, sm, sm, sm}, ab[4] = {sb, sb, sb, sb};
+    const int at = (t >> 4) * 2 * 128 + (x & 3) * 32 + 2 * (t & 15) + (x >> 2);
     uint2 w[2];
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-        m[i] *= s[2];
-        b[i] *= s[3];
-    }
-    halves4(m, w);
+    halves4(m, am, w);
+    uint2* to = reinterpret_cast<uint2*>(&out.m[0][0][0]) + at;
     to[0] = w[0];
-    to[kChunk * 8] = w[1];
-    halves4(b, w);
-    to[2 * kChunk * 8] = w[0];
-    to[3 * kChunk * 8] = w[1];
+    to[128] = w[1];
+    halves4(b, ab, w);
+    to = reinterpret_cast<uint2*>(&out.b[0][0][0]) + at;
+    to[0] = w[0];
+    to[128] = w[1];
 }
 
-struct KdaTile {
-    uint16_t q[2][kChunk][kRowPitch];    // q e^G by row
-    uint16_t k[2][kChunk][kRowPitch];    // k e^G by row
-    uint16_t kt[2][kD][kColPitch];       // k e^{G_C-G} by channel, the rows in operand order
-    float keep[kD];                      // e^{G_C}
-};
-
-constexpr int kKdaCols = 32;   // value columns of a workgroup
-
-// max over the four lanes that share a column
-__device__ __forceinline__ float column_max(float x) {
-    x = fmaxf(x, __shfl_xor(x, 16));
-    return fmaxf(x, __shfl_xor(x, 32));
-}
-
-// The chunks of one sequence and head, 32 value columns.  Waves 4..7 prepare
-// the next chunk's operands in LDS while waves 0..3 take the current one
-// through: wave 2 * half + c has value columns 16 c.. and key channels
-// 64 half.. of the state in 16 registers, and the two halves of a column block
-// exchange their parts of the sums over channels through LDS.
+// The chunks in slots slot0 .. slot1-1 of one sequence and head, 16 * NC value
+// columns.  Wave NC * half + c has the columns of block c and key channels
+// 64 half.. of the state in 16 registers; the two halves of a column block
+// exchange their parts of the sums over channels through LDS.  The next chunk's
+// operands are on their way to registers while the current one is worked on,
+// and go to the other half of LDS behind it.
 //
 // Operands are two f16 words of a value scaled by a power of two (3 products,
 // 22 bits): state, right-hand side and deltas by their column's largest,
 // k, q, M and B by the chunk's.
-template <bool BF16, bool OUT>
-__global__ void __launch_bounds__(512) kda_chunk_kernel(PromptArgs a, const char* pairs,
-                                                        const ChunkScale* scales) {
-    __shared__ __align__(16) KdaTile tiles[2];
-    __shared__ f32x4 xr[4][2][64], xo[4][64];
+template <bool BF16, bool OUT, int NC>
+__global__ void __launch_bounds__(128 * NC) kda_chunk_kernel(PromptArgs a, const KdaBlock* blocks, int slot0,
+                                                             int slot1) {
+    __shared__ __align__(16) KdaBlock tiles[2];
+    __shared__ f32x4 xr[2 * NC][2][64], xo[2 * NC][64];
+    constexpr int slices = 8 / NC, threads = 128 * NC, pieces = sizeof(KdaBlock) / 16;
+    constexpr int copies = (pieces + threads - 1) / threads;
+    constexpr int es = BF16 ? 2 : 4;
     const int tid = threadIdx.x, wave = __builtin_amdgcn_readfirstlane(tid >> 6), lane = tid & 63, g4 = lane >> 4, l16 = lane & 15;
-    constexpr int slices = kD / kKdaCols;
-    const int h = blockIdx.x / slices % a.H, b = blockIdx.x / slices / a.H, slice = blockIdx.x % slices;
+    // workgroups go round 8 XCDs: the slices of a head to one of them, whose L2
+    // then has the operands that they share
+    const int turn = blockIdx.x / (8 * slices), within = blockIdx.x % (8 * slices);
+    const int bh = 8 * turn + (within & 7), slice = within >> 3;
+    if (bh >= a.B * a.H) return;
+    const int h = bh % a.H, b = bh / a.H;
     int first, last;
     sequence(a, b, first, last);
+    const int own = first / kChunk + b, chunks = (last - first + kChunk - 1) / kChunk;
+    const int begin = max(slot0 - own, 0), end = min(slot1 - own, chunks);
     float* state = a.s_ptrs[b];
-    if (state == nullptr || first >= last) return;
+    if (state == nullptr || begin >= end) return;
     state += static_cast<long long>(h) * kD * kD;
-    const int chunks = (last - first + kChunk - 1) / kChunk;
-    constexpr int es = BF16 ? 2 : 4;
-    const long long slot0 = (static_cast<long long>(first / kChunk) + b) * a.H + h;
+    blocks += static_cast<long long>(own - slot0) * a.H + h;
 
-    if (wave >= 4) {
-        const int x = tid - 256, rg = x & 7, cg = x >> 3;
-        Patch<BF16> pq, pk, pg;
-        ChunkScale sc{};
-        const auto fetch = [&](int i) {
-            const int t0 = first + i * kChunk, n = last - t0;
-            if (OUT) load_patch<BF16>(pq, rows_of(a.q, es, t0, n, a.H, h), 4 * rg, 4 * cg);
-            load_patch<BF16>(pk, rows_of(a.k, es, t0, n, a.H, h), 4 * rg, 4 * cg);
-            load_patch<BF16>(pg, rows_of(a.g, es, t0, n, a.H, h), 4 * rg, 4 * cg);
-            sc = scales[slot0 + static_cast<long long>(i) * a.H];
-        };
-        float k[4][4], q[4][4], pre[4][4], suf[4][4], keep[4];
-        float sk = 1.f, sq = 1.f;
-        // the next chunk's decays, and the loads of the one behind it
-        const auto decays = [&](int next) {
-            float d[4][4];
-            patch_values<BF16>(pg, d);
-            patch_values<BF16>(pk, k);
-            if (OUT) patch_values<BF16>(pq, q);
-            sk = sc.k;
-            sq = sc.q;
-            if (next < chunks) fetch(next);
-#pragma unroll
-            for (int c = 0; c < 4; ++c) {
-#pragma unroll
-                for (int i = 0; i < 4; ++i) d[i][c] = decay(d[i][c]);
-                pre[0][c] = d[0][c];
-#pragma unroll
-                for (int i = 1; i < 4; ++i) pre[i][c] = pre[i - 1][c] * d[i][c];
-                suf[3][c] = 1.f;
-#pragma unroll
-                for (int i = 2; i >= 0; --i) suf[i][c] = suf[i + 1][c] * d[i + 1][c];
-                // products over the row groups before and behind this one
-                float up = pre[3][c], down = pre[3][c];
-#pragma unroll
-                for (int s = 1; s < 8; s <<= 1) {
-                    const float y = __shfl_up(up, s), z = __shfl_down(down, s);
-                    if (rg >= s) up *= y;
-                    if (rg + s < 8) down *= z;
-                }
-                float before = __shfl_up(up, 1), behind = __shfl_down(down, 1);
-                if (rg == 0) before = 1.f;
-                if (rg == 7) behind = 1.f;
-                keep[c] = up;
-#pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    pre[i][c] *= before;
-                    suf[i][c] *= behind;
-                }
-            }
-        };
-        const auto stage = [&](KdaTile& T) {
-            if (rg == 7) *reinterpret_cast<float4*>(&T.keep[4 * cg]) = make_float4(keep[0], keep[1], keep[2], keep[3]);
-            uint2 w[4][2];
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                float y[4];
-#pragma unroll
-                for (int c = 0; c < 4; ++c) y[c] = k[i][c] * pre[i][c] * sk;
-                halves4(y, w[i]);
-            }
-            store_rows<2>(T.k, cg, rg, w);
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                float y[4];
-#pragma unroll
-                for (int c = 0; c < 4; ++c) y[c] = k[i][c] * suf[i][c] * sk;
-                halves4(y, w[i]);
-            }
-            store_columns<2>(T.kt, cg, 8 * (rg & 3) + 4 * (rg >> 2), w);
-            if (OUT) {
-#pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    float y[4];
-#pragma unroll
-                    for (int c = 0; c < 4; ++c) y[c] = q[i][c] * pre[i][c] * sq;
-                    halves4(y, w[i]);
-                }
-                store_rows<2>(T.q, cg, rg, w);
-            }
-        };
-        fetch(0);
-        decays(1);
-        stage(tiles[0]);
-        for (int i = 0; i < chunks; ++i) {
-            __syncthreads();
-            if (i + 1 < chunks) decays(i + 2);
-            __syncthreads();
-            if (i + 1 < chunks) stage(tiles[(i + 1) & 1]);
-        }
-        return;
-    }
-
-    const int half = wave >> 1, col = kKdaCols * slice + 16 * (wave & 1) + l16;
+    const int half = wave / NC, partner = (wave + NC) % (2 * NC), col = 16 * (NC * slice + wave % NC) + l16;
     f32x4 S[4];
     float smax = 0.f;
 #pragma unroll
-    for (int m = 0; m < 4; ++m)
+    for (int m = 0; m < 4; ++m) {
 #pragma unroll
-        for (int r = 0; r < 4; ++r) {
-            S[m][r] = state[(64 * half + 16 * m + 4 * g4 + r) * kD + col];
-            smax = fmaxf(smax, fabsf(S[m][r]));
-        }
-    uint4 mf[2][2], bf[2];
+        for (int r = 0; r < 4; ++r) S[m][r] = state[(64 * half + 16 * m + 4 * g4 + r) * kD + col];
+        smax = abs_max(S[m], smax);
+    }
+    u32x4 next[copies];
     uint32_t v[2][4];
-    ChunkScale sc{};
     const auto fetch = [&](int i) {
-        const long long at = slot0 + static_cast<long long>(i) * a.H;
-        const uint4* p = reinterpret_cast<const uint4*>(pairs + at * kPairBytes);
+        const u32x4* p = reinterpret_cast<const u32x4*>(blocks + static_cast<long long>(i) * a.H);
 #pragma unroll
-        for (int s = 0; s < 2; ++s) {
-#pragma unroll
-            for (int tb = 0; tb < 2; ++tb) mf[tb][s] = p[(s * kChunk + 16 * tb + l16) * 4 + g4];
-            if (OUT) bf[s] = p[((2 + s) * kChunk + 16 * half + l16) * 4 + g4];
-        }
-        sc = scales[at];
-        if (half == 0) {
-            const int t0 = first + i * kChunk;
-            const Rows rv = rows_of(a.v, es, t0, last - t0, a.H, h);
-#pragma unroll
-            for (int tb = 0; tb < 2; ++tb)
-#pragma unroll
-                for (int r = 0; r < 4; ++r) v[tb][r] = load_raw<BF16>(rv, 16 * tb + 4 * g4 + r, col);
-        }
+        for (int x = 0; x < copies; ++x) next[x] = p[min(x * threads + tid, pieces - 1)];
     };
-    fetch(0);
+    const auto fetch_v = [&](int i) {
+        const int t0 = first + i * kChunk;
+        const Rows rv = rows_of(a.v, es, t0, last - t0, a.H, h);
+#pragma unroll
+        for (int tb = 0; tb < 2; ++tb)
+#pragma unroll
+            for (int r = 0; r < 4; ++r) v[tb][r] = load_raw<BF16>(rv, 16 * tb + 4 * g4 + r, col);
+    };
+    const auto store = [&](KdaBlock& T) {
+        u32x4* p = reinterpret_cast<u32x4*>(&T);
+#pragma unroll
+        for (int x = 0; x < copies; ++x)
+            if ((x + 1) * threads <= pieces || x * threads + tid < pieces) p[x * threads + tid] = next[x];
+    };
+    fetch(begin);
+    if (half == 0) fetch_v(begin);
+    store(tiles[0]);
 
-    for (int i = 0; i < chunks; ++i) {
-        const KdaTile& T = tiles[i & 1];
+    for (int i = begin; i < end; ++i) {
+        const KdaBlock& T = tiles[(i - begin) & 1];
         const float ss = scale_of(column_max(smax));
-        const float sk = inverse_of(sc.k), sq = inverse_of(sc.q), si = inverse_of(ss);
         uint4 sf[2][2];
 #pragma unroll
         for (int ks = 0; ks < 2; ++ks) halves8(S[2 * ks], S[2 * ks + 1], ss, sf[ks]);
         __syncthreads();
+        if (i + 1 < end) fetch(i + 1);
+        uint4 kf[2][2][2], qf[2][2][2];
+#pragma unroll
+        for (int ks = 0; ks < 2; ++ks)
+#pragma unroll
+            for (int tb = 0; tb < 2; ++tb)
+#pragma unroll
+                for (int w = 0; w < 2; ++w) {
+                    kf[ks][tb][w] = T.k[tb][2 * half + ks][w][lane];
+                    if (OUT) qf[ks][tb][w] = T.q[tb][2 * half + ks][w][lane];
+                }
+        const ChunkScale sc = T.scale;
+        // what undoes the scales; a product that leaves f32 only does so where
+        // the value itself would
+        const float sk = inverse_of(sc.k), si = inverse_of(ss), rs = -sk * si, qs = inverse_of(sc.q) * si;
         f32x4 R[2], Q[2];
 #pragma unroll
         for (int tb = 0; tb < 2; ++tb) R[tb] = Q[tb] = f32x4{0.f, 0.f, 0.f, 0.f};
 #pragma unroll
         for (int ks = 0; ks < 2; ++ks)
 #pragma unroll
-            for (int tb = 0; tb < 2; ++tb) {
-                uint4 f[2];
-                read_rows<2>(T.k, 16 * tb + l16, 64 * half + 32 * ks + 8 * g4, f);
-                R[tb] = product16(f, sf[ks], R[tb]);
-                if (OUT) {
-                    read_rows<2>(T.q, 16 * tb + l16, 64 * half + 32 * ks + 8 * g4, f);
-                    Q[tb] = product16(f, sf[ks], Q[tb]);
-                }
-            }
+            for (int tb = 0; tb < 2; ++tb) R[tb] = product16(kf[ks][tb], sf[ks], R[tb]);
+        if (OUT)
+#pragma unroll
+            for (int ks = 0; ks < 2; ++ks)
+#pragma unroll
+                for (int tb = 0; tb < 2; ++tb) Q[tb] = product16(qf[ks][tb], sf[ks], Q[tb]);
 #pragma unroll
         for (int tb = 0; tb < 2; ++tb) {
-            R[tb] = R[tb] * sk * si;
-            if (half == 0)
 #pragma unroll
-                for (int r = 0; r < 4; ++r) R[tb][r] -= element<BF16>(v[tb][r]);
+            for (int r = 0; r < 4; ++r) R[tb][r] = fmaf(R[tb][r], rs, half == 0 ? element<BF16>(v[tb][r]) : 0.f);
             xr[wave][tb][lane] = R[tb];
-            Q[tb] = Q[tb] * sq * si;
+            if (OUT) Q[tb] *= qs;
         }
         if (OUT) xo[wave][lane] = half == 0 ? Q[1] : Q[0];
+        if (half == 0 && i + 1 < end) fetch_v(i + 1);
         __syncthreads();
+        uint4 mf[2][2], bf[2], tf[4][2];
+        f32x4 keep[4];
         float rmax = 0.f;
 #pragma unroll
         for (int tb = 0; tb < 2; ++tb) {
-            R[tb] = -(R[tb] + xr[wave ^ 2][tb][lane]);
+            R[tb] += xr[partner][tb][lane];
+            rmax = abs_max(R[tb], rmax);
 #pragma unroll
-            for (int r = 0; r < 4; ++r) rmax = fmaxf(rmax, fabsf(R[tb][r]));
+            for (int w = 0; w < 2; ++w) mf[tb][w] = T.m[tb][w][lane];
         }
-        const float sr = scale_of(column_max(rmax)), sm = inverse_of(sc.m);
+        if (OUT)
+#pragma unroll
+            for (int w = 0; w < 2; ++w) bf[w] = T.b[half][w][lane];
+#pragma unroll
+        for (int m = 0; m < 4; ++m) {
+#pragma unroll
+            for (int w = 0; w < 2; ++w) tf[m][w] = T.kt[4 * half + m][w][lane];
+            keep[m] = *reinterpret_cast<const f32x4*>(&T.keep[64 * half + 16 * m + 4 * g4]);
+        }
+        const float sr = scale_of(column_max(rmax));
         uint4 rf[2], ef[2];
         halves8(R[0], R[1], sr, rf);
-        f32x4 E[2];
+        f32x4 E[2];    // the deltas, scaled as M and R are
         float emax = 0.f;
 #pragma unroll
         for (int tb = 0; tb < 2; ++tb) {
-            E[tb] = product16(mf[tb], rf, f32x4{0.f, 0.f, 0.f, 0.f}) * sm * inverse_of(sr);
-#pragma unroll
-            for (int r = 0; r < 4; ++r) emax = fmaxf(emax, fabsf(E[tb][r]));
+            E[tb] = product16(mf[tb], rf, f32x4{0.f, 0.f, 0.f, 0.f});
+            emax = abs_max(E[tb], emax);
         }
-        const float se = scale_of(column_max(emax)), ei = inverse_of(se);
+        const float se = scale_of(column_max(emax));
+        const float ei = inverse_of(sc.m) * inverse_of(sr) * inverse_of(se);
         halves8(E[0], E[1], se, ef);
+        const float ke = sk * ei;
+        smax = 0.f;
+#pragma unroll
+        for (int m = 0; m < 4; ++m) {
+            const f32x4 y = product16(tf[m], ef, f32x4{0.f, 0.f, 0.f, 0.f});
+#pragma unroll
+            for (int r = 0; r < 4; ++r) S[m][r] = fmaf(y[r], ke, S[m][r] * keep[m][r]);
+            smax = abs_max(S[m], smax);
+        }
         if (OUT) {
             f32x4 O = half == 0 ? Q[0] : Q[1];
-            O = O + xo[wave ^ 2][lane] + product16(bf, ef, f32x4{0.f, 0.f, 0.f, 0.f}) * inverse_of(sc.b) * ei;
+            O += xo[partner][lane];
+            const f32x4 y = product16(bf, ef, f32x4{0.f, 0.f, 0.f, 0.f});
+            const float bs = inverse_of(sc.b) * ei;
             const int t0 = first + i * kChunk;
             const Rows ro = rows_of(a.o, 4, t0, last - t0, a.H, h);
 #pragma unroll
             for (int r = 0; r < 4; ++r)
-                __builtin_amdgcn_raw_buffer_store_b32(bits(O[r] * kScale), ro.buffer,
+                __builtin_amdgcn_raw_buffer_store_b32(bits(fmaf(y[r], bs, O[r]) * kScale), ro.buffer,
                                                       (16 * half + 4 * g4 + r) * ro.pitch + 4 * col, 0, 0);
         }
-        if (i + 1 < chunks) fetch(i + 1);
-        smax = 0.f;
-#pragma unroll
-        for (int m = 0; m < 4; ++m) {
-            const int c = 64 * half + 16 * m;
-            uint4 kf[2];
-            read_columns<2, kD>(T.kt, c + l16, 8 * g4, kf);
-            const f32x4 keep = *reinterpret_cast<const f32x4*>(&T.keep[c + 4 * g4]);
-            S[m] = S[m] * keep + product16(kf, ef, f32x4{0.f, 0.f, 0.f, 0.f}) * sk * ei;
-#pragma unroll
-            for (int r = 0; r < 4; ++r) smax = fmaxf(smax, fabsf(S[m][r]));
-        }
+        if (i + 1 < end) store(tiles[(i + 1 - begin) & 1]);
     }
 #pragma unroll
     for (int m = 0; m < 4; ++m)
@@ -1182,24 +1216,44 @@ long long linear_work_bytes(int R, int B, int H) {
     return part_slots(R, B, 512) * H * (kD * kD * 4ll + 8);
 }
 
+// The prepared chunks of a call, or of as many slots as fit kWorkCap: longer
+// calls go through the workspace in turns.
+constexpr long long kWorkCap = 2ll << 30;
+
 long long prompt_work_bytes(int R, int B, int H) {
-    return part_slots(R, B, kChunk) * H * (kPairBytes + static_cast<long long>(sizeof(ChunkScale)));
+    const long long row = static_cast<long long>(H) * sizeof(KdaBlock), all = part_slots(R, B, kChunk) * row;
+    const long long most = kWorkCap > row ? kWorkCap : row;
+    return all < most ? all : most;
+}
+
+template <bool BF16, int NC>
+static void launch_chunks(const PromptArgs& a, const KdaBlock* blocks, int slot0, int slot1, hipStream_t stream) {
+    const unsigned turns = static_cast<unsigned>((static_cast<long long>(a.B) * a.H + 7) / 8);
+    const dim3 grid(turns * 8 * (8 / NC));
+    if (a.o)
+        kda_chunk_kernel<BF16, true, NC><<<grid, dim3(128 * NC), 0, stream>>>(a, blocks, slot0, slot1);
+    else
+        kda_chunk_kernel<BF16, false, NC><<<grid, dim3(128 * NC), 0, stream>>>(a, blocks, slot0, slot1);
 }
 
 template <bool BF16>
 static hipError_t launch_kda(const PromptArgs& a, hipStream_t stream) {
-    const long long pairs = part_slots(a.R, a.B, kChunk) * a.H;
-    const long long blocks = static_cast<long long>(a.B) * a.H * (kD / kKdaCols);
-    if (pairs > 0x7FFFFFFFll || blocks > 0x7FFFFFFFll) return hipErrorInvalidValue;
-    char* const words = static_cast<char*>(a.work);
-    ChunkScale* const scales = reinterpret_cast<ChunkScale*>(words + pairs * kPairBytes);
-    kda_pair_kernel<BF16><<<dim3(static_cast<unsigned>(pairs)), dim3(256), 0, stream>>>(a, words, scales);
-    const dim3 grid(static_cast<unsigned>(blocks));
-    if (a.o)
-        kda_chunk_kernel<BF16, true><<<grid, dim3(512), 0, stream>>>(a, words, scales);
-    else
-        kda_chunk_kernel<BF16, false><<<grid, dim3(512), 0, stream>>>(a, words, scales);
-    return hipGetLastError();
+    const long long slots = part_slots(a.R, a.B, kChunk), heads = static_cast<long long>(a.B) * a.H;
+    const long long turn = prompt_work_bytes(a.R, a.B, a.H) / (static_cast<long long>(a.H) * sizeof(KdaBlock));
+    KdaBlock* const blocks = static_cast<KdaBlock*>(a.work);
+    for (long long s0 = 0; s0 < slots; s0 += turn) {
+        const int slot0 = static_cast<int>(s0), slot1 = static_cast<int>(s0 + turn < slots ? s0 + turn : slots);
+        kda_prepare_kernel<BF16><<<dim3(static_cast<unsigned>((slot1 - slot0) * static_cast<long long>(a.H))),
+                                   dim3(256), 0, stream>>>(a, blocks, slot0);
+        // few (sequence, head) pairs: fewer columns a workgroup, more workgroups
+        if (heads > 64)
+            launch_chunks<BF16, 4>(a, blocks, slot0, slot1, stream);
+        else
+            launch_chunks<BF16, 2>(a, blocks, slot0, slot1, stream);
+        const hipError_t e = hipGetLastError();
+        if (e != hipSuccess) return e;
+    }
+    return hipSuccess;
 }
 
 hipError_t launch_prompt(const PromptArgs& a, bool bf16, hipStream_t stream) {
