@@ -3,126 +3,386 @@
 //
 // With m = max x, z = sum exp(x - m), y = x - m:
 //   lp = y[token] - log z,   entropy = log z - (sum exp(y) y) / z
-// and the top n by (value, lowest index first).  One workgroup a row: a pass
-// for m, one for the sums, one pass for each alternative.
+// and the top n by (value, lowest index first).
+//
+// One pass over the logits.  A lane carries its own running m, z and
+// w = sum exp(y) y, moved to the new maximum once a 16-byte load; a wave keeps
+// the best n keys it has seen, sorted, one a lane.  A step of the wave costs
+// the list one compare a lane while nothing beats its last entry (a wave's
+// steps rise in index, so an equal value never does); what does is inserted by
+// a ballot for its place and a shift of the lanes behind it.
+//
+// Few rows are split over workgroups, whose waves leave their sums and lists
+// in the workspace for a second launch; many rows take a workgroup each, which
+// joins its waves through LDS.  The join takes, of W sorted lists, those whose
+// head is among the n best heads, and ranks what is left by counting.  Keys
+// are unique, so neither the order of the lists nor the positions that the
+// candidates take change the result; sums are joined in a fixed order.
 
 #include <hip/hip_runtime.h>
 
 #include <cstdint>
 
+#include "kda.h"
 #include "kda_launch.h"
 #include "kda_ops.h"
 
 namespace kda {
 namespace {
 
-template <bool BF16>
-__device__ __forceinline__ float logit(const void* row, int i) {
-    if constexpr (BF16) {
-        const uint32_t b = static_cast<const uint16_t*>(row)[i];
-        return __builtin_bit_cast(float, b << 16);
-    } else {
-        return static_cast<const float*>(row)[i];
-    }
-}
+constexpr float kLog2e = 1.44269504088896340736f;
+constexpr float kInf = __builtin_inff();
+constexpr int kSplitThreads = 256;    // workgroup of a split row
+constexpr int kRowThreads = 512;      // workgroup of a whole row
+constexpr int kMaxSplits = 64;        // workgroups of a row, at most
+constexpr int kMaxLists = kMaxSplits * (kSplitThreads / 64);
 
-// Keys order as (value, then lowest index): greater is better, -0 equals +0.
-__device__ __forceinline__ uint64_t key_of(float x, int i) {
+using Key = unsigned long long;       // ordered value, then ~index: greater is better, 0 is none
+
+// The value's bits in the order of the values, -0 as +0.
+__device__ __forceinline__ uint32_t ordered(float x) {
     const uint32_t b = __builtin_bit_cast(uint32_t, x + 0.f);
-    const uint32_t o = b ^ (static_cast<uint32_t>(static_cast<int32_t>(b) >> 31) | 0x80000000u);
-    return static_cast<uint64_t>(o) << 32 | ~static_cast<uint32_t>(i);
+    return b ^ (static_cast<uint32_t>(static_cast<int32_t>(b) >> 31) | 0x80000000u);
 }
 
-constexpr int kThreads = 1024;
-
-template <typename T, typename F>
-__device__ __forceinline__ T block_reduce(T x, T* part, F f) {
-#pragma unroll
-    for (int m = 32; m >= 1; m >>= 1) x = f(x, static_cast<T>(__shfl_xor(x, m)));
-    __syncthreads();
-    if ((threadIdx.x & 63) == 0) part[threadIdx.x >> 6] = x;
-    __syncthreads();
-    x = part[0];
-#pragma unroll
-    for (int w = 1; w < kThreads / 64; ++w) x = f(x, part[w]);
-    return x;
+__device__ __forceinline__ float value_of(Key k) {
+    const uint32_t o = static_cast<uint32_t>(k >> 32);
+    return __builtin_bit_cast(float, o & 0x80000000u ? o ^ 0x80000000u : ~o);
 }
 
-template <bool BF16>
-__global__ void __launch_bounds__(kThreads) logprob_row_kernel(LogprobArgs a) {
-    __shared__ float pf[kThreads / 64];
-    __shared__ unsigned long long pk[kThreads / 64];
-    const int tid = threadIdx.x;
-    const long long r = blockIdx.x;
-    const void* row = static_cast<const char*>(a.logits) + r * a.ld * (BF16 ? 2 : 4);
-    const float inf = __builtin_inff(), nan = __builtin_nanf("");
+// Sums of a part of a row, relative to m.  A NaN in z says that the part holds
+// a NaN or +inf.
+struct Sums {
+    float m, z, w;
+};
 
-    float m = -inf;
-    bool bad = false;   // a NaN or +inf: no distribution
-    for (int i = tid; i < a.V; i += kThreads) {
-        const float x = logit<BF16>(row, i);
-        bad |= !(x < inf);
-        m = fmaxf(m, x);
+__device__ __forceinline__ float exp_of(float y) { return __builtin_amdgcn_exp2f(y * kLog2e); }
+
+// Moves s to a maximum m >= s.m.
+__device__ __forceinline__ void move_to(Sums& s, float m) {
+    // (held above -1e30, whose exponential is 0 as well, so that z d stays finite)
+    const float d = s.m == -kInf || s.m == m ? 0.f : fmaxf(s.m - m, -1e30f);
+    const float c = s.m == -kInf ? 0.f : exp_of(d);
+    s.w = c * fmaf(s.z, d, s.w);
+    s.z *= c;
+    s.m = m;
+}
+
+__device__ __forceinline__ void join(Sums& a, Sums b) {
+    const bool bad = a.z != a.z || b.z != b.z;
+    const float m = fmaxf(a.m, b.m);
+    move_to(a, m);
+    move_to(b, m);
+    a.z = bad ? __builtin_nanf("") : a.z + b.z;
+    a.w += b.w;
+}
+
+// The best n keys of a wave, best first, key i in lane i.
+struct List {
+    Key mine;
+    float bar;    // a value has to be above it to enter
+    Key last;     // the n-th key
+};
+
+__device__ __forceinline__ Key lane_key(Key k, int lane) {
+    return static_cast<Key>(static_cast<uint32_t>(__builtin_amdgcn_readlane(static_cast<int>(k >> 32), lane))) << 32 |
+           static_cast<uint32_t>(__builtin_amdgcn_readlane(static_cast<int>(k), lane));
+}
+
+__device__ __forceinline__ void insert(List& l, Key k, int n) {
+    const int lane = threadIdx.x & 63;
+    const int at = __builtin_popcountll(__ballot(l.mine > k));
+    // the key of the lane before (wave_shr:1)
+    const Key up = static_cast<Key>(static_cast<uint32_t>(__builtin_amdgcn_update_dpp(
+                       0, static_cast<int>(l.mine >> 32), 0x138, 0xF, 0xF, true))) << 32 |
+                   static_cast<uint32_t>(__builtin_amdgcn_update_dpp(0, static_cast<int>(l.mine), 0x138, 0xF, 0xF, true));
+    l.mine = lane < at ? l.mine : lane == at ? k : up;
+    l.last = lane_key(l.mine, n - 1);
+}
+
+// Takes the lanes' values x, of index i each.
+__device__ __forceinline__ void offer(List& l, float x, uint32_t i, int n) {
+    const Key k = x > -kInf ? static_cast<Key>(ordered(x)) << 32 | static_cast<uint32_t>(~i) : 0;
+    uint64_t mask = __ballot(k > l.last);
+    while (mask) {
+        insert(l, lane_key(k, __builtin_ctzll(mask)), n);
+        mask &= mask - 1;
+        mask &= __ballot(k > l.last);
     }
-    bad = __syncthreads_or(bad);
-    m = block_reduce(m, pf, [](float x, float y) { return fmaxf(x, y); });
-    const bool empty = m == -inf;
-    float z = 0.f, w = 0.f;
-    if (!bad && !empty) {
-        for (int i = tid; i < a.V; i += kThreads) {
-            const float y = logit<BF16>(row, i) - m;
-            const float p = expf(y);
-            z += p;
-            if (p > 0.f) w = fmaf(p, y, w);
+    l.bar = l.last == 0 ? -kInf : value_of(l.last);
+}
+
+// E values of a lane, whose indexes follow each other from i.
+template <int E, bool TOP>
+__device__ __forceinline__ void take(Sums& s, List& l, const float (&x)[E], uint32_t i, int n) {
+    float top = x[0];
+#pragma unroll
+    for (int e = 1; e < E; ++e) top = fmaxf(top, x[e]);
+    const float m = fmaxf(s.m, top);
+    move_to(s, m);
+    const float base = m == -kInf ? 0.f : m;
+#pragma unroll
+    for (int e = 0; e < E; ++e) {
+        const float y = x[e] - base;
+        const float p = exp_of(y);
+        s.z += p;
+        s.w = fmaf(p, fmaxf(y, -1e30f), s.w);
+    }
+    if constexpr (TOP) {
+        if (__ballot(top > l.bar)) {
+#pragma unroll
+            for (int e = 0; e < E; ++e) offer(l, x[e], i + e, n);
         }
     }
-    const auto add = [](float x, float y) { return x + y; };
-    z = block_reduce(z, pf, add);
-    w = block_reduce(w, pf, add);
-    const float log_z = logf(z);
+}
+
+template <bool BF16>
+__device__ __forceinline__ float logit(const void* row, long long i) {
+    if constexpr (BF16)
+        return __builtin_bit_cast(float, static_cast<uint32_t>(static_cast<const uint16_t*>(row)[i]) << 16);
+    else
+        return static_cast<const float*>(row)[i];
+}
+
+template <bool BF16>
+__device__ __forceinline__ void values(uint4 u, float (&x)[BF16 ? 8 : 4]) {
+    const uint32_t w[4] = {u.x, u.y, u.z, u.w};
+    if constexpr (BF16) {
+#pragma unroll
+        for (int e = 0; e < 8; ++e) x[e] = __builtin_bit_cast(float, e & 1 ? w[e >> 1] & 0xFFFF0000u : w[e >> 1] << 16);
+    } else {
+#pragma unroll
+        for (int e = 0; e < 4; ++e) x[e] = __builtin_bit_cast(float, w[e]);
+    }
+}
+
+__device__ __forceinline__ Sums wave_sums(Sums s) {
+#pragma unroll
+    for (int d = 32; d >= 1; d >>= 1)
+        join(s, Sums{__shfl_xor(s.m, d), __shfl_xor(s.z, d), __shfl_xor(s.w, d)});
+    return s;
+}
+
+// Part `part` of `parts` of a row, by one workgroup: the wave's sums (all lanes
+// alike) and list.  The row is read from its first 16-byte boundary on in whole
+// loads, four a lane in flight; what lies before and behind goes to one wave.
+template <bool BF16, bool TOP, int THREADS>
+__device__ __forceinline__ void read_part(const LogprobArgs& a, const void* row, int part, int parts, Sums& s, List& l) {
+    constexpr int E = BF16 ? 8 : 4, U = 4;
+    const int tid = threadIdx.x, lane = tid & 63;
+    const bool first = tid < 64;
+    const uintptr_t at = reinterpret_cast<uintptr_t>(row);
+    const int head = min(a.V, static_cast<int>((16 - (at & 15)) & 15) / (BF16 ? 2 : 4));
+    const int vectors = (a.V - head) / E;
+    const int tail = a.V - head - vectors * E;
+    const int each = (vectors + parts - 1) / parts;
+    const int begin = min(part * each, vectors), end = min(begin + each, vectors);
+    const uint4* body = reinterpret_cast<const uint4*>(static_cast<const char*>(row) + head * (BF16 ? 2 : 4));
+    s = Sums{-kInf, 0.f, 0.f};
+    l = List{0, -kInf, 0};
+    if (first && part == 0 && head > 0) {
+        const float x[1] = {lane < head ? logit<BF16>(row, lane) : -kInf};
+        take<1, TOP>(s, l, x, lane, a.n_top);
+    }
+    const uint32_t low = BF16 ? 0xFF80FF80u : 0xFF800000u;   // -inf
+    for (int v0 = begin; v0 < end; v0 += U * THREADS) {
+        uint4 u[U];
+#pragma unroll
+        for (int i = 0; i < U; ++i) {
+            const int v = v0 + i * THREADS + tid;
+            u[i] = v < end ? body[v] : make_uint4(low, low, low, low);
+        }
+#pragma unroll
+        for (int i = 0; i < U; ++i) {
+            const int v = v0 + i * THREADS;
+            if (v + (tid & ~63) >= end) break;
+            float x[E];
+            values<BF16>(u[i], x);
+            take<E, TOP>(s, l, x, head + (v + tid) * E, a.n_top);
+        }
+    }
+    if (first && part == parts - 1 && tail > 0) {
+        const int i = a.V - tail + lane;
+        const float x[1] = {lane < tail ? logit<BF16>(row, i) : -kInf};
+        take<1, TOP>(s, l, x, i, a.n_top);
+    }
+    s = wave_sums(s);
+}
+
+// Joins W lists and their sums to the outputs of row r.  sums and lists: W
+// entries and W * n_top keys; THREADS >= W or W <= THREADS / 64 * 64.
+template <bool BF16, int THREADS>
+__device__ __forceinline__ void finish(const LogprobArgs& a, const void* row, long long r, int W, const Sums* sums,
+                                       const Key* lists) {
+    __shared__ Sums waves[THREADS / 64];
+    __shared__ Key heads[THREADS], found[KDA_TOP_MAX * KDA_TOP_MAX];
+    __shared__ Key bar;
+    __shared__ int count;
+    const int tid = threadIdx.x, n = a.n_top;
+    Sums s{-kInf, 0.f, 0.f};
+    Key head = 0;
+    if (tid < W) {
+        s = sums[tid];
+        if (n > 0) head = lists[tid * n];
+    }
+    s = wave_sums(s);
+    if ((tid & 63) == 0) waves[tid >> 6] = s;
+    heads[tid] = head;
+    if (tid == 0) {
+        count = 0;
+        bar = 1;
+    }
+    __syncthreads();
+    s = waves[0];
+#pragma unroll
+    for (int w = 1; w < THREADS / 64; ++w) join(s, waves[w]);
+    const bool bad = s.z != s.z, empty = s.m == -kInf;
+    const float log_z = logf(s.z);
     if (tid == 0) {
         if (a.lp) {
             const uint32_t tok = a.tokens[r];
-            float lp = nan;
+            float lp = __builtin_nanf("");
             if (!bad && tok < static_cast<uint32_t>(a.V))
-                lp = empty ? -inf : logit<BF16>(row, static_cast<int>(tok)) - m - log_z;
+                lp = empty ? -kInf : logit<BF16>(row, tok) - s.m - log_z;
             a.lp[r] = lp;
         }
-        if (a.entropy) a.entropy[r] = bad ? nan : empty ? 0.f : log_z - w / z;
+        if (a.entropy) a.entropy[r] = bad ? __builtin_nanf("") : empty ? 0.f : log_z - s.w / s.z;
     }
-    unsigned long long last = ~0ull;
-    for (int n = 0; n < a.n_top; ++n) {
-        unsigned long long best = 0;
-        if (!bad && !empty) {
-            for (int i = tid; i < a.V; i += kThreads) {
-                const float x = logit<BF16>(row, i);
-                const unsigned long long key = key_of(x, i);
-                if (x > -inf && key < last && key > best) best = key;
-            }
-        }
-        best = block_reduce(best, pk, [](unsigned long long x, unsigned long long y) { return x > y ? x : y; });
-        if (tid == 0) {
-            const uint32_t id = ~static_cast<uint32_t>(best);
-            const bool none = best == 0;
-            a.top_ids[r * a.n_top + n] = none ? kNoToken : id;
-            a.top_lp[r * a.n_top + n] =
-                bad ? nan : none ? -inf : logit<BF16>(row, static_cast<int>(id)) - m - log_z;
-        }
-        last = best;
+    if (n == 0) return;
+    // only keys at or above the n-th best head can be among the n best
+    if (W > n && head != 0) {
+        int rank = 0;
+        for (int i = 0; i < W; ++i) rank += heads[i] > head;
+        if (rank == n - 1) bar = head;
     }
+    __syncthreads();
+    if (tid < W && !bad) {
+        const Key least = bar;
+        for (int j = 0; j < n; ++j) {
+            const Key k = lists[tid * n + j];
+            if (k < least) break;
+            found[atomicAdd(&count, 1)] = k;
+        }
+    }
+    __syncthreads();
+    const int c = count;
+    for (int i = tid; i < c; i += THREADS) {
+        const Key k = found[i];
+        int rank = 0;
+        for (int j = 0; j < c; ++j) rank += found[j] > k;
+        if (rank < n) {
+            a.top_ids[r * n + rank] = ~static_cast<uint32_t>(k);
+            a.top_lp[r * n + rank] = value_of(k) - s.m - log_z;
+        }
+    }
+    for (int i = c + tid; i < n; i += THREADS) {
+        a.top_ids[r * n + i] = kNoToken;
+        a.top_lp[r * n + i] = bad ? __builtin_nanf("") : -kInf;
+    }
+}
+
+template <bool BF16>
+__device__ __forceinline__ const void* row_at(const LogprobArgs& a, long long r) {
+    return static_cast<const char*>(a.logits) + r * a.ld * (BF16 ? 2 : 4);
+}
+
+// A workgroup a row.
+template <bool BF16, bool TOP>
+__global__ void __launch_bounds__(kRowThreads) logprob_row_kernel(LogprobArgs a) {
+    constexpr int W = kRowThreads / 64;
+    __shared__ Sums sums[W];
+    __shared__ Key lists[TOP ? W * KDA_TOP_MAX : 1];
+    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+    const long long r = blockIdx.x;
+    const void* row = row_at<BF16>(a, r);
+    Sums s;
+    List l;
+    read_part<BF16, TOP, kRowThreads>(a, row, 0, 1, s, l);
+    if (lane == 0) sums[wave] = s;
+    if (TOP && lane < a.n_top) lists[wave * a.n_top + lane] = l.mine;
+    __syncthreads();
+    finish<BF16, kRowThreads>(a, row, r, W, sums, lists);
+}
+
+// Where the waves of split rows leave their results.
+struct Split {
+    Sums* sums;     // [t][W]
+    Key* lists;     // [t][W][n_top]
+    int parts;      // workgroups a row; W = parts * 4
+};
+
+template <bool BF16, bool TOP>
+__global__ void __launch_bounds__(kSplitThreads) logprob_part_kernel(LogprobArgs a, Split x) {
+    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+    const long long r = blockIdx.y;
+    Sums s;
+    List l;
+    read_part<BF16, TOP, kSplitThreads>(a, row_at<BF16>(a, r), blockIdx.x, x.parts, s, l);
+    const long long at = (r * x.parts + blockIdx.x) * (kSplitThreads / 64) + wave;
+    if (lane == 0) x.sums[at] = s;
+    if (TOP && lane < a.n_top) x.lists[at * a.n_top + lane] = l.mine;
+}
+
+template <bool BF16>
+__global__ void __launch_bounds__(kMaxLists) logprob_join_kernel(LogprobArgs a, Split x) {
+    const long long r = blockIdx.x;
+    const int W = x.parts * (kSplitThreads / 64);
+    finish<BF16, kMaxLists>(a, row_at<BF16>(a, r), r, W, x.sums + r * W, x.lists + r * W * a.n_top);
+}
+
+// Workgroups a row: 1 (a row each, joined in place) from 512 rows on, where
+// the rows alone fill the chip; below that enough for 1024 workgroups, but not
+// with less than four loads a lane.
+int parts_of(int t, int V, int es) {
+    if (t >= 512) return 1;
+    const long long loads = (static_cast<long long>(V) * es + 15) / 16;
+    long long p = (loads + 4 * kSplitThreads - 1) / (4 * kSplitThreads);
+    const long long fill = (1024 + t - 1) / t;
+    p = p < fill ? p : fill;
+    return static_cast<int>(p > kMaxSplits ? kMaxSplits : p);
+}
+
+long long split_bytes(int t, int parts, int n_top) {
+    if (parts == 1) return 0;
+    return static_cast<long long>(t) * parts * (kSplitThreads / 64) *
+           (static_cast<long long>(sizeof(Sums)) + 8ll * n_top);
+}
+
+template <bool BF16>
+hipError_t launch(const LogprobArgs& a, hipStream_t stream) {
+    Split x{};
+    x.parts = parts_of(a.t, a.V, BF16 ? 2 : 4);
+    const bool top = a.n_top > 0;
+    if (x.parts == 1) {
+        const dim3 grid(static_cast<unsigned>(a.t));
+        if (top)
+            logprob_row_kernel<BF16, true><<<grid, dim3(kRowThreads), 0, stream>>>(a);
+        else
+            logprob_row_kernel<BF16, false><<<grid, dim3(kRowThreads), 0, stream>>>(a);
+        return hipGetLastError();
+    }
+    // the keys first: they need 8-byte alignment
+    const long long lists = static_cast<long long>(a.t) * x.parts * (kSplitThreads / 64);
+    x.lists = static_cast<Key*>(a.work);
+    x.sums = reinterpret_cast<Sums*>(x.lists + lists * a.n_top);
+    const dim3 grid(static_cast<unsigned>(x.parts), static_cast<unsigned>(a.t));
+    if (top)
+        logprob_part_kernel<BF16, true><<<grid, dim3(kSplitThreads), 0, stream>>>(a, x);
+    else
+        logprob_part_kernel<BF16, false><<<grid, dim3(kSplitThreads), 0, stream>>>(a, x);
+    logprob_join_kernel<BF16><<<dim3(static_cast<unsigned>(a.t)), dim3(kMaxLists), 0, stream>>>(a, x);
+    return hipGetLastError();
 }
 
 }  // namespace
 
-long long logprob_work_bytes(int, int, int) { return 0; }
+long long logprob_work_bytes(int t, int V, int n_top) {
+    // f32 rows are the longer ones: never fewer parts than bf16 rows
+    return split_bytes(t, parts_of(t, V, 4), n_top);
+}
 
 hipError_t launch_logprobs(const LogprobArgs& a, bool bf16, hipStream_t stream) {
-    const dim3 grid(static_cast<unsigned>(a.t));
-    if (bf16)
-        logprob_row_kernel<true><<<grid, dim3(kThreads), 0, stream>>>(a);
-    else
-        logprob_row_kernel<false><<<grid, dim3(kThreads), 0, stream>>>(a);
-    return hipGetLastError();
+    return bf16 ? launch<true>(a, stream) : launch<false>(a, stream);
 }
 
 }  // namespace kda
