@@ -10,7 +10,8 @@
 // the best n keys it has seen, sorted, one a lane.  A step of the wave costs
 // the list one compare a lane while nothing beats its last entry (a wave's
 // steps rise in index, so an equal value never does); what does is inserted by
-// a ballot for its place and a shift of the lanes behind it.
+// a ballot for its place and a shift of the lanes behind it.  The first loads of
+// a wave fill its list at once.
 //
 // Few rows are split over workgroups, whose waves leave their sums and lists
 // in the workspace for a second launch; many rows take a workgroup each, which
@@ -32,8 +33,8 @@ namespace {
 
 constexpr float kLog2e = 1.44269504088896340736f;
 constexpr float kInf = __builtin_inff();
+constexpr float kSlack = 4.0f;
 constexpr int kSplitThreads = 256;    // workgroup of a split row
-constexpr int kRowThreads = 512;      // workgroup of a whole row
 constexpr int kMaxSplits = 64;        // workgroups of a row, at most
 constexpr int kMaxLists = kMaxSplits * (kSplitThreads / 64);
 
@@ -50,8 +51,9 @@ __device__ __forceinline__ float value_of(Key k) {
     return __builtin_bit_cast(float, o & 0x80000000u ? o ^ 0x80000000u : ~o);
 }
 
-// Sums of a part of a row, relative to m.  A NaN in z says that the part holds
-// a NaN or +inf.
+// Sums of a part of a row, relative to m, which no value exceeds by more than
+// kSlack (a move costs an exponential; e^4 costs the sums nothing).  A NaN in z
+// says that the part holds a NaN or +inf.
 struct Sums {
     float m, z, w;
 };
@@ -112,15 +114,63 @@ __device__ __forceinline__ void offer(List& l, float x, uint32_t i, int n) {
     l.bar = l.last == 0 ? -kInf : value_of(l.last);
 }
 
+// The list of a wave's first N values a lane, value e of index at(e).  Without
+// it each of the first hundreds of values would be inserted.  The n-th largest
+// of the lanes' maxima is found bit by bit; at least n values reach it, and few
+// more: they are gathered in LDS and ranked by counting.  More than 64 (many
+// equal values) are inserted one by one.  space: 64 keys of this wave's.
+template <int N, typename At>
+__device__ __forceinline__ void start(List& l, const float (&x)[N], At at, int n, volatile Key* space) {
+    const int lane = threadIdx.x & 63;
+    float top = x[0];
+#pragma unroll
+    for (int e = 1; e < N; ++e) top = fmaxf(top, x[e]);
+    const uint32_t o = ordered(top);
+    uint32_t t = 0;
+#pragma unroll
+    for (int bit = 31; bit >= 0; --bit) {
+        const uint32_t up = t | 1u << bit;
+        if (__builtin_popcountll(__ballot(o >= up)) >= n) t = up;
+    }
+    const float least = value_of(static_cast<Key>(t) << 32);
+    int c = 0;
+#pragma unroll
+    for (int e = 0; e < N; ++e) c += __builtin_popcountll(__ballot(x[e] >= least && x[e] > -kInf));
+    if (c > 64) {
+#pragma unroll
+        for (int e = 0; e < N; ++e) offer(l, x[e], at(e), n);
+        return;
+    }
+    int p = 0;
+#pragma unroll
+    for (int e = 0; e < N; ++e) {
+        const bool in = x[e] >= least && x[e] > -kInf;
+        const uint64_t mask = __ballot(in);
+        const int before = __builtin_amdgcn_mbcnt_hi(static_cast<uint32_t>(mask >> 32),
+                                                     __builtin_amdgcn_mbcnt_lo(static_cast<uint32_t>(mask), 0));
+        if (in) space[p + before] = static_cast<Key>(ordered(x[e])) << 32 | static_cast<uint32_t>(~at(e));
+        p += __builtin_popcountll(mask);
+    }
+    __builtin_amdgcn_wave_barrier();
+    Key k = lane < c ? space[lane] : 0;
+    int rank = 0;
+    for (int i = 0; i < c; ++i) rank += lane_key(k, i) > k;
+    if (lane < c) space[rank] = k;
+    __builtin_amdgcn_wave_barrier();
+    l.mine = lane < c ? space[lane] : 0;
+    l.last = lane_key(l.mine, n - 1);
+    l.bar = l.last == 0 ? -kInf : value_of(l.last);
+}
+
 // E values of a lane, whose indexes follow each other from i.
 template <int E, bool TOP>
 __device__ __forceinline__ void take(Sums& s, List& l, const float (&x)[E], uint32_t i, int n) {
     float top = x[0];
 #pragma unroll
     for (int e = 1; e < E; ++e) top = fmaxf(top, x[e]);
-    const float m = fmaxf(s.m, top);
-    move_to(s, m);
-    const float base = m == -kInf ? 0.f : m;
+    // m need not be the maximum: it follows once a value is well above it
+    if (__ballot(top > s.m + kSlack || s.m == -kInf)) move_to(s, fmaxf(s.m, top));
+    const float base = s.m == -kInf ? 0.f : s.m;
 #pragma unroll
     for (int e = 0; e < E; ++e) {
         const float y = x[e] - base;
@@ -166,9 +216,10 @@ __device__ __forceinline__ Sums wave_sums(Sums s) {
 // Part `part` of `parts` of a row, by one workgroup: the wave's sums (all lanes
 // alike) and list.  The row is read from its first 16-byte boundary on in whole
 // loads, four a lane in flight; what lies before and behind goes to one wave.
-template <bool BF16, bool TOP, int THREADS>
+// FILL of a lane's first loads fill the list.
+template <bool BF16, bool TOP, int THREADS, int LOADS, int FILL>
 __device__ __forceinline__ void read_part(const LogprobArgs& a, const void* row, int part, int parts, Sums& s, List& l) {
-    constexpr int E = BF16 ? 8 : 4, U = 4;
+    constexpr int E = BF16 ? 8 : 4, U = LOADS;
     const int tid = threadIdx.x, lane = tid & 63;
     const bool first = tid < 64;
     const uintptr_t at = reinterpret_cast<uintptr_t>(row);
@@ -180,17 +231,52 @@ __device__ __forceinline__ void read_part(const LogprobArgs& a, const void* row,
     const uint4* body = reinterpret_cast<const uint4*>(static_cast<const char*>(row) + head * (BF16 ? 2 : 4));
     s = Sums{-kInf, 0.f, 0.f};
     l = List{0, -kInf, 0};
-    if (first && part == 0 && head > 0) {
-        const float x[1] = {lane < head ? logit<BF16>(row, lane) : -kInf};
-        take<1, TOP>(s, l, x, lane, a.n_top);
-    }
+    __shared__ Key space[TOP ? THREADS / 64 : 1][64];
+    const float x0[1] = {first && part == 0 && lane < head ? logit<BF16>(row, lane) : -kInf};
+    if (first && part == 0 && head > 0) take<1, false>(s, l, x0, lane, a.n_top);
     const uint32_t low = BF16 ? 0xFF80FF80u : 0xFF800000u;   // -inf
-    for (int v0 = begin; v0 < end; v0 += U * THREADS) {
-        uint4 u[U];
+    const auto fetch = [&](int v0, uint4 (&u)[U]) {
+        if (v0 + U * THREADS <= end) {
 #pragma unroll
-        for (int i = 0; i < U; ++i) {
-            const int v = v0 + i * THREADS + tid;
-            u[i] = v < end ? body[v] : make_uint4(low, low, low, low);
+            for (int i = 0; i < U; ++i) u[i] = body[v0 + i * THREADS + tid];
+        } else {
+#pragma unroll
+            for (int i = 0; i < U; ++i) {
+                const int v = v0 + i * THREADS + tid;
+                u[i] = v < end ? body[v] : make_uint4(low, low, low, low);
+            }
+        }
+    };
+    uint4 u[U], next[U];
+    if (begin < end) fetch(begin, next);
+    for (int v0 = begin; v0 < end; v0 += U * THREADS) {
+#pragma unroll
+        for (int i = 0; i < U; ++i) u[i] = next[i];
+        if (v0 + U * THREADS < end) fetch(v0 + U * THREADS, next);
+        if (TOP && v0 == begin) {
+            float x[FILL * E + 1];
+            x[FILL * E] = x0[0];
+#pragma unroll
+            for (int i = 0; i < FILL; ++i) {
+                float y[E];
+                values<BF16>(u[i], y);
+#pragma unroll
+                for (int e = 0; e < E; ++e) x[i * E + e] = y[e];
+            }
+            const auto at = [&](int e) {
+                return e == FILL * E ? lane : head + (v0 + e / E * THREADS + tid) * E + e % E;
+            };
+            start(l, x, at, a.n_top, space[tid >> 6]);
+#pragma unroll
+            for (int i = 0; i < U; ++i) {
+                float y[E];
+                values<BF16>(u[i], y);
+                if (i < FILL)
+                    take<E, false>(s, l, y, 0, 0);
+                else
+                    take<E, true>(s, l, y, head + (v0 + i * THREADS + tid) * E, a.n_top);
+            }
+            continue;
         }
 #pragma unroll
         for (int i = 0; i < U; ++i) {
@@ -201,6 +287,7 @@ __device__ __forceinline__ void read_part(const LogprobArgs& a, const void* row,
             take<E, TOP>(s, l, x, head + (v + tid) * E, a.n_top);
         }
     }
+    if (TOP && begin >= end && part == 0 && first) offer(l, x0[0], lane, a.n_top);   // no whole load
     if (first && part == parts - 1 && tail > 0) {
         const int i = a.V - tail + lane;
         const float x[1] = {lane < tail ? logit<BF16>(row, i) : -kInf};
@@ -210,8 +297,8 @@ __device__ __forceinline__ void read_part(const LogprobArgs& a, const void* row,
 }
 
 // Joins W lists and their sums to the outputs of row r.  sums and lists: W
-// entries and W * n_top keys; THREADS >= W or W <= THREADS / 64 * 64.
-template <bool BF16, int THREADS>
+// entries and W * n_top keys, W <= THREADS; AHEAD keys a thread are read at once.
+template <bool BF16, int THREADS, int AHEAD>
 __device__ __forceinline__ void finish(const LogprobArgs& a, const void* row, long long r, int W, const Sums* sums,
                                        const Key* lists) {
     __shared__ Sums waves[THREADS / 64];
@@ -221,6 +308,9 @@ __device__ __forceinline__ void finish(const LogprobArgs& a, const void* row, lo
     const int tid = threadIdx.x, n = a.n_top;
     Sums s{-kInf, 0.f, 0.f};
     Key head = 0;
+    Key ahead[AHEAD];
+#pragma unroll
+    for (int i = 0; i < AHEAD; ++i) ahead[i] = i * THREADS + tid < W * n ? lists[i * THREADS + tid] : 0;
     if (tid < W) {
         s = sums[tid];
         if (n > 0) head = lists[tid * n];
@@ -252,16 +342,19 @@ __device__ __forceinline__ void finish(const LogprobArgs& a, const void* row, lo
     // only keys at or above the n-th best head can be among the n best
     if (W > n && head != 0) {
         int rank = 0;
+#pragma unroll 8
         for (int i = 0; i < W; ++i) rank += heads[i] > head;
         if (rank == n - 1) bar = head;
     }
     __syncthreads();
-    if (tid < W && !bad) {
+    if (!bad) {
         const Key least = bar;
-        for (int j = 0; j < n; ++j) {
-            const Key k = lists[tid * n + j];
-            if (k < least) break;
-            found[atomicAdd(&count, 1)] = k;
+#pragma unroll
+        for (int i = 0; i < AHEAD; ++i)
+            if (ahead[i] >= least) found[atomicAdd(&count, 1)] = ahead[i];
+        for (int i = AHEAD * THREADS + tid; i < W * n; i += THREADS) {
+            const Key k = lists[i];
+            if (k >= least) found[atomicAdd(&count, 1)] = k;
         }
     }
     __syncthreads();
@@ -269,6 +362,7 @@ __device__ __forceinline__ void finish(const LogprobArgs& a, const void* row, lo
     for (int i = tid; i < c; i += THREADS) {
         const Key k = found[i];
         int rank = 0;
+#pragma unroll 8
         for (int j = 0; j < c; ++j) rank += found[j] > k;
         if (rank < n) {
             a.top_ids[r * n + rank] = ~static_cast<uint32_t>(k);
@@ -287,9 +381,9 @@ __device__ __forceinline__ const void* row_at(const LogprobArgs& a, long long r)
 }
 
 // A workgroup a row.
-template <bool BF16, bool TOP>
-__global__ void __launch_bounds__(kRowThreads) logprob_row_kernel(LogprobArgs a) {
-    constexpr int W = kRowThreads / 64;
+template <bool BF16, bool TOP, int THREADS>
+__global__ void __launch_bounds__(THREADS, THREADS == 64 ? 4 : 6) logprob_row_kernel(LogprobArgs a) {
+    constexpr int W = THREADS / 64;
     __shared__ Sums sums[W];
     __shared__ Key lists[TOP ? W * KDA_TOP_MAX : 1];
     const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
@@ -297,11 +391,11 @@ __global__ void __launch_bounds__(kRowThreads) logprob_row_kernel(LogprobArgs a)
     const void* row = row_at<BF16>(a, r);
     Sums s;
     List l;
-    read_part<BF16, TOP, kRowThreads>(a, row, 0, 1, s, l);
+    read_part<BF16, TOP, THREADS, THREADS == 64 ? 4 : 2, 1>(a, row, 0, 1, s, l);
     if (lane == 0) sums[wave] = s;
     if (TOP && lane < a.n_top) lists[wave * a.n_top + lane] = l.mine;
     __syncthreads();
-    finish<BF16, kRowThreads>(a, row, r, W, sums, lists);
+    finish<BF16, THREADS, 1>(a, row, r, W, sums, lists);
 }
 
 // Where the waves of split rows leave their results.
@@ -317,7 +411,7 @@ __global__ void __launch_bounds__(kSplitThreads) logprob_part_kernel(LogprobArgs
     const long long r = blockIdx.y;
     Sums s;
     List l;
-    read_part<BF16, TOP, kSplitThreads>(a, row_at<BF16>(a, r), blockIdx.x, x.parts, s, l);
+    read_part<BF16, TOP, kSplitThreads, 4, 4>(a, row_at<BF16>(a, r), blockIdx.x, x.parts, s, l);
     const long long at = (r * x.parts + blockIdx.x) * (kSplitThreads / 64) + wave;
     if (lane == 0) x.sums[at] = s;
     if (TOP && lane < a.n_top) x.lists[at * a.n_top + lane] = l.mine;
@@ -327,14 +421,16 @@ template <bool BF16>
 __global__ void __launch_bounds__(kMaxLists) logprob_join_kernel(LogprobArgs a, Split x) {
     const long long r = blockIdx.x;
     const int W = x.parts * (kSplitThreads / 64);
-    finish<BF16, kMaxLists>(a, row_at<BF16>(a, r), r, W, x.sums + r * W, x.lists + r * W * a.n_top);
+    finish<BF16, kMaxLists, 12>(a, row_at<BF16>(a, r), r, W, x.sums + r * W, x.lists + r * W * a.n_top);
 }
 
-// Workgroups a row: 1 (a row each, joined in place) from 512 rows on, where
+// Workgroups a row: 1 (a row each, joined in place) from 256 rows on, where
 // the rows alone fill the chip; below that enough for 1024 workgroups, but not
 // with less than four loads a lane.
+constexpr int kWholeRows = 256, kWaveRows = 2048;
+
 int parts_of(int t, int V, int es) {
-    if (t >= 512) return 1;
+    if (t >= kWholeRows) return 1;
     const long long loads = (static_cast<long long>(V) * es + 15) / 16;
     long long p = (loads + 4 * kSplitThreads - 1) / (4 * kSplitThreads);
     const long long fill = (1024 + t - 1) / t;
@@ -355,10 +451,20 @@ hipError_t launch(const LogprobArgs& a, hipStream_t stream) {
     const bool top = a.n_top > 0;
     if (x.parts == 1) {
         const dim3 grid(static_cast<unsigned>(a.t));
-        if (top)
-            logprob_row_kernel<BF16, true><<<grid, dim3(kRowThreads), 0, stream>>>(a);
-        else
-            logprob_row_kernel<BF16, false><<<grid, dim3(kRowThreads), 0, stream>>>(a);
+        // A wave a row from 2048 rows on (two waves a SIMD), four below: a list is
+        // filled and joined for each wave, and a row's end waits for its slowest.
+        // 150,000 bf16 logits, 8 alternatives: 2048 rows 130 us with a wave, 139
+        // with four; 1024 rows 102 and 83; 512 rows 106 and 54.
+        if (a.t >= kWaveRows) {
+            if (top)
+                logprob_row_kernel<BF16, true, 64><<<grid, dim3(64), 0, stream>>>(a);
+            else
+                logprob_row_kernel<BF16, false, 64><<<grid, dim3(64), 0, stream>>>(a);
+        } else if (top) {
+            logprob_row_kernel<BF16, true, 256><<<grid, dim3(256), 0, stream>>>(a);
+        } else {
+            logprob_row_kernel<BF16, false, 256><<<grid, dim3(256), 0, stream>>>(a);
+        }
         return hipGetLastError();
     }
     // the keys first: they need 8-byte alignment
