@@ -954,24 +954,31 @@ __global__ void __launch_bounds__(256) kda_prepare_kernel(PromptArgs a, KdaBlock
     to[128] = w[1];
 }
 
-// The chunks in slots slot0 .. slot1-1 of one sequence and head, 16 * NC value
-// columns.  Wave NC * half + c has the columns of block c and key channels
-// 64 half.. of the state in 16 registers; the two halves of a column block
-// exchange their parts of the sums over channels through LDS.  The next chunk's
-// operands are on their way to registers while the current one is worked on,
-// and go to the other half of LDS behind it.
+// The chunks in slots slot0 .. slot1-1 of one sequence and head, 32 value columns.
+//
+// What ties the chunks together, S_0 -> R = V - (k e^G) S_0 -> E = M R -> S_C, is
+// done by waves 0..3 and nothing else: wave 2 * half + c has columns 16 c.. and
+// key channels 64 half.. of the state in 16 registers, and the two halves of a
+// column block exchange their parts of R through LDS.  Waves 4..7 follow them:
+// they bring the next chunk's operands and values from memory to LDS, and form
+// the outputs of 16 rows x 16 columns each from the state's words and the
+// deltas that waves 0..3 leave in LDS, one barrier behind.
 //
 // Operands are two f16 words of a value scaled by a power of two (3 products,
-// 22 bits): state, right-hand side and deltas by their column's largest,
-// k, q, M and B by the chunk's.
-template <bool BF16, bool OUT, int NC>
-__global__ void __launch_bounds__(128 * NC) kda_chunk_kernel(PromptArgs a, const KdaBlock* blocks, int slot0,
-                                                             int slot1) {
+// 22 bits): state and right-hand side by their column's largest, k, q, M and B
+// by the chunk's.  The deltas need no search: with the largest |M| and |R| under
+// 2^14 their sums of 32 products stay under 2^33, and 2^-18 of them in f16.
+constexpr int kKdaCols = 32;
+
+template <bool BF16, bool OUT>
+__global__ void __launch_bounds__(512) kda_chunk_kernel(PromptArgs a, const KdaBlock* blocks, int slot0, int slot1) {
     __shared__ __align__(16) KdaBlock tiles[2];
-    __shared__ f32x4 xr[2 * NC][2][64], xo[2 * NC][64];
-    constexpr int slices = 8 / NC, threads = 128 * NC, pieces = sizeof(KdaBlock) / 16;
-    constexpr int copies = (pieces + threads - 1) / threads;
-    constexpr int es = BF16 ? 2 : 4;
+    __shared__ f32x4 xr[4][2][64];          // parts of R
+    __shared__ f32x4 xv[2][2][64];          // V: column block, row block
+    __shared__ uint4 sw[2][2][2][2][64];    // the state: column block, half, 32 channels, word
+    __shared__ uint4 ew[2][2][64];          // the deltas: column block, word
+    __shared__ float si[2][2][64], ei[2][64];   // what undoes their scales
+    constexpr int slices = kD / kKdaCols, es = BF16 ? 2 : 4;
     const int tid = threadIdx.x, wave = __builtin_amdgcn_readfirstlane(tid >> 6), lane = tid & 63, g4 = lane >> 4, l16 = lane & 15;
     // workgroups go round 8 XCDs: the slices of a head to one of them, whose L2
     // then has the operands that they share
@@ -987,8 +994,98 @@ __global__ void __launch_bounds__(128 * NC) kda_chunk_kernel(PromptArgs a, const
     if (state == nullptr || begin >= end) return;
     state += static_cast<long long>(h) * kD * kD;
     blocks += static_cast<long long>(own - slot0) * a.H + h;
+    const f32x4 zero{0.f, 0.f, 0.f, 0.f};
 
-    const int half = wave / NC, partner = (wave + NC) % (2 * NC), col = 16 * (NC * slice + wave % NC) + l16;
+    if (wave >= 4) {
+        const int c = wave & 1, tb = (wave >> 1) & 1, x = tid - 256;
+        const int col = kKdaCols * slice + 16 * c + l16;
+        constexpr int pieces = sizeof(KdaBlock) / 4096, rest = sizeof(KdaBlock) % 4096 / 16;
+        u32x4 next[pieces + 1];
+        uint32_t v[4];
+        const auto fetch = [&](int i) {
+            const auto from = __builtin_amdgcn_make_buffer_rsrc(
+                const_cast<KdaBlock*>(blocks + static_cast<long long>(i) * a.H), 0, sizeof(KdaBlock), 0x00020000);
+#pragma unroll
+            for (int j = 0; j <= pieces; ++j)
+                next[j] = __builtin_amdgcn_raw_buffer_load_b128(from, 16 * x, 4096 * j, 0);
+            const int t0 = first + i * kChunk;
+            const Rows rv = rows_of(a.v, es, t0, last - t0, a.H, h);
+#pragma unroll
+            for (int r = 0; r < 4; ++r) v[r] = load_raw<BF16>(rv, 16 * tb + 4 * g4 + r, col);
+        };
+        const auto store = [&](KdaBlock& T) {
+            u32x4* to = reinterpret_cast<u32x4*>(&T) + x;
+#pragma unroll
+            for (int j = 0; j < pieces; ++j) to[256 * j] = next[j];
+            if (x < rest) to[256 * pieces] = next[pieces];
+            xv[c][tb][lane] = f32x4{element<BF16>(v[0]), element<BF16>(v[1]), element<BF16>(v[2]), element<BF16>(v[3])};
+        };
+        fetch(begin);
+        store(tiles[0]);
+        if (begin + 1 < end) fetch(begin + 1);
+        f32x4 Q = zero;
+        uint4 bf[2];
+        float bs = 0.f;
+        for (int i = begin; i <= end; ++i) {
+            const KdaBlock& T = tiles[(i - begin) & 1];
+            __syncthreads();
+            // the chunk before: its deltas are there now
+            uint4 ef[2];
+            float e = 0.f;
+            if (OUT && i > begin) {
+#pragma unroll
+                for (int w = 0; w < 2; ++w) ef[w] = ew[c][w][lane];
+                e = ei[c][lane];
+            }
+            uint4 qf[4][2], sf[4][2];
+            float s0 = 0.f, s1 = 0.f;
+            if (OUT && i < end) {
+#pragma unroll
+                for (int ks = 0; ks < 4; ++ks)
+#pragma unroll
+                    for (int w = 0; w < 2; ++w) {
+                        qf[ks][w] = T.q[tb][ks][w][lane];
+                        sf[ks][w] = sw[c][ks >> 1][ks & 1][w][lane];
+                    }
+                s0 = si[c][0][lane];
+                s1 = si[c][1][lane];
+            }
+            if (i < end) __syncthreads();
+            if (OUT && i > begin) {
+                const f32x4 y = product16(bf, ef, zero);
+                const float f = bs * e;
+                const int t0 = first + (i - 1) * kChunk;
+                const Rows ro = rows_of(a.o, 4, t0, last - t0, a.H, h);
+#pragma unroll
+                for (int r = 0; r < 4; ++r)
+                    __builtin_amdgcn_raw_buffer_store_b32(bits(fmaf(y[r], f, Q[r]) * kScale), ro.buffer,
+                                                          (16 * tb + 4 * g4 + r) * ro.pitch + 4 * col, 0, 0);
+            }
+            if (i == end) break;
+            if (i + 1 < end) {
+                store(tiles[(i + 1 - begin) & 1]);
+                if (i + 2 < end) fetch(i + 2);
+            }
+            if (OUT) {
+                f32x4 q0 = zero, q1 = zero;
+                const float qs = inverse_of(T.scale.q);
+                bs = inverse_of(T.scale.b);
+#pragma unroll
+                for (int w = 0; w < 2; ++w) bf[w] = T.b[tb][w][lane];
+#pragma unroll
+                for (int ks = 0; ks < 2; ++ks) {
+                    q0 = product16(qf[ks], sf[ks], q0);
+                    q1 = product16(qf[2 + ks], sf[2 + ks], q1);
+                }
+                const float f0 = qs * s0, f1 = qs * s1;
+#pragma unroll
+                for (int r = 0; r < 4; ++r) Q[r] = fmaf(q0[r], f0, q1[r] * f1);
+            }
+        }
+        return;
+    }
+
+    const int half = wave >> 1, c = wave & 1, col = kKdaCols * slice + 16 * c + l16;
     f32x4 S[4];
     float smax = 0.f;
 #pragma unroll
@@ -997,88 +1094,57 @@ __global__ void __launch_bounds__(128 * NC) kda_chunk_kernel(PromptArgs a, const
         for (int r = 0; r < 4; ++r) S[m][r] = state[(64 * half + 16 * m + 4 * g4 + r) * kD + col];
         smax = abs_max(S[m], smax);
     }
-    u32x4 next[copies];
-    uint32_t v[2][4];
-    const auto fetch = [&](int i) {
-        const u32x4* p = reinterpret_cast<const u32x4*>(blocks + static_cast<long long>(i) * a.H);
-#pragma unroll
-        for (int x = 0; x < copies; ++x) next[x] = p[min(x * threads + tid, pieces - 1)];
-    };
-    const auto fetch_v = [&](int i) {
-        const int t0 = first + i * kChunk;
-        const Rows rv = rows_of(a.v, es, t0, last - t0, a.H, h);
-#pragma unroll
-        for (int tb = 0; tb < 2; ++tb)
-#pragma unroll
-            for (int r = 0; r < 4; ++r) v[tb][r] = load_raw<BF16>(rv, 16 * tb + 4 * g4 + r, col);
-    };
-    const auto store = [&](KdaBlock& T) {
-        u32x4* p = reinterpret_cast<u32x4*>(&T);
-#pragma unroll
-        for (int x = 0; x < copies; ++x)
-            if ((x + 1) * threads <= pieces || x * threads + tid < pieces) p[x * threads + tid] = next[x];
-    };
-    fetch(begin);
-    if (half == 0) fetch_v(begin);
-    store(tiles[0]);
-
     for (int i = begin; i < end; ++i) {
         const KdaBlock& T = tiles[(i - begin) & 1];
-        const float ss = scale_of(column_max(smax));
+        const float ss = scale_of(column_max(smax)), s1 = inverse_of(ss);
         uint4 sf[2][2];
 #pragma unroll
-        for (int ks = 0; ks < 2; ++ks) halves8(S[2 * ks], S[2 * ks + 1], ss, sf[ks]);
+        for (int ks = 0; ks < 2; ++ks) {
+            halves8(S[2 * ks], S[2 * ks + 1], ss, sf[ks]);
+            if (OUT)
+#pragma unroll
+                for (int w = 0; w < 2; ++w) sw[c][half][ks][w][lane] = sf[ks][w];
+        }
+        if (OUT) si[c][half][lane] = s1;
         __syncthreads();
-        if (i + 1 < end) fetch(i + 1);
-        uint4 kf[2][2][2], qf[2][2][2];
+        uint4 kf[2][2][2];
 #pragma unroll
         for (int ks = 0; ks < 2; ++ks)
 #pragma unroll
             for (int tb = 0; tb < 2; ++tb)
 #pragma unroll
-                for (int w = 0; w < 2; ++w) {
-                    kf[ks][tb][w] = T.k[tb][2 * half + ks][w][lane];
-                    if (OUT) qf[ks][tb][w] = T.q[tb][2 * half + ks][w][lane];
-                }
-        const ChunkScale sc = T.scale;
+                for (int w = 0; w < 2; ++w) kf[ks][tb][w] = T.k[tb][2 * half + ks][w][lane];
+        f32x4 R[2] = {zero, zero}, V[2] = {zero, zero};
+        if (half == 0)
+#pragma unroll
+            for (int tb = 0; tb < 2; ++tb) V[tb] = xv[c][tb][lane];
+        const float ki = inverse_of(T.scale.k), mi = inverse_of(T.scale.m);
         // what undoes the scales; a product that leaves f32 only does so where
         // the value itself would
-        const float sk = inverse_of(sc.k), si = inverse_of(ss), rs = -sk * si, qs = inverse_of(sc.q) * si;
-        f32x4 R[2], Q[2];
-#pragma unroll
-        for (int tb = 0; tb < 2; ++tb) R[tb] = Q[tb] = f32x4{0.f, 0.f, 0.f, 0.f};
+        const float rs = -ki * s1;
 #pragma unroll
         for (int ks = 0; ks < 2; ++ks)
 #pragma unroll
             for (int tb = 0; tb < 2; ++tb) R[tb] = product16(kf[ks][tb], sf[ks], R[tb]);
-        if (OUT)
-#pragma unroll
-            for (int ks = 0; ks < 2; ++ks)
-#pragma unroll
-                for (int tb = 0; tb < 2; ++tb) Q[tb] = product16(qf[ks][tb], sf[ks], Q[tb]);
 #pragma unroll
         for (int tb = 0; tb < 2; ++tb) {
 #pragma unroll
-            for (int r = 0; r < 4; ++r) R[tb][r] = fmaf(R[tb][r], rs, half == 0 ? element<BF16>(v[tb][r]) : 0.f);
+            for (int r = 0; r < 4; ++r) R[tb][r] = fmaf(R[tb][r], rs, V[tb][r]);
             xr[wave][tb][lane] = R[tb];
-            if (OUT) Q[tb] *= qs;
         }
-        if (OUT) xo[wave][lane] = half == 0 ? Q[1] : Q[0];
-        if (half == 0 && i + 1 < end) fetch_v(i + 1);
-        __syncthreads();
-        uint4 mf[2][2], bf[2], tf[4][2];
+        uint4 mf[2][2], tf[4][2];
         f32x4 keep[4];
+#pragma unroll
+        for (int tb = 0; tb < 2; ++tb)
+#pragma unroll
+            for (int w = 0; w < 2; ++w) mf[tb][w] = T.m[tb][w][lane];
+        __syncthreads();
         float rmax = 0.f;
 #pragma unroll
         for (int tb = 0; tb < 2; ++tb) {
-            R[tb] += xr[partner][tb][lane];
+            R[tb] += xr[wave ^ 2][tb][lane];
             rmax = abs_max(R[tb], rmax);
-#pragma unroll
-            for (int w = 0; w < 2; ++w) mf[tb][w] = T.m[tb][w][lane];
         }
-        if (OUT)
-#pragma unroll
-            for (int w = 0; w < 2; ++w) bf[w] = T.b[half][w][lane];
 #pragma unroll
         for (int m = 0; m < 4; ++m) {
 #pragma unroll
@@ -1089,38 +1155,26 @@ __global__ void __launch_bounds__(128 * NC) kda_chunk_kernel(PromptArgs a, const
         uint4 rf[2], ef[2];
         halves8(R[0], R[1], sr, rf);
         f32x4 E[2];    // the deltas, scaled as M and R are
-        float emax = 0.f;
 #pragma unroll
-        for (int tb = 0; tb < 2; ++tb) {
-            E[tb] = product16(mf[tb], rf, f32x4{0.f, 0.f, 0.f, 0.f});
-            emax = abs_max(E[tb], emax);
-        }
-        const float se = scale_of(column_max(emax));
-        const float ei = inverse_of(sc.m) * inverse_of(sr) * inverse_of(se);
+        for (int tb = 0; tb < 2; ++tb) E[tb] = product16(mf[tb], rf, zero);
+        constexpr float se = 1.f / (1 << 18);
         halves8(E[0], E[1], se, ef);
-        const float ke = sk * ei;
+        const float e = mi * inverse_of(sr) * (1 << 18), ke = ki * e;
+        if (OUT && half == 0) {
+#pragma unroll
+            for (int w = 0; w < 2; ++w) ew[c][w][lane] = ef[w];
+            ei[c][lane] = e;
+        }
         smax = 0.f;
 #pragma unroll
         for (int m = 0; m < 4; ++m) {
-            const f32x4 y = product16(tf[m], ef, f32x4{0.f, 0.f, 0.f, 0.f});
+            const f32x4 y = product16(tf[m], ef, zero);
 #pragma unroll
             for (int r = 0; r < 4; ++r) S[m][r] = fmaf(y[r], ke, S[m][r] * keep[m][r]);
             smax = abs_max(S[m], smax);
         }
-        if (OUT) {
-            f32x4 O = half == 0 ? Q[0] : Q[1];
-            O += xo[partner][lane];
-            const f32x4 y = product16(bf, ef, f32x4{0.f, 0.f, 0.f, 0.f});
-            const float bs = inverse_of(sc.b) * ei;
-            const int t0 = first + i * kChunk;
-            const Rows ro = rows_of(a.o, 4, t0, last - t0, a.H, h);
-#pragma unroll
-            for (int r = 0; r < 4; ++r)
-                __builtin_amdgcn_raw_buffer_store_b32(bits(fmaf(y[r], bs, O[r]) * kScale), ro.buffer,
-                                                      (16 * half + 4 * g4 + r) * ro.pitch + 4 * col, 0, 0);
-        }
-        if (i + 1 < end) store(tiles[(i + 1 - begin) & 1]);
     }
+    __syncthreads();
 #pragma unroll
     for (int m = 0; m < 4; ++m)
 #pragma unroll
@@ -1226,16 +1280,6 @@ long long prompt_work_bytes(int R, int B, int H) {
     return all < most ? all : most;
 }
 
-template <bool BF16, int NC>
-static void launch_chunks(const PromptArgs& a, const KdaBlock* blocks, int slot0, int slot1, hipStream_t stream) {
-    const unsigned turns = static_cast<unsigned>((static_cast<long long>(a.B) * a.H + 7) / 8);
-    const dim3 grid(turns * 8 * (8 / NC));
-    if (a.o)
-        kda_chunk_kernel<BF16, true, NC><<<grid, dim3(128 * NC), 0, stream>>>(a, blocks, slot0, slot1);
-    else
-        kda_chunk_kernel<BF16, false, NC><<<grid, dim3(128 * NC), 0, stream>>>(a, blocks, slot0, slot1);
-}
-
 template <bool BF16>
 static hipError_t launch_kda(const PromptArgs& a, hipStream_t stream) {
     const long long slots = part_slots(a.R, a.B, kChunk), heads = static_cast<long long>(a.B) * a.H;
@@ -1245,11 +1289,11 @@ static hipError_t launch_kda(const PromptArgs& a, hipStream_t stream) {
         const int slot0 = static_cast<int>(s0), slot1 = static_cast<int>(s0 + turn < slots ? s0 + turn : slots);
         kda_prepare_kernel<BF16><<<dim3(static_cast<unsigned>((slot1 - slot0) * static_cast<long long>(a.H))),
                                    dim3(256), 0, stream>>>(a, blocks, slot0);
-        // few (sequence, head) pairs: fewer columns a workgroup, more workgroups
-        if (heads > 64)
-            launch_chunks<BF16, 4>(a, blocks, slot0, slot1, stream);
+        const dim3 grid(static_cast<unsigned>((heads + 7) / 8 * 8 * (kD / kKdaCols)));
+        if (a.o)
+            kda_chunk_kernel<BF16, true><<<grid, dim3(512), 0, stream>>>(a, blocks, slot0, slot1);
         else
-            launch_chunks<BF16, 2>(a, blocks, slot0, slot1, stream);
+            kda_chunk_kernel<BF16, false><<<grid, dim3(512), 0, stream>>>(a, blocks, slot0, slot1);
         const hipError_t e = hipGetLastError();
         if (e != hipSuccess) return e;
     }
