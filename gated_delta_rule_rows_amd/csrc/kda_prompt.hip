@@ -705,12 +705,13 @@ template <int N> __device__ __forceinline__ float lane_behind(float x) { return 
 template <bool BF16>
 __global__ void __launch_bounds__(256) kda_prepare_kernel(PromptArgs a, KdaBlock* blocks, int slot0) {
     struct Factors {
-        float F[kChunk][kD + 4];
+        float f[kChunk][kD + 4];      // e^{G-G_mid}
+        float inverse[kChunk][kD + 4];
         float between[kD];
     };
     __shared__ __align__(16) union {
         Factors f;
-        uint4 words[3 * 16 * 64];   // k, q and kt of the block
+        uint4 words[16 * 64];   // k, q or kt of the block, in turn
     } U;
     __shared__ float A[kChunk][kChunk + 1], B[kChunk][kChunk + 1], T[kChunk][kChunk + 1];
     __shared__ float beta[kChunk], top[4][4];
@@ -738,8 +739,6 @@ __global__ void __launch_bounds__(256) kda_prepare_kernel(PromptArgs a, KdaBlock
         if (low && wantA) load_eight<BF16>(et[ks], rk, tr, 32 * ks + 8 * g4);
         if (wantB) load_eight<BF16>(eq[ks], rq, tr, 32 * ks + 8 * g4);
     }
-    load_patch<BF16>(pk, rk, 4 * rg, 4 * cg);
-    load_patch<BF16>(pq, rq, 4 * rg, 4 * cg);
     if (tid < kChunk)
         beta[tid] = tid < n ? load<BF16>(a.beta, static_cast<long long>(t0 + tid) * a.H + h) : 0.f;
 
@@ -766,7 +765,9 @@ __global__ void __launch_bounds__(256) kda_prepare_kernel(PromptArgs a, KdaBlock
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
                 const float y = (late ? pre[i][c] : suf[i][c]) * beyond;
-                U.f.F[4 * rg + i][4 * cg + c] = late ? y : __builtin_amdgcn_rcpf(y);
+                const float r = __builtin_amdgcn_rcpf(y);
+                U.f.f[4 * rg + i][4 * cg + c] = late ? y : r;
+                U.f.inverse[4 * rg + i][4 * cg + c] = late ? r : y;
             }
             // between the middles: row groups 2, 3 and 4, 5
             const float pair = all * near, next = lane_behind<2>(pair);
@@ -793,40 +794,40 @@ __global__ void __launch_bounds__(256) kda_prepare_kernel(PromptArgs a, KdaBlock
     }
     __syncthreads();
 
+    // (f32 products: these operands would take three bf16 words and six
+    // products, and taking them apart costs more than the matrix cores gain)
     f32x4 xa{0.f, 0.f, 0.f, 0.f}, xb{0.f, 0.f, 0.f, 0.f};
     float kmax = 0.f, qmax = 0.f;
 #pragma unroll
     for (int ks = 0; ks < 4; ++ks) {
         const int c = 32 * ks + 8 * g4;
-        float x[8], y[8], ft[8];
-        uint4 kj[3], w[3];
+        float x[8], kj[8], ft[8];
         eight_values<BF16>(ek[ks], x);
 #pragma unroll
         for (int i = 0; i < 8; ++i) {
             kmax = fmaxf(kmax, fabsf(x[i]));
-            y[i] = x[i] * __builtin_amdgcn_rcpf(U.f.F[jr][c + i]);
+            kj[i] = x[i] * U.f.inverse[jr][c + i];
+            ft[i] = U.f.f[tr][c + i];
         }
-        split8(y, kj);
+        if (low)
 #pragma unroll
-        for (int i = 0; i < 8; ++i) ft[i] = U.f.F[tr][c + i] * (low ? U.f.between[c + i] : 1.f);
+            for (int i = 0; i < 8; ++i) ft[i] *= U.f.between[c + i];
         if (wantA) {
             if (low) eight_values<BF16>(et[ks], x);
 #pragma unroll
-            for (int i = 0; i < 8; ++i) y[i] = x[i] * ft[i];
-            split8(y, w);
-            xa = product<3, 3>(w, kj, xa);
+            for (int i = 0; i < 8; ++i) xa = __builtin_amdgcn_mfma_f32_16x16x4f32(x[i] * ft[i], kj[i], xa, 0, 0, 0);
         }
         if (wantB) {
             eight_values<BF16>(eq[ks], x);
 #pragma unroll
             for (int i = 0; i < 8; ++i) {
                 qmax = fmaxf(qmax, fabsf(x[i]));
-                y[i] = x[i] * ft[i];
+                xb = __builtin_amdgcn_mfma_f32_16x16x4f32(x[i] * ft[i], kj[i], xb, 0, 0, 0);
             }
-            split8(y, w);
-            xb = product<3, 3>(w, kj, xb);
         }
     }
+    load_patch<BF16>(pk, rk, 4 * rg, 4 * cg);
+    load_patch<BF16>(pq, rq, 4 * rg, 4 * cg);
     kmax = wave_max(kmax);
     qmax = wave_max(qmax);
     if (lane == 0) {
@@ -858,25 +859,48 @@ __global__ void __launch_bounds__(256) kda_prepare_kernel(PromptArgs a, KdaBlock
     // ... and beside it the operands; the factors' memory is free
     const float sk = scale_of(fmaxf(fmaxf(top[0][0], top[0][1]), fmaxf(top[0][2], top[0][3])));
     const float sq = scale_of(fmaxf(fmaxf(top[1][0], top[1][1]), fmaxf(top[1][2], top[1][3])));
+    KdaBlock& out = blocks[blockIdx.x];
+    if (rg == 7) *reinterpret_cast<float4*>(&out.keep[4 * cg]) = make_float4(keep[0], keep[1], keep[2], keep[3]);
     {
         float x[4][4];
         uint2 w[4][2];
+        // (16-byte piece p of an operand lies at p ^ its lane group, so that the
+        // writes of a wave spread over the banks)
         uint2* const to = reinterpret_cast<uint2*>(U.words);
         const int at = (cg >> 3) * 2 * 128 + (cg & 3) * 32 + (cg >> 2 & 1);   // channel part of a row operand
+        const auto by_row = [&](float sc) {
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                float y[4];
+#pragma unroll
+                for (int c = 0; c < 4; ++c) y[c] = pre[i][c] * sc;
+                halves4(x[i], y, w[i]);
+                const int t = 4 * rg + i;
+#pragma unroll
+                for (int s = 0; s < 2; ++s) to[(t >> 4) * 8 * 128 + s * 128 + at + 2 * ((t & 15) ^ (cg & 3))] = w[i][s];
+            }
+        };
+        const auto copy = [&](uint4* to) {
+#pragma unroll
+            for (int i = 0; i < 4; ++i) to[256 * i + tid] = U.words[256 * i + (tid ^ g4)];
+        };
+        patch_values<BF16>(pq, x);
+        by_row(sq);
+        __syncthreads();
+        copy(&out.q[0][0][0][0]);
+        __syncthreads();
         patch_values<BF16>(pk, x);
-#pragma unroll
-        for (int i = 0; i < 4; ++i)
-#pragma unroll
-            for (int c = 0; c < 4; ++c) x[i][c] *= sk;
+        by_row(sk);
+        __syncthreads();
+        copy(&out.k[0][0][0][0]);
+        __syncthreads();
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
-            halves4(x[i], pre[i], w[i]);
-            const int t = 4 * rg + i;
+            float y[4];
 #pragma unroll
-            for (int s = 0; s < 2; ++s) to[(t >> 4) * 8 * 128 + s * 128 + at + 2 * (t & 15)] = w[i][s];
+            for (int c = 0; c < 4; ++c) y[c] = suf[i][c] * sk;
+            halves4(x[i], y, w[i]);
         }
-#pragma unroll
-        for (int i = 0; i < 4; ++i) halves4(x[i], suf[i], w[i]);
 #pragma unroll
         for (int s = 0; s < 2; ++s)
 #pragma unroll
@@ -885,28 +909,10 @@ __global__ void __launch_bounds__(256) kda_prepare_kernel(PromptArgs a, KdaBlock
                 uint2 y;
                 y.x = __builtin_amdgcn_perm(c < 2 ? w[1][s].x : w[1][s].y, c < 2 ? w[0][s].x : w[0][s].y, sel);
                 y.y = __builtin_amdgcn_perm(c < 2 ? w[3][s].x : w[3][s].y, c < 2 ? w[2][s].x : w[2][s].y, sel);
-                to[32 * 128 + ((cg >> 2) * 2 + s) * 128 + (rg & 3) * 32 + 2 * (4 * (cg & 3) + c) + (rg >> 2)] = y;
+                to[((cg >> 2) * 2 + s) * 128 + (rg & 3) * 32 + 2 * ((4 * (cg & 3) + c) ^ (rg & 3)) + (rg >> 2)] = y;
             }
-        patch_values<BF16>(pq, x);
-#pragma unroll
-        for (int i = 0; i < 4; ++i)
-#pragma unroll
-            for (int c = 0; c < 4; ++c) x[i][c] *= sq;
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            halves4(x[i], pre[i], w[i]);
-            const int t = 4 * rg + i;
-#pragma unroll
-            for (int s = 0; s < 2; ++s) to[16 * 128 + (t >> 4) * 8 * 128 + s * 128 + at + 2 * (t & 15)] = w[i][s];
-        }
-    }
-    KdaBlock& out = blocks[blockIdx.x];
-    if (rg == 7) *reinterpret_cast<float4*>(&out.keep[4 * cg]) = make_float4(keep[0], keep[1], keep[2], keep[3]);
-    __syncthreads();
-    {
-        uint4* to = &out.k[0][0][0][0];
-#pragma unroll
-        for (int i = 0; i < 12; ++i) to[256 * i + tid] = U.words[256 * i + tid];
+        __syncthreads();
+        copy(&out.kt[0][0][0]);
         // the block of T below the diagonal
         const int t = tid >> 4, j = tid & 15;
         float s = 0.f;
