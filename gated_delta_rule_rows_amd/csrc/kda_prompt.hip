@@ -94,8 +94,8 @@ __device__ __forceinline__ void sequence(const PromptArgs& a, int b, int& first,
 // where neither is.  G is summed in 64 bits: behind a row of strong decay a
 // 32-bit running sum would lose the weak ones.
 //
-// A workgroup (4 waves) owns a head and a part of a sequence; a wave owns 32
-// value columns, its 128 x 32 piece of the state stays in 64 registers.  The
+// A workgroup (8 waves) owns a head and a part of a sequence; a wave owns 16
+// value columns, its 128 x 16 piece of the state stays in 32 registers.  The
 // state's accumulator layout is an operand layout as it stands, with the key
 // channels of a 32-block in the order p(16 h + 4 g + r) = 8 g + 4 h + r; q and
 // k are stored in LDS in that order.
@@ -186,6 +186,11 @@ __device__ __forceinline__ void load_patch(Patch<BF16>& p, const Rows& x, int ro
             p.r[i] = __builtin_bit_cast(uint4, __builtin_amdgcn_raw_buffer_load_b128(x.buffer, at, 0, 0));
         }
     }
+}
+
+// One head's state as a buffer (one offset a lane, whatever the row).
+__device__ __forceinline__ __amdgpu_buffer_rsrc_t state_of(const float* s) {
+    return __builtin_amdgcn_make_buffer_rsrc(const_cast<float*>(s), 0, kD * kD * 4, 0x00020000);
 }
 
 // One element, raw; element() makes it a number.
@@ -279,8 +284,8 @@ struct Parts {
 // STATES: the part's own state, from zero, into its slot (all but a sequence's
 // last part).  Otherwise the outputs, and from a sequence's last part its state.
 template <bool BF16, bool STATES>
-__global__ void __launch_bounds__(256, BF16 ? 2 : 1) linear_chunk_kernel(PromptArgs a, Parts parts) {
-    constexpr int NS = BF16 ? 1 : 3;
+__global__ void __launch_bounds__(512, BF16 ? 4 : 2) linear_chunk_kernel(PromptArgs a, Parts parts) {
+    constexpr int NS = BF16 ? 1 : 3, es = BF16 ? 2 : 4;
     __shared__ __align__(16) LinearTile<NS> T;
     const int tid = threadIdx.x, wave = __builtin_amdgcn_readfirstlane(tid >> 6), lane = tid & 63, g4 = lane >> 4, l16 = lane & 15;
     const int h = blockIdx.x % a.H, slot = blockIdx.x / a.H;
@@ -296,12 +301,11 @@ __global__ void __launch_bounds__(256, BF16 ? 2 : 1) linear_chunk_kernel(PromptA
     const bool out = !STATES && a.o != nullptr;
     if (STATES ? last_part : !out && !last_part) return;
 
-    f32x4 S[8][2];
+    const int col = 16 * wave + l16;
+    f32x4 S[8];
     if constexpr (STATES) {
 #pragma unroll
-        for (int m = 0; m < 8; ++m)
-#pragma unroll
-            for (int c = 0; c < 2; ++c) S[m][c] = f32x4{0.f, 0.f, 0.f, 0.f};
+        for (int m = 0; m < 8; ++m) S[m] = f32x4{0.f, 0.f, 0.f, 0.f};
     } else {
         // the chained states lie one slot back; a first part's in the last slot
         const float* from = state;
@@ -309,13 +313,12 @@ __global__ void __launch_bounds__(256, BF16 ? 2 : 1) linear_chunk_kernel(PromptA
             const int back = f.index > 0 ? slot - 1 : slot + (f.last - f.first - 1) / parts.rows;
             from = parts.states + (static_cast<long long>(back) * a.H + h) * kD * kD;
         }
+        const auto buffer = state_of(from);
 #pragma unroll
         for (int m = 0; m < 8; ++m)
 #pragma unroll
-            for (int c = 0; c < 2; ++c)
-#pragma unroll
-                for (int r = 0; r < 4; ++r)
-                    S[m][c][r] = from[(16 * m + 4 * g4 + r) * kD + 32 * wave + 16 * c + l16];
+            for (int r = 0; r < 4; ++r)
+                S[m][r] = real(__builtin_amdgcn_raw_buffer_load_b32(buffer, (4 * g4 * kD + col) * 4, (16 * m + r) * kD * 4, 0));
         // the weights' upper block stays zero
         if (tid < 16)
 #pragma unroll
@@ -325,17 +328,20 @@ __global__ void __launch_bounds__(256, BF16 ? 2 : 1) linear_chunk_kernel(PromptA
             }
     }
 
-    const int rg = tid & 7, cg = tid >> 3;
-    constexpr int es = BF16 ? 2 : 4;
-    Patch<BF16> pq, pk, pv;
+    // waves 0..3 bring k and g, 4..7 q and v
+    const int x = tid & 255, rg = x & 7, cg = x >> 3;
+    Patch<BF16> pa, pb;
     float pg = 0.f;
     const auto fetch = [&](int t0) {
         const int n = end - t0;
-        if (out) load_patch<BF16>(pq, rows_of(a.q, es, t0, n, a.Hk, hk), 4 * rg, 4 * cg);
-        load_patch<BF16>(pk, rows_of(a.k, es, t0, n, a.Hk, hk), 4 * rg, 4 * cg);
-        load_patch<BF16>(pv, rows_of(a.v, es, t0, n, a.H, h), 4 * rg, 4 * cg);
-        if (tid < kChunk)
-            pg = t0 + tid < end ? static_cast<const float*>(a.g)[static_cast<long long>(t0 + tid) * a.H + h] : 0.f;
+        if (wave < 4) {
+            load_patch<BF16>(pa, rows_of(a.k, es, t0, n, a.Hk, hk), 4 * rg, 4 * cg);
+            if (tid < kChunk)
+                pg = t0 + tid < end ? static_cast<const float*>(a.g)[static_cast<long long>(t0 + tid) * a.H + h] : 0.f;
+        } else {
+            load_patch<BF16>(pa, rows_of(a.v, es, t0, n, a.H, h), 4 * rg, 4 * cg);
+            if (out) load_patch<BF16>(pb, rows_of(a.q, es, t0, n, a.Hk, hk), 4 * rg, 4 * cg);
+        }
     };
     fetch(begin);
     double sum = 0.0;
@@ -344,17 +350,19 @@ __global__ void __launch_bounds__(256, BF16 ? 2 : 1) linear_chunk_kernel(PromptA
         __syncthreads();
         {
             uint2 w[4][NS];
-            if (out) {
-                patch_words<BF16>(pq, w);
-                store_rows<NS>(T.q, cg, rg, w);
+            patch_words<BF16>(pa, w);
+            if (wave < 4) {
+                store_columns<NS>(T.kt, cg, 4 * rg, w);
+                if (out) store_rows<NS>(T.k, cg, rg, w);
+            } else {
+                store_columns<NS>(T.vt, cg, 4 * rg, w);
+                if (out) {
+                    patch_words<BF16>(pb, w);
+                    store_rows<NS>(T.q, cg, rg, w);
+                }
             }
-            patch_words<BF16>(pk, w);
-            if (out) store_rows<NS>(T.k, cg, rg, w);
-            store_columns<NS>(T.kt, cg, 4 * rg, w);
-            patch_words<BF16>(pv, w);
-            store_columns<NS>(T.vt, cg, 4 * rg, w);
         }
-        if (tid < 64) {
+        if (wave == 0) {
             double x = lane < kChunk ? fminf(fmaxf(pg, kGateOff), 0.f) : 0.f;
 #pragma unroll
             for (int d = 1; d < kChunk; d <<= 1) {
@@ -390,7 +398,8 @@ __global__ void __launch_bounds__(256, BF16 ? 2 : 1) linear_chunk_kernel(PromptA
 #pragma unroll
                 for (int r = 0; r < 4; ++r) {
                     const int j = 16 * jb + 4 * g4 + r;
-                    y[r] = j <= t ? x[r] * expf(static_cast<float>(Gt - T.G[j])) : 0.f;
+                    const float e = expf(static_cast<float>(fmin(Gt - T.G[j], 0.0)));
+                    y[r] = j <= t ? x[r] * e : 0.f;
                 }
                 uint2 w[3];
                 split4(y, w);
@@ -399,54 +408,41 @@ __global__ void __launch_bounds__(256, BF16 ? 2 : 1) linear_chunk_kernel(PromptA
                     *reinterpret_cast<uint2*>(&T.p[s][t][16 * jb + 4 * g4]) = w[s];
             }
             const Rows o = rows_of(a.o, 4, t0, end - t0, a.H, h);
-            f32x4 O[2][2];
-#pragma unroll
-            for (int c = 0; c < 2; ++c)
-#pragma unroll
-                for (int tb = 0; tb < 2; ++tb) O[c][tb] = f32x4{0.f, 0.f, 0.f, 0.f};
+            f32x4 O[2] = {f32x4{0.f, 0.f, 0.f, 0.f}, f32x4{0.f, 0.f, 0.f, 0.f}};
 #pragma unroll
             for (int ks = 0; ks < 4; ++ks) {
-                uint4 sf[2][3];
-#pragma unroll
-                for (int c = 0; c < 2; ++c) {
-                    const f32x4 lo = S[2 * ks][c], hi = S[2 * ks + 1][c];
-                    const float x[8] = {lo[0], lo[1], lo[2], lo[3], hi[0], hi[1], hi[2], hi[3]};
-                    split8(x, sf[c]);
-                }
+                const f32x4 lo = S[2 * ks], hi = S[2 * ks + 1];
+                const float x[8] = {lo[0], lo[1], lo[2], lo[3], hi[0], hi[1], hi[2], hi[3]};
+                uint4 sf[3];
+                split8(x, sf);
 #pragma unroll
                 for (int tb = 0; tb < 2; ++tb) {
                     uint4 qf[NS];
                     read_rows<NS>(T.q, 16 * tb + l16, 32 * ks + 8 * g4, qf);
-#pragma unroll
-                    for (int c = 0; c < 2; ++c) O[c][tb] = product<3, NS>(sf[c], qf, O[c][tb]);
+                    O[tb] = product<3, NS>(sf, qf, O[tb]);
                 }
             }
             __syncthreads();
+            uint4 vf[NS];
+            read_columns<NS, kD>(T.vt, col, 8 * g4, vf);
 #pragma unroll
             for (int tb = 0; tb < 2; ++tb) {
                 const float e = T.eG[16 * tb + l16];
                 uint4 pf[3];
                 read_columns<3, kChunk>(T.p, 16 * tb + l16, 8 * g4, pf);
-#pragma unroll
-                for (int c = 0; c < 2; ++c) {
-                    uint4 vf[NS];
-                    read_columns<NS, kD>(T.vt, 32 * wave + 16 * c + l16, 8 * g4, vf);
-                    O[c][tb] *= e;
-                    O[c][tb] = product<NS, 3>(vf, pf, O[c][tb]);
-                    const f32x4 y = O[c][tb] * kScale;
-                    __builtin_amdgcn_raw_buffer_store_b128(__builtin_bit_cast(u32x4, y), o.buffer,
-                                                           (16 * tb + l16) * o.pitch +
-                                                               4 * (32 * wave + 16 * c + 4 * g4), 0, 0);
-                }
+                O[tb] *= e;
+                O[tb] = product<NS, 3>(vf, pf, O[tb]);
+                const f32x4 y = O[tb] * kScale;
+                __builtin_amdgcn_raw_buffer_store_b128(__builtin_bit_cast(u32x4, y), o.buffer,
+                                                       (16 * tb + l16) * o.pitch + 4 * (16 * wave + 4 * g4), 0, 0);
             }
         }
 
         // the state: e^{G_C} S + k^T (weighted v)
-        uint4 vw[2][3];
-#pragma unroll
-        for (int c = 0; c < 2; ++c) {
+        uint4 vw[3];
+        {
             uint4 vf[NS];
-            read_columns<NS, kD>(T.vt, 32 * wave + 16 * c + l16, 8 * g4, vf);
+            read_columns<NS, kD>(T.vt, col, 8 * g4, vf);
             float x[8];
 #pragma unroll
             for (int i = 0; i < 8; ++i) {
@@ -458,27 +454,25 @@ __global__ void __launch_bounds__(256, BF16 ? 2 : 1) linear_chunk_kernel(PromptA
                 }
                 x[i] = v * T.w[8 * g4 + i];
             }
-            split8(x, vw[c]);
+            split8(x, vw);
         }
         const float keep = T.eG[kChunk - 1];
 #pragma unroll
         for (int m = 0; m < 8; ++m) {
             uint4 kf[NS];
             read_columns<NS, kD>(T.kt, 16 * m + l16, 8 * g4, kf);
-#pragma unroll
-            for (int c = 0; c < 2; ++c) S[m][c] = product<NS, 3>(kf, vw[c], S[m][c] * keep);
+            S[m] = product<NS, 3>(kf, vw, S[m] * keep);
         }
     }
 
     if (STATES || last_part) {
         float* to = STATES ? parts.states + (static_cast<long long>(slot) * a.H + h) * kD * kD : state;
+        const auto buffer = state_of(to);
 #pragma unroll
         for (int m = 0; m < 8; ++m)
 #pragma unroll
-            for (int c = 0; c < 2; ++c)
-#pragma unroll
-                for (int r = 0; r < 4; ++r)
-                    to[(16 * m + 4 * g4 + r) * kD + 32 * wave + 16 * c + l16] = S[m][c][r];
+            for (int r = 0; r < 4; ++r)
+                __builtin_amdgcn_raw_buffer_store_b32(bits(S[m][r]), buffer, (4 * g4 * kD + col) * 4, (16 * m + r) * kD * 4, 0);
         if (STATES && tid == 0) parts.sums[static_cast<long long>(slot) * a.H + h] = sum;
     }
 }
@@ -1321,11 +1315,11 @@ static hipError_t launch_linear(const PromptArgs& a, hipStream_t stream) {
     if (a.R > parts.rows) {   // a sequence may have several parts
         parts.states = static_cast<float*>(a.work);
         parts.sums = reinterpret_cast<double*>(parts.states + blocks * kD * kD);
-        linear_chunk_kernel<BF16, true><<<grid, dim3(256), 0, stream>>>(a, parts);
+        linear_chunk_kernel<BF16, true><<<grid, dim3(512), 0, stream>>>(a, parts);
         const dim3 chain(static_cast<unsigned>(static_cast<long long>(a.B) * a.H), kD * kD / 4 / 256);
         linear_chain_kernel<<<chain, dim3(256), 0, stream>>>(a, parts);
     }
-    linear_chunk_kernel<BF16, false><<<grid, dim3(256), 0, stream>>>(a, parts);
+    linear_chunk_kernel<BF16, false><<<grid, dim3(512), 0, stream>>>(a, parts);
     return hipGetLastError();
 }
 
