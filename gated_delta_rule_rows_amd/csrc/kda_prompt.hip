@@ -968,32 +968,66 @@ __global__ void __launch_bounds__(256) kda_prepare_kernel(PromptArgs a, KdaBlock
 // 22 bits): state and right-hand side by their column's largest, k, q, M and B
 // by the chunk's.  The deltas need no search: with the largest |M| and |R| under
 // 2^14 their sums of 32 products stay under 2^33, and 2^-18 of them in f16.
+//
+// Few sequences and heads leave most of the chip idle, and their chunks wait for
+// each other.  Then a sequence runs in parts side by side: a part's end state is
+// linear in the state it starts from, T S_0 + U, with T the end state from the
+// identity without values, and U that from zero.  STATES leaves both (the
+// slices behind the first four are T's columns); kda_chain_kernel chains them
+// to the state that each part starts from; then the parts are walked again.
 constexpr int kKdaCols = 32;
+constexpr int kWhole = 1 << 30;   // rows of a part where sequences are not divided
 
-template <bool BF16, bool OUT>
-__global__ void __launch_bounds__(512) kda_chunk_kernel(PromptArgs a, const KdaBlock* blocks, int slot0, int slot1) {
+// Slot s of head h: U, and later the next part's first state, at states +
+// (s * H + h) * 128 * 128; T at moves likewise.
+struct KdaParts {
+    float* states;
+    float* moves;
+    int rows;
+};
+
+template <bool BF16, bool OUT, bool STATES>
+__global__ void __launch_bounds__(512) kda_chunk_kernel(PromptArgs a, const KdaBlock* blocks, int slot0, int slot1,
+                                                        KdaParts parts, int units) {
+    static_assert(!(OUT && STATES), "a part's own states have no outputs");
     __shared__ __align__(16) KdaBlock tiles[2];
     __shared__ f32x4 xr[4][2][64];          // parts of R
     __shared__ f32x4 xv[2][2][64];          // V: column block, row block
     __shared__ uint4 sw[2][2][2][2][64];    // the state: column block, half, 32 channels, word
     __shared__ uint4 ew[2][2][64];          // the deltas: column block, word
     __shared__ float si[2][2][64], ei[2][64];   // what undoes their scales
-    constexpr int slices = kD / kKdaCols, es = BF16 ? 2 : 4;
+    constexpr int slices = kD / kKdaCols * (STATES ? 2 : 1), es = BF16 ? 2 : 4;
     const int tid = threadIdx.x, wave = __builtin_amdgcn_readfirstlane(tid >> 6), lane = tid & 63, g4 = lane >> 4, l16 = lane & 15;
     // workgroups go round 8 XCDs: the slices of a head to one of them, whose L2
     // then has the operands that they share
     const int turn = blockIdx.x / (8 * slices), within = blockIdx.x % (8 * slices);
-    const int bh = 8 * turn + (within & 7), slice = within >> 3;
-    if (bh >= a.B * a.H) return;
-    const int h = bh % a.H, b = bh / a.H;
-    int first, last;
-    sequence(a, b, first, last);
-    const int own = first / kChunk + b, chunks = (last - first + kChunk - 1) / kChunk;
-    const int begin = max(slot0 - own, 0), end = min(slot1 - own, chunks);
-    float* state = a.s_ptrs[b];
+    const int unit = 8 * turn + (within & 7), slice = within >> 3 & 3;
+    const bool move = STATES && within >> 3 > 3;
+    if (unit >= units) return;
+    const int h = unit % a.H;
+    const Part f = find_part(a, parts.rows, unit / a.H);
+    if (f.b < 0) return;
+    const int first = f.first, last = f.last;
+    const int own = first / kChunk + f.b, chunks = (last - first + kChunk - 1) / kChunk;
+    const int part_begin = f.index * (parts.rows / kChunk), part_end = min(part_begin + parts.rows / kChunk, chunks);
+    const bool last_part = part_end == chunks;
+    const int begin = max(slot0 - own, part_begin), end = min(slot1 - own, part_end);
+    float* state = a.s_ptrs[f.b];
     if (state == nullptr || begin >= end) return;
+    if (STATES ? last_part : !OUT && !last_part) return;
     state += static_cast<long long>(h) * kD * kD;
+    const long long head = static_cast<long long>(kD) * kD;
     blocks += static_cast<long long>(own - slot0) * a.H + h;
+    // the chained states lie one slot back; a first part's in the last slot
+    const float* from = state;
+    float* to = state;
+    if (STATES) {
+        to = (move ? parts.moves : parts.states) + unit * head;
+    } else if (f.index > 0) {
+        from = parts.states + (unit - a.H) * head;
+    } else if (!last_part) {
+        from = parts.states + (unit + static_cast<long long>((last - first - 1) / parts.rows) * a.H) * head;
+    }
     const f32x4 zero{0.f, 0.f, 0.f, 0.f};
 
     if (wave >= 4) {
@@ -1011,7 +1045,7 @@ __global__ void __launch_bounds__(512) kda_chunk_kernel(PromptArgs a, const KdaB
             const int t0 = first + i * kChunk;
             const Rows rv = rows_of(a.v, es, t0, last - t0, a.H, h);
 #pragma unroll
-            for (int r = 0; r < 4; ++r) v[r] = load_raw<BF16>(rv, 16 * tb + 4 * g4 + r, col);
+            for (int r = 0; r < 4; ++r) v[r] = move ? 0 : load_raw<BF16>(rv, 16 * tb + 4 * g4 + r, col);
         };
         const auto store = [&](KdaBlock& T) {
             u32x4* to = reinterpret_cast<u32x4*>(&T) + x;
@@ -1088,11 +1122,20 @@ __global__ void __launch_bounds__(512) kda_chunk_kernel(PromptArgs a, const KdaB
     const int half = wave >> 1, c = wave & 1, col = kKdaCols * slice + 16 * c + l16;
     f32x4 S[4];
     float smax = 0.f;
+    const int at = ((64 * half + 4 * g4) * kD + col) * 4;
+    {
+        const auto buffer = state_of(from);
 #pragma unroll
-    for (int m = 0; m < 4; ++m) {
+        for (int m = 0; m < 4; ++m) {
 #pragma unroll
-        for (int r = 0; r < 4; ++r) S[m][r] = state[(64 * half + 16 * m + 4 * g4 + r) * kD + col];
-        smax = abs_max(S[m], smax);
+            for (int r = 0; r < 4; ++r) {
+                if (STATES)
+                    S[m][r] = move && 64 * half + 16 * m + 4 * g4 + r == col ? 1.f : 0.f;
+                else
+                    S[m][r] = real(__builtin_amdgcn_raw_buffer_load_b32(buffer, at, (16 * m + r) * kD * 4, 0));
+            }
+            smax = abs_max(S[m], smax);
+        }
     }
     for (int i = begin; i < end; ++i) {
         const KdaBlock& T = tiles[(i - begin) & 1];
@@ -1175,10 +1218,77 @@ __global__ void __launch_bounds__(512) kda_chunk_kernel(PromptArgs a, const KdaB
         }
     }
     __syncthreads();
+    if (!STATES && !last_part) return;
+    const auto buffer = state_of(to);
 #pragma unroll
     for (int m = 0; m < 4; ++m)
 #pragma unroll
-        for (int r = 0; r < 4; ++r) state[(64 * half + 16 * m + 4 * g4 + r) * kD + col] = S[m][r];
+        for (int r = 0; r < 4; ++r)
+            __builtin_amdgcn_raw_buffer_store_b32(bits(S[m][r]), buffer, at, (16 * m + r) * kD * 4, 0);
+}
+
+// Chains the parts of each (sequence, head): S <- T_i S + U_i, into slot i (the
+// state that part i + 1 starts from); the last slot gets the state the sequence
+// came with, for its first part.  A workgroup has 16 value columns, a wave 32
+// rows of the product (f32 matrix products), and the rows meet in LDS.
+__global__ void __launch_bounds__(256) kda_chain_kernel(PromptArgs a, KdaParts parts) {
+    __shared__ f32x4 rows[2][8][64];
+    const int tid = threadIdx.x, wave = __builtin_amdgcn_readfirstlane(tid >> 6), lane = tid & 63, g4 = lane >> 4, l16 = lane & 15;
+    const int h = blockIdx.x % a.H, b = blockIdx.x / a.H, col = 16 * blockIdx.y + l16;
+    int first, last;
+    sequence(a, b, first, last);
+    const float* state = a.s_ptrs[b];
+    const int n = (last - first + parts.rows - 1) / parts.rows;
+    if (state == nullptr || n < 2) return;
+    const long long step = static_cast<long long>(a.H) * kD * kD;
+    const long long slot = (static_cast<long long>(first / parts.rows + b) * a.H + h) * kD * kD;
+    float* states = parts.states + slot;
+    const float* moves = parts.moves + slot;
+    state += static_cast<long long>(h) * kD * kD;
+
+    f32x4 S[8];
+#pragma unroll
+    for (int m = 0; m < 8; ++m)
+#pragma unroll
+        for (int r = 0; r < 4; ++r) S[m][r] = state[(16 * m + 4 * g4 + r) * kD + col];
+#pragma unroll
+    for (int m = 0; m < 2; ++m)
+#pragma unroll
+        for (int r = 0; r < 4; ++r)
+            states[(n - 1) * step + (32 * wave + 16 * m + 4 * g4 + r) * kD + col] =
+                state[(32 * wave + 16 * m + 4 * g4 + r) * kD + col];
+    f32x4 T[2][8], U[2];
+    const auto fetch = [&](int i) {
+#pragma unroll
+        for (int m = 0; m < 2; ++m) {
+#pragma unroll
+            for (int k = 0; k < 8; ++k)
+                T[m][k] = *reinterpret_cast<const f32x4*>(moves + i * step + (32 * wave + 16 * m + l16) * kD + 16 * k + 4 * g4);
+#pragma unroll
+            for (int r = 0; r < 4; ++r) U[m][r] = states[i * step + (32 * wave + 16 * m + 4 * g4 + r) * kD + col];
+        }
+    };
+    fetch(0);
+    for (int i = 0; i < n - 1; ++i) {
+        f32x4 X[2] = {U[0], U[1]};
+#pragma unroll
+        for (int k = 0; k < 8; ++k)
+#pragma unroll
+            for (int r = 0; r < 4; ++r)
+#pragma unroll
+                for (int m = 0; m < 2; ++m) X[m] = __builtin_amdgcn_mfma_f32_16x16x4f32(T[m][k][r], S[k][r], X[m], 0, 0, 0);
+        if (i + 1 < n - 1) fetch(i + 1);
+#pragma unroll
+        for (int m = 0; m < 2; ++m) {
+            rows[i & 1][2 * wave + m][lane] = X[m];
+#pragma unroll
+            for (int r = 0; r < 4; ++r)
+                states[i * step + (32 * wave + 16 * m + 4 * g4 + r) * kD + col] = X[m][r];
+        }
+        __syncthreads();
+#pragma unroll
+        for (int k = 0; k < 8; ++k) S[k] = rows[i & 1][k][lane];
+    }
 }
 
 // ------------------------------------------------------------------ single token
@@ -1271,29 +1381,57 @@ long long linear_work_bytes(int R, int B, int H) {
 }
 
 // The prepared chunks of a call, or of as many slots as fit kWorkCap: longer
-// calls go through the workspace in turns.
+// calls go through the workspace in turns.  Before them the parts' states.
 constexpr long long kWorkCap = 2ll << 30;
+constexpr int kFewHeads = 16, kPartRows = 512, kPartFill = 64;
+constexpr long long kPartBytes = 2ll * (kPartFill + kFewHeads) * kD * kD * 4;
 
-long long prompt_work_bytes(int R, int B, int H) {
+// Rows of a part.  Up to 16 (sequence, head) pairs of four workgroups each leave
+// three CUs of four idle; parts of R * H / 64 rows give each CU a workgroup.
+// In parts every chunk but those of a sequence's last part is walked three times
+// (U, T, outputs), so it takes four parts to gain: 8192 rows x 8 heads 197 us
+// in 8 parts against 399 in one piece; 2048 x 32 would be 125 in 2 against 109.
+static int kda_part_rows(int R, int B, int H) {
+    if (static_cast<long long>(B) * H > kFewHeads || R < 4 * kPartRows) return kWhole;
+    const long long rows = (static_cast<long long>(R) * H / kPartFill + kChunk - 1) / kChunk * kChunk;
+    return static_cast<int>(rows > kPartRows ? rows : kPartRows);
+}
+
+static long long parts_bytes(int R) { return R < 4 * kPartRows ? 0 : kPartBytes; }
+
+static long long blocks_bytes(int R, int B, int H) {
     const long long row = static_cast<long long>(H) * sizeof(KdaBlock), all = part_slots(R, B, kChunk) * row;
     const long long most = kWorkCap > row ? kWorkCap : row;
     return all < most ? all : most;
 }
 
+long long prompt_work_bytes(int R, int B, int H) { return parts_bytes(R) + blocks_bytes(R, B, H); }
+
 template <bool BF16>
 static hipError_t launch_kda(const PromptArgs& a, hipStream_t stream) {
-    const long long slots = part_slots(a.R, a.B, kChunk), heads = static_cast<long long>(a.B) * a.H;
-    const long long turn = prompt_work_bytes(a.R, a.B, a.H) / (static_cast<long long>(a.H) * sizeof(KdaBlock));
-    KdaBlock* const blocks = static_cast<KdaBlock*>(a.work);
+    const long long slots = part_slots(a.R, a.B, kChunk);
+    const long long turn = blocks_bytes(a.R, a.B, a.H) / (static_cast<long long>(a.H) * sizeof(KdaBlock));
+    KdaParts parts{};
+    parts.rows = turn < slots ? kWhole : kda_part_rows(a.R, a.B, a.H);
+    parts.states = static_cast<float*>(a.work);
+    const int units = static_cast<int>(part_slots(a.R, a.B, parts.rows) * a.H);   // at most 80 in parts
+    parts.moves = parts.states + static_cast<long long>(units) * kD * kD;
+    KdaBlock* const blocks = reinterpret_cast<KdaBlock*>(static_cast<char*>(a.work) + parts_bytes(a.R));
+    const auto grid = [&](int slices) { return dim3(static_cast<unsigned>((units + 7) / 8 * 8 * slices)); };
+    constexpr int slices = kD / kKdaCols;
     for (long long s0 = 0; s0 < slots; s0 += turn) {
         const int slot0 = static_cast<int>(s0), slot1 = static_cast<int>(s0 + turn < slots ? s0 + turn : slots);
         kda_prepare_kernel<BF16><<<dim3(static_cast<unsigned>((slot1 - slot0) * static_cast<long long>(a.H))),
                                    dim3(256), 0, stream>>>(a, blocks, slot0);
-        const dim3 grid(static_cast<unsigned>((heads + 7) / 8 * 8 * (kD / kKdaCols)));
+        if (parts.rows != kWhole) {
+            kda_chunk_kernel<BF16, false, true><<<grid(2 * slices), dim3(512), 0, stream>>>(a, blocks, slot0, slot1, parts, units);
+            const dim3 chain(static_cast<unsigned>(a.B * a.H), 8);
+            kda_chain_kernel<<<chain, dim3(256), 0, stream>>>(a, parts);
+        }
         if (a.o)
-            kda_chunk_kernel<BF16, true><<<grid, dim3(512), 0, stream>>>(a, blocks, slot0, slot1);
+            kda_chunk_kernel<BF16, true, false><<<grid(slices), dim3(512), 0, stream>>>(a, blocks, slot0, slot1, parts, units);
         else
-            kda_chunk_kernel<BF16, false><<<grid, dim3(512), 0, stream>>>(a, blocks, slot0, slot1);
+            kda_chunk_kernel<BF16, false, false><<<grid(slices), dim3(512), 0, stream>>>(a, blocks, slot0, slot1, parts, units);
         const hipError_t e = hipGetLastError();
         if (e != hipSuccess) return e;
     }

@@ -86,6 +86,15 @@ def test_prompt_long(op, dtype, H):
     _check(op, lens, xs, ref.states(6, 2, H))
 
 
+@pytest.mark.parametrize("op", ["linear", "kda"])
+@pytest.mark.parametrize("lens,H,g_scale", [([2100, 0, 600], 2, 0.02), ([2048], 16, 5.0), ([5, 2600], 1, 0.5),
+                                            ([513, 512, 511, 544], 4, 0.01), ([2560], 3, 0.0)], ids=str)
+def test_prompt_in_parts(op, lens, H, g_scale):
+    # few heads and long sequences: parts side by side, chained by their transitions
+    xs = _inputs(op, H + len(lens), sum(lens), H, torch.bfloat16, g_scale=g_scale)
+    _check(op, lens, xs, ref.states(23, len(lens), H))
+
+
 @pytest.mark.parametrize("Hk,H", [(1, 1), (1, 4), (2, 4), (3, 6), (5, 5)])
 @pytest.mark.parametrize("dtype", list(DTYPES))
 def test_linear_prompt_shared_key_heads(Hk, H, dtype):
