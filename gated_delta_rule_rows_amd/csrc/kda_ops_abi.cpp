@@ -45,9 +45,9 @@ int prompt(const char* fn, bool linear, const PromptArgs& a, int in_dtype, long 
     if ((rc = check_dtype(fn, in_dtype)) || (rc = check_heads(fn, a.Hk, a.H)) ||
         (rc = check_packed(fn, a.R, a.B)))
         return rc;
-    if (static_cast<long long>(a.B) * a.H > INT_MAX / 8)
-        return refuse(KDA_ERR_RANGE, "%s: B*H=%lld too large", fn,
-                      static_cast<long long>(a.B) * a.H);
+    if (static_cast<long long>(a.R) * a.H > 1ll << 40)
+        return refuse(KDA_ERR_RANGE, "%s: R*H=%lld too large", fn,
+                      static_cast<long long>(a.R) * a.H);
     const long long need = linear ? linear_work_bytes(a.R, a.B, a.H) : prompt_work_bytes(a.R, a.B, a.H);
     if ((rc = check_work(fn, work_bytes, need))) return rc;
     const unsigned es = in_dtype == KDA_IN_BF16 ? 2 : 4;
@@ -147,9 +147,9 @@ int kda_linear_step(float* const* s_ptrs, const void* q, const void* k, const vo
 
 long long kda_logprobs_work_bytes(int t, int V, int n_top) {
     const char* fn = "kda_logprobs_work_bytes";
-    if (t < 1 || V < 1 || n_top < 0 || n_top > KDA_TOP_MAX) {
-        refuse(KDA_ERR_RANGE, "%s: t=%d, V=%d, n_top=%d: need t, V >= 1, n_top in 0..%d", fn, t, V,
-               n_top, KDA_TOP_MAX);
+    if (t < 1 || V < 1 || V > 1 << 30 || n_top < 0 || n_top > KDA_TOP_MAX) {
+        refuse(KDA_ERR_RANGE, "%s: t=%d, V=%d, n_top=%d: need t >= 1, V in 1..2^30, n_top in 0..%d", fn,
+               t, V, n_top, KDA_TOP_MAX);
         return -1;
     }
     return logprob_work_bytes(t, V, n_top);
@@ -162,7 +162,7 @@ int kda_logprobs(const void* logits, int t, int V, long long ld, int in_dtype,
     int rc;
     if ((rc = check_dtype(fn, in_dtype))) return rc;
     if (t < 1) return refuse(KDA_ERR_RANGE, "%s: t=%d, need t >= 1", fn, t);
-    if (V < 1) return refuse(KDA_ERR_RANGE, "%s: V=%d, need V >= 1", fn, V);
+    if (V < 1 || V > 1 << 30) return refuse(KDA_ERR_RANGE, "%s: V=%d outside 1..2^30", fn, V);
     if (n_top < 0 || n_top > KDA_TOP_MAX)
         return refuse(KDA_ERR_RANGE, "%s: n_top=%d outside 0..%d", fn, n_top, KDA_TOP_MAX);
     if (t == 1) ld = V;

@@ -58,7 +58,7 @@ extern "C" {
 #define KDA_CONV_RING_ROWS 3          /* short-conv history: kernel size 4 keeps 3 raw rows */
 #define KDA_MAX_PREV_ROUNDS 4         /* earlier rounds one kda_verify_round_multi can replay */
 #define KDA_PROMPT_ROWS_MAX 268435456 /* packed rows of one prompt call */
-#define KDA_PROMPT_SEQS_MAX 1048576   /* sequences of one prompt call */
+#define KDA_PROMPT_SEQS_MAX 4096      /* sequences of one prompt call */
 #define KDA_TOP_MAX 32                /* alternatives kda_logprobs lists for a row */
 
 enum { KDA_IN_F32 = 0, KDA_IN_BF16 = 1 };
@@ -411,7 +411,8 @@ int kda_copy_batch(const uint64_t* table, int n, long long words, void* stream);
  *   The rows run in chunks (the recurrence is linear in the state, so a chunk
  *   is a few matrix products), which sums in another order than the row scan:
  *   results agree with kda_scan_rows to f32 rounding, not bit for bit.  They
- *   are deterministic, and do not depend on the other sequences of the call.
+ *   are deterministic, and do not depend on what the other sequences hold (the
+ *   call's R, B and H choose how it is divided).
  *   s_ptrs      : DEVICE array of B pointers, s_ptrs[b] to sequence b's state
  *                 [H][128][128] f32 (16-byte aligned; zero it for a fresh
  *                 sequence).  A NULL entry leaves sequence b out: its rows of
@@ -431,7 +432,9 @@ int kda_copy_batch(const uint64_t* table, int n, long long words, void* stream);
  *                 NULL when none are needed.  Calls that can run at the same
  *                 time need different work buffers.
  *   0 <= R <= KDA_PROMPT_ROWS_MAX, 1 <= B <= KDA_PROMPT_SEQS_MAX,
- *   1 <= H <= 65535.  With R = 0 nothing is enqueued.
+ *   1 <= H <= 65535, R * H <= 2^40.  With R = 0 nothing is enqueued.
+ *   Products keep f32's precision while the values that meet in one chunk of 32
+ *   rows (k, q; v and the state by column) lie within 2^16 of the largest.
  */
 int kda_prompt(float* const* s_ptrs, const int32_t* offsets, const void* q, const void* k,
                const void* v, const void* g, const void* beta, float* o, int R, int B, int H,
@@ -490,7 +493,8 @@ int kda_linear_step(float* const* s_ptrs, const void* q, const void* k, const vo
  *   work    : kda_logprobs_work_bytes(t, V, n_top) bytes, 16-byte aligned, in
  *             any state on entry; NULL when none are needed.  Calls that can
  *             run at the same time need different work buffers.
- *   logits, ld, in_dtype as kda_accept_greedy; t, V >= 1, t * ld <= 2^40.
+ *   logits, ld, in_dtype as kda_accept_greedy; t >= 1, 1 <= V <= 2^30,
+ *   t * ld <= 2^40.
  */
 int kda_logprobs(const void* logits, int t, int V, long long ld, int in_dtype,
                  const uint32_t* tokens, int n_top, float* lp, float* entropy, uint32_t* top_ids,

@@ -86,7 +86,7 @@ def test_prompt_refusals(lib, b, call):
     no(ERR_RANGE, "B=", B=_header_constant("KDA_PROMPT_SEQS_MAX") + 1)
     no(ERR_RANGE, "H=0", H=0)
     no(ERR_RANGE, "H=", H=65536)
-    no(ERR_RANGE, "B*H", B=1 << 20, H=60000)
+    no(ERR_RANGE, "R*H", R=1 << 28, H=65532)
     for name in ("s", "off", "q", "k", "v", "g"):
         no(ERR_ARG, "NULL", **{name: None})
     for name, step in (("s", 4), ("off", 2), ("q", 4), ("k", 8), ("v", 2), ("o", 4), ("g", 2)):
@@ -157,6 +157,7 @@ def test_logprobs_refusals(lib, b):
     no(ERR_ARG, "in_dtype", dt=5)
     no(ERR_RANGE, "t=0", t=0)
     no(ERR_RANGE, "V=0", V=0)
+    no(ERR_RANGE, "outside 1..2^30", V=(1 << 30) + 1, ld=1 << 31)
     no(ERR_RANGE, "n_top=-1", n=-1)
     no(ERR_RANGE, "n_top=33", n=33)
     no(ERR_RANGE, "ld=99", ld=99)
