@@ -207,9 +207,15 @@ __device__ __forceinline__ void values(uint4 u, float (&x)[BF16 ? 8 : 4]) {
 }
 
 __device__ __forceinline__ Sums wave_sums(Sums s) {
+    float m = s.m;
 #pragma unroll
-    for (int d = 32; d >= 1; d >>= 1)
-        join(s, Sums{__shfl_xor(s.m, d), __shfl_xor(s.z, d), __shfl_xor(s.w, d)});
+    for (int d = 32; d >= 1; d >>= 1) m = fmaxf(m, __shfl_xor(m, d));
+    if (m > s.m) move_to(s, m);
+#pragma unroll
+    for (int d = 32; d >= 1; d >>= 1) {
+        s.z += __shfl_xor(s.z, d);
+        s.w += __shfl_xor(s.w, d);
+    }
     return s;
 }
 
@@ -308,6 +314,12 @@ __device__ __forceinline__ void finish(const LogprobArgs& a, const void* row, lo
     const int tid = threadIdx.x, n = a.n_top;
     Sums s{-kInf, 0.f, 0.f};
     Key head = 0;
+    uint32_t tok = kNoToken;
+    float given = 0.f;
+    if (a.lp && tid == 0) {
+        tok = a.tokens[r];
+        if (tok < static_cast<uint32_t>(a.V)) given = logit<BF16>(row, tok);
+    }
     Key ahead[AHEAD];
 #pragma unroll
     for (int i = 0; i < AHEAD; ++i) ahead[i] = i * THREADS + tid < W * n ? lists[i * THREADS + tid] : 0;
@@ -330,10 +342,8 @@ __device__ __forceinline__ void finish(const LogprobArgs& a, const void* row, lo
     const float log_z = logf(s.z);
     if (tid == 0) {
         if (a.lp) {
-            const uint32_t tok = a.tokens[r];
             float lp = __builtin_nanf("");
-            if (!bad && tok < static_cast<uint32_t>(a.V))
-                lp = empty ? -kInf : logit<BF16>(row, tok) - s.m - log_z;
+            if (!bad && tok < static_cast<uint32_t>(a.V)) lp = empty ? -kInf : given - s.m - log_z;
             a.lp[r] = lp;
         }
         if (a.entropy) a.entropy[r] = bad ? __builtin_nanf("") : empty ? 0.f : log_z - s.w / s.z;
@@ -342,7 +352,7 @@ __device__ __forceinline__ void finish(const LogprobArgs& a, const void* row, lo
     // only keys at or above the n-th best head can be among the n best
     if (W > n && head != 0) {
         int rank = 0;
-#pragma unroll 8
+#pragma unroll 16
         for (int i = 0; i < W; ++i) rank += heads[i] > head;
         if (rank == n - 1) bar = head;
     }
