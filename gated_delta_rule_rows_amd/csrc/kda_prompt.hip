@@ -18,6 +18,7 @@
 
 #include <cstdint>
 
+#include "kda.h"
 #include "kda_launch.h"
 #include "kda_ops.h"
 
@@ -47,35 +48,51 @@ struct Part {
     int last;
 };
 
+// Inclusive running maximum over the lanes.
+__device__ __forceinline__ int running_max(int x) {
+    const int lane = threadIdx.x & 63;
+#pragma unroll
+    for (int d = 1; d < 64; d <<= 1) {
+        const int y = __shfl_up(x, d);
+        if (lane >= d) x = max(x, y);
+    }
+    return x;
+}
+
 // The sequence of a slot: the last one whose slots begin at or before it.  The
 // table is read with a running maximum, clamped to [0, R], so that any table
-// gives disjoint rows and slots; every wave runs this by itself.
+// gives disjoint rows and slots; every wave runs this by itself.  Beyond 64
+// sequences each lane first takes 1/64 of the table (64 entries at most), to
+// find the stretch of it that is searched.
 __device__ __forceinline__ Part find_part(const PromptArgs& a, int part_rows, int slot) {
+    static_assert(KDA_PROMPT_SEQS_MAX <= 64 * 64, "two levels of 64");
     const int lane = threadIdx.x & 63;
+    const auto row = [&](int b) { return min(max(a.offsets[b], 0), a.R); };
     Part f{-1, 0, 0, 0};
-    int carry = 0;
-    for (int b0 = 0; b0 < a.B; b0 += 64) {
-        const int b = b0 + lane;
-        int x = b < a.B ? min(max(a.offsets[b], 0), a.R) : a.R;
-        x = max(x, carry);
-#pragma unroll
-        for (int d = 1; d < 64; d <<= 1) {
-            const int y = __shfl_up(x, d);
-            if (lane >= d) x = max(x, y);
-        }
-        const uint64_t before = __ballot(b < a.B && x / part_rows + b <= slot);
-        if (before == 0) break;
-        const int n = __builtin_popcountll(before) - 1;
-        f.b = b0 + n;
-        f.first = __builtin_amdgcn_readlane(x, n);
-        carry = __builtin_amdgcn_readlane(x, 63);
-        if (n < 63) break;
+    int b0 = 0, n = min(a.B, 64), before = 0;   // the stretch, and the largest entry before it
+    if (a.B > 64) {
+        const int each = (a.B + 63) / 64, from = lane * each, to = min(from + each, a.B);
+        int x = 0;
+        for (int b = from; b < to; ++b) x = max(x, row(b));
+        const int upto = running_max(x);
+        int ahead = __shfl_up(upto, 1);
+        if (lane == 0) ahead = 0;
+        const uint64_t mask = __ballot(from < to && max(ahead, row(min(from, a.B - 1))) / part_rows + from <= slot);
+        if (mask == 0) return f;
+        const int at = 63 - __builtin_clzll(mask);
+        b0 = at * each;
+        n = min(each, a.B - b0);
+        before = __builtin_amdgcn_readlane(ahead, at);
     }
-    if (f.b < 0) return f;
-    f.b = __builtin_amdgcn_readfirstlane(f.b);
-    f.index = slot - (f.first / part_rows + f.b);
-    f.last = min(max(a.offsets[f.b + 1], f.first), a.R);
-    if (f.first + static_cast<long long>(f.index) * part_rows >= f.last) f.b = -1;
+    const int b = b0 + lane;
+    const int x = running_max(max(before, lane < n ? row(b) : 0));
+    const uint64_t mask = __ballot(lane < n && x / part_rows + b <= slot);
+    if (mask == 0) return f;
+    const int at = 63 - __builtin_clzll(mask);
+    f.first = __builtin_amdgcn_readlane(x, at);
+    f.index = slot - (f.first / part_rows + b0 + at);
+    f.last = min(max(a.offsets[b0 + at + 1], f.first), a.R);
+    if (f.first + static_cast<long long>(f.index) * part_rows < f.last) f.b = b0 + at;
     return f;
 }
 
@@ -84,12 +101,7 @@ __device__ __forceinline__ Part find_part(const PromptArgs& a, int part_rows, in
 __device__ __forceinline__ int longest_first(const PromptArgs& a, int place) {
     if (a.B == 1 || a.B > 64) return place;
     const int lane = threadIdx.x & 63;
-    int first = lane < a.B ? min(max(a.offsets[lane], 0), a.R) : a.R;
-#pragma unroll
-    for (int d = 1; d < 64; d <<= 1) {
-        const int y = __shfl_up(first, d);
-        if (lane >= d) first = max(first, y);
-    }
+    const int first = running_max(lane < a.B ? min(max(a.offsets[lane], 0), a.R) : 0);
     const int last = lane < a.B ? min(max(a.offsets[lane + 1], first), a.R) : first;
     const int rows = lane < a.B ? last - first : -1;
     int rank = 0;
@@ -1048,8 +1060,14 @@ __global__ void __launch_bounds__(512) kda_chunk_kernel(PromptArgs a, const KdaB
     if (unit >= units) return;
     const int h = unit % a.H;
     const int place = unit / a.H;
-    const Part f = find_part(a, parts.rows, parts.rows == kWhole ? longest_first(a, place) : place);
-    if (f.b < 0) return;
+    Part f{0, 0, 0, 0};
+    if (parts.rows == kWhole) {
+        f.b = longest_first(a, place);
+        sequence(a, f.b, f.first, f.last);
+    } else {
+        f = find_part(a, parts.rows, place);
+        if (f.b < 0) return;
+    }
     const int first = f.first, last = f.last;
     const int own = first / kChunk + f.b, chunks = (last - first + kChunk - 1) / kChunk;
     const int part_begin = f.index * (parts.rows / kChunk), part_end = min(part_begin + parts.rows / kChunk, chunks);

@@ -241,10 +241,35 @@ def test_prompt_rows_past_32_bit_offsets(op):
 
 
 @pytest.mark.parametrize("op", ["linear", "kda"])
-def test_prompt_many_short_sequences(op):
-    lens = [(7 * i) % 5 for i in range(300)]
+@pytest.mark.parametrize("B", [64, 65, 300, 4096])
+def test_prompt_many_short_sequences(op, B):
+    lens = [(7 * i) % 5 if i % 64 < 50 else 0 for i in range(B)]
+    lens[B // 2] = 70
     xs = _inputs(op, 21, sum(lens), 1)
-    _check(op, lens, xs, ref.states(18, 300, 1))
+    _check(op, lens, xs, ref.states(18, B, 1))
+
+
+@pytest.mark.parametrize("op", ["linear", "kda"])
+def test_prompt_long_tables_with_bad_entries(op):
+    # 200 entries, some far out or falling: as if by the running maximum
+    B, R = 200, 900
+    gen = torch.Generator().manual_seed(24)
+    off = torch.sort(torch.randint(0, R + 1, (B + 1,), generator=gen)).values.to(torch.int32)
+    off[3], off[70], off[150], off[199] = -5, 0, 2 ** 31 - 1, -2 ** 31
+    read = torch.cummax(off.clamp(0, R), 0).values.tolist()
+    xs = _inputs(op, 25, R, 1)
+    S0 = ref.states(26, B, 1)
+    S = S0.cuda()
+    o = torch.full((R, 1, D), 7.0, device="cuda")
+    CALL[op](S, None, _cuda(*xs), o, off=off.cuda())
+    for b in range(B):
+        lo, hi = read[b], read[b + 1]
+        if lo == hi:
+            assert torch.equal(S[b].cpu(), S0[b]), b
+        else:
+            want_o, want_S = ROWS[op](S0[b], *(x[lo:hi] for x in xs))
+            assert ref.relative(S[b], want_S) <= ref.tolerance(hi - lo), b
+            assert ref.relative(o[lo:hi], want_o) <= ref.tolerance(hi - lo), b
 
 
 @pytest.mark.parametrize("op", ["linear", "kda"])
