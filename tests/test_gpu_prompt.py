@@ -171,6 +171,35 @@ def test_prompt_scales_with_the_state_and_values(op, scale):
 
 
 @pytest.mark.parametrize("op", ["linear", "kda"])
+def test_prompt_columns_of_very_different_size(op):
+    # value columns never meet: powers of two by column come out to the bit
+    lens = [100, 33]
+    xs = list(_inputs(op, 27, 133, 2, g_scale=0.3))
+    S0 = ref.states(28, 2, 2)
+    scale = torch.exp2((torch.arange(D) * 7 % 61 - 30).float())
+    got = []
+    for f in (torch.ones(D), scale):
+        S, ys = (S0 * f).cuda(), list(xs)
+        ys[2] = xs[2] * f
+        o = torch.empty(xs[2].shape, device="cuda")
+        CALL[op](S, lens, _cuda(*ys), o)
+        got.append((o.cpu() / f, S.cpu() / f))
+    assert torch.equal(got[0][0], got[1][0]) and torch.equal(got[0][1], got[1][1])
+
+
+@pytest.mark.parametrize("op", ["linear", "kda"])
+def test_prompt_rows_of_very_different_size(op):
+    # rows of v over 2^16, beta of 0 in the largest, a state far above what the rows add
+    lens = [96]
+    xs = list(_inputs(op, 29, 96, 2, g_scale=0.3))
+    size = torch.exp2((torch.arange(96) * 5 % 17).float())
+    xs[2] = xs[2] * size[:, None, None]
+    if op == "kda":
+        xs[4] = torch.where(size[:, None] > 2.0 ** 15, torch.zeros(()), xs[4])
+    _check(op, lens, xs, ref.states(30, 1, 2, 1000.0))
+
+
+@pytest.mark.parametrize("op", ["linear", "kda"])
 def test_prompt_leaves_rows_outside_its_sequences(op):
     # rows before, between and behind the sequences, and a sequence with no state
     R, H = 120, 2
@@ -273,10 +302,10 @@ def test_prompt_long_tables_with_bad_entries(op):
 
 
 @pytest.mark.parametrize("op", ["linear", "kda"])
-def test_prompt_graph_replays_and_two_streams(op):
+@pytest.mark.parametrize("lens", [[[150, 20], [64, 300]], [[2100, 20], [7, 2300]]], ids=["chunks", "parts"])
+def test_prompt_graph_replays_and_two_streams(op, lens):
     """A captured call replays to the eager bits, and two calls on two streams with a
     workspace each do not disturb each other."""
-    lens = [[150, 20], [64, 300]]
     H = 4
     xs = [_cuda(*_inputs(op, 22 + i, sum(n), H, torch.bfloat16)) for i, n in enumerate(lens)]
     S0 = [ref.states(19 + i, 2, H).cuda() for i in range(2)]
