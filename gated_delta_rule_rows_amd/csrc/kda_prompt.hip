@@ -9,8 +9,8 @@
 //
 // Prompts run in chunks of 32 rows, whose rows meet in matrix products.  On an
 // MI355X, calls in a loop (the bytes that a call cannot do without, at the 4.69
-// TB/s of a large copy, in brackets): KDA 4096 rows x 64 heads bf16 426 us (88),
-// 8192 x 8 bf16 233 us (22), a ragged batch of 2,586 x 32 f32 160 us (52);
+// TB/s of a large copy, in brackets): KDA 4096 rows x 64 heads bf16 420 us (88),
+// 8192 x 8 bf16 233 us (22), a ragged batch of 2,586 x 32 f32 158 us (52);
 // linear 4096 x 64 bf16 152-158 us (74), 16384 x 8 f32 153-169 us (58); the
 // single-token step over 34 x 15 x 64 states 837 us (919: it writes in place).
 
@@ -69,6 +69,13 @@ __device__ __forceinline__ Part find_part(const PromptArgs& a, int part_rows, in
     const int lane = threadIdx.x & 63;
     const auto row = [&](int b) { return min(max(a.offsets[b], 0), a.R); };
     Part f{-1, 0, 0, 0};
+    if (a.B == 1) {
+        f.first = row(0);
+        f.index = slot - f.first / part_rows;
+        f.last = max(row(1), f.first);
+        if (f.index >= 0 && f.first + static_cast<long long>(f.index) * part_rows < f.last) f.b = 0;
+        return f;
+    }
     int b0 = 0, n = min(a.B, 64), before = 0;   // the stretch, and the largest entry before it
     if (a.B > 64) {
         const int each = (a.B + 63) / 64, from = lane * each, to = min(from + each, a.B);
@@ -774,18 +781,17 @@ __global__ void __launch_bounds__(256) kda_prepare_kernel(PromptArgs a, KdaBlock
     const int tb = wave != 0, jb = wave == 1;
     const bool low = wave >= 2, wantA = wave != 3, wantB = wave != 2;
     const int tr = 16 * tb + l16, jr = 16 * jb + l16;
-    // (f32 rows are read where they are used: ahead they would take 96 registers,
-    // and with them a third workgroup from the CU: 87 us against 75 for the
-    // ragged batch of 2,586 rows x 32 heads)
+    // (f32 rows are read one step ahead of their use: all at once they would take
+    // 96 registers, and with them a third workgroup from the CU: 87 us against 74
+    // for the ragged batch of 2,586 rows x 32 heads)
     Eight<BF16> ek[4], et[4], eq[4];
     const auto rows = [&](int ks) {
         load_eight<BF16>(ek[ks], rk, jr, 32 * ks + 8 * g4);
         if (low && wantA) load_eight<BF16>(et[ks], rk, tr, 32 * ks + 8 * g4);
         if (wantB) load_eight<BF16>(eq[ks], rq, tr, 32 * ks + 8 * g4);
     };
-    if (BF16)
 #pragma unroll
-        for (int ks = 0; ks < 4; ++ks) rows(ks);
+    for (int ks = 0; ks < (BF16 ? 4 : 1); ++ks) rows(ks);
     if (tid < kChunk)
         beta[tid] = tid < n ? load<BF16>(a.beta, static_cast<long long>(t0 + tid) * a.H + h) : 0.f;
 
@@ -849,7 +855,7 @@ __global__ void __launch_bounds__(256) kda_prepare_kernel(PromptArgs a, KdaBlock
     for (int ks = 0; ks < 4; ++ks) {
         const int c = 32 * ks + 8 * g4;
         float x[8], kj[8], ft[8];
-        if (!BF16) rows(ks);
+        if (!BF16 && ks < 3) rows(ks + 1);
         eight_values<BF16>(ek[ks], x);
 #pragma unroll
         for (int i = 0; i < 8; ++i) {
