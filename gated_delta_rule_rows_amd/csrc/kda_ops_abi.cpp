@@ -15,7 +15,8 @@ using namespace kda;
 
 namespace {
 
-constexpr unsigned long long kRow = kD;   // elements of a row of one head
+constexpr unsigned long long kRow = kD;         // elements of a row of one head
+constexpr int kLogprobRows = (1 << 26) - 1;     // a wave each, 2^32 threads
 
 int check_heads(const char* fn, int Hk, int H) {
     if (H < 1 || H > 65535) return refuse(KDA_ERR_RANGE, "%s: H=%d outside 1..65535", fn, H);
@@ -24,11 +25,16 @@ int check_heads(const char* fn, int Hk, int H) {
     return KDA_OK;
 }
 
-int check_packed(const char* fn, int R, int B) {
+// The products keep every launch below the 2^32 threads of a grid.
+int check_packed(const char* fn, int R, int B, int H) {
     if (R < 0 || R > KDA_PROMPT_ROWS_MAX)
         return refuse(KDA_ERR_RANGE, "%s: R=%d outside 0..%d", fn, R, KDA_PROMPT_ROWS_MAX);
     if (B < 1 || B > KDA_PROMPT_SEQS_MAX)
         return refuse(KDA_ERR_RANGE, "%s: B=%d outside 1..%d", fn, B, KDA_PROMPT_SEQS_MAX);
+    if (static_cast<long long>(R) * H > 1ll << 34)
+        return refuse(KDA_ERR_RANGE, "%s: R*H=%lld too large", fn, static_cast<long long>(R) * H);
+    if (static_cast<long long>(B) * H > 1ll << 20)
+        return refuse(KDA_ERR_RANGE, "%s: B*H=%lld too large", fn, static_cast<long long>(B) * H);
     return KDA_OK;
 }
 
@@ -43,11 +49,8 @@ int prompt(const char* fn, bool linear, const PromptArgs& a, int in_dtype, long 
            void* stream) {
     int rc;
     if ((rc = check_dtype(fn, in_dtype)) || (rc = check_heads(fn, a.Hk, a.H)) ||
-        (rc = check_packed(fn, a.R, a.B)))
+        (rc = check_packed(fn, a.R, a.B, a.H)))
         return rc;
-    if (static_cast<long long>(a.R) * a.H > 1ll << 40)
-        return refuse(KDA_ERR_RANGE, "%s: R*H=%lld too large", fn,
-                      static_cast<long long>(a.R) * a.H);
     const long long need = linear ? linear_work_bytes(a.R, a.B, a.H) : prompt_work_bytes(a.R, a.B, a.H);
     if ((rc = check_work(fn, work_bytes, need))) return rc;
     const unsigned es = in_dtype == KDA_IN_BF16 ? 2 : 4;
@@ -81,7 +84,7 @@ int prompt(const char* fn, bool linear, const PromptArgs& a, int in_dtype, long 
 extern "C" {
 
 long long kda_prompt_work_bytes(int R, int B, int H) {
-    if (check_heads("kda_prompt_work_bytes", 1, H) || check_packed("kda_prompt_work_bytes", R, B))
+    if (check_heads("kda_prompt_work_bytes", 1, H) || check_packed("kda_prompt_work_bytes", R, B, H))
         return -1;
     return prompt_work_bytes(R, B, H);
 }
@@ -98,7 +101,7 @@ int kda_prompt(float* const* s_ptrs, const int32_t* offsets, const void* q, cons
 
 long long kda_linear_prompt_work_bytes(int R, int B, int H) {
     if (check_heads("kda_linear_prompt_work_bytes", 1, H) ||
-        check_packed("kda_linear_prompt_work_bytes", R, B))
+        check_packed("kda_linear_prompt_work_bytes", R, B, H))
         return -1;
     return linear_work_bytes(R, B, H);
 }
@@ -123,7 +126,7 @@ int kda_linear_step(float* const* s_ptrs, const void* q, const void* k, const vo
         return rc;
     if (B < 1) return refuse(KDA_ERR_RANGE, "%s: B=%d, need B >= 1", fn, B);
     const unsigned long long n = static_cast<unsigned long long>(L) * B;
-    if (n > INT_MAX || n * H > INT_MAX)
+    if (n > INT_MAX || n * H >= 1u << 24)   // 2^32 threads
         return refuse(KDA_ERR_RANGE, "%s: L*B*H=%llu too large", fn, n * H);
     const unsigned es = in_dtype == KDA_IN_BF16 ? 2 : 4;
     const Span in[] = {
@@ -147,8 +150,8 @@ int kda_linear_step(float* const* s_ptrs, const void* q, const void* k, const vo
 
 long long kda_logprobs_work_bytes(int t, int V, int n_top) {
     const char* fn = "kda_logprobs_work_bytes";
-    if (t < 1 || V < 1 || V > 1 << 30 || n_top < 0 || n_top > KDA_TOP_MAX) {
-        refuse(KDA_ERR_RANGE, "%s: t=%d, V=%d, n_top=%d: need t >= 1, V in 1..2^30, n_top in 0..%d", fn,
+    if (t < 1 || t > kLogprobRows || V < 1 || V > 1 << 30 || n_top < 0 || n_top > KDA_TOP_MAX) {
+        refuse(KDA_ERR_RANGE, "%s: t=%d, V=%d, n_top=%d: need t in 1..2^26-1, V in 1..2^30, n_top in 0..%d", fn,
                t, V, n_top, KDA_TOP_MAX);
         return -1;
     }
@@ -161,7 +164,8 @@ int kda_logprobs(const void* logits, int t, int V, long long ld, int in_dtype,
     const char* fn = "kda_logprobs";
     int rc;
     if ((rc = check_dtype(fn, in_dtype))) return rc;
-    if (t < 1) return refuse(KDA_ERR_RANGE, "%s: t=%d, need t >= 1", fn, t);
+    if (t < 1 || t > kLogprobRows)
+        return refuse(KDA_ERR_RANGE, "%s: t=%d outside 1..%d", fn, t, kLogprobRows);
     if (V < 1 || V > 1 << 30) return refuse(KDA_ERR_RANGE, "%s: V=%d outside 1..2^30", fn, V);
     if (n_top < 0 || n_top > KDA_TOP_MAX)
         return refuse(KDA_ERR_RANGE, "%s: n_top=%d outside 0..%d", fn, n_top, KDA_TOP_MAX);

@@ -432,7 +432,7 @@ int kda_copy_batch(const uint64_t* table, int n, long long words, void* stream);
  *                 NULL when none are needed.  Calls that can run at the same
  *                 time need different work buffers.
  *   0 <= R <= KDA_PROMPT_ROWS_MAX, 1 <= B <= KDA_PROMPT_SEQS_MAX,
- *   1 <= H <= 65535, R * H <= 2^40.  With R = 0 nothing is enqueued.
+ *   1 <= H <= 65535, R * H <= 2^34, B * H <= 2^20.  With R = 0 nothing is enqueued.
  *   Products keep f32's precision while the values that meet in one chunk of 32
  *   rows (k, q; v and the state by column) lie within 2^16 of the largest.
  */
@@ -461,7 +461,7 @@ long long kda_prompt_work_bytes(int R, int B, int H);
  *   s_ptrs, offsets, work : as kda_prompt; for the step s_ptrs[l*B + b] is
  *                 session b's layer-l state, and a NULL entry leaves that
  *                 session out (its row of o is not written).
- *   The step takes any B >= 1 with L*B*H < 2^31.
+ *   The step takes any B >= 1 with L*B*H < 2^24.
  */
 int kda_linear_prompt(float* const* s_ptrs, const int32_t* offsets, const void* q, const void* k,
                       const void* v, const float* g, float* o, int R, int B, int Hk, int H,
@@ -493,7 +493,7 @@ int kda_linear_step(float* const* s_ptrs, const void* q, const void* k, const vo
  *   work    : kda_logprobs_work_bytes(t, V, n_top) bytes, 16-byte aligned, in
  *             any state on entry; NULL when none are needed.  Calls that can
  *             run at the same time need different work buffers.
- *   logits, ld, in_dtype as kda_accept_greedy; t >= 1, 1 <= V <= 2^30,
+ *   logits, ld, in_dtype as kda_accept_greedy; 1 <= t < 2^26, 1 <= V <= 2^30,
  *   t * ld <= 2^40.
  */
 int kda_logprobs(const void* logits, int t, int V, long long ld, int in_dtype,

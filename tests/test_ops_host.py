@@ -248,3 +248,20 @@ def test_python_refusals_on_device_tensors():
         kda.kda_logprobs(logits, top_lp=torch.zeros(4, 3, **d), work=w)
     with pytest.raises(kda.KdaError, match="rows would overlap"):
         kda.kda_logprobs(torch.zeros(60, **d).as_strided((4, 50), (3, 1)), tok, lp, work=w)
+
+
+def test_grids_beyond_the_launch_limit_are_refused(lib, b):
+    """A grid holds fewer than 2^32 threads; what would need more is refused before any launch."""
+    for call, space in ((_prompt, lib.kda_prompt_work_bytes), (_linear, lib.kda_linear_prompt_work_bytes)):
+        _refused(lib, call(lib, b, B=4096, H=257, Hk=257) if call is _linear else call(lib, b, B=4096, H=257),
+                 ERR_RANGE, "B*H")
+        _refused(lib, call(lib, b, R=1 << 28, H=65) if call is _prompt else call(lib, b, R=1 << 28, H=65, Hk=65),
+                 ERR_RANGE, "R*H")
+        assert space(40, 4096, 257) == -1
+        assert space(40, 4096, 256) >= 0
+        assert space(1 << 28, 1, 65) == -1
+        assert space(1 << 28, 1, 64) > 0
+    _refused(lib, _step(lib, b, L=1 << 10, B=1 << 12), ERR_RANGE, "L*B*H")      # 4 heads: 2^24
+    _refused(lib, _logprobs(lib, b, t=1 << 26), ERR_RANGE, "t=67108864")
+    assert lib.kda_logprobs_work_bytes(1 << 26, 1, 0) == -1
+    assert lib.kda_logprobs_work_bytes((1 << 26) - 1, 1, 0) == 0
