@@ -270,6 +270,33 @@ def test_prompt_rows_past_32_bit_offsets(op):
 
 
 @pytest.mark.parametrize("op", ["linear", "kda"])
+def test_prompt_sequence_across_a_full_workspace(op):
+    # 581 slots of prepared chunks, of which the workspace holds 574: the second sequence's
+    # chunks (slots 572..576) are walked in two turns, the third's in the last
+    H, R, cuts = 64, 18500, [0, 18300, 18450, 18500]
+    xs = _inputs(op, 25, R - cuts[1], H, torch.bfloat16, g_scale=0.1)
+    S0 = ref.states(26, 3, H)
+    big = []
+    for x in xs:
+        y = torch.zeros(R, *x.shape[1:], dtype=x.dtype, device="cuda")
+        y[cuts[1]:] = x.cuda()
+        big.append(y)
+    S = S0.cuda()
+    ptrs = _pointers(S)
+    ptrs[0] = 0
+    o = torch.full((R, H, D), 7.0, device="cuda")
+    CALL[op](S, None, big, o, off=torch.tensor(cuts, dtype=torch.int32, device="cuda"), ptrs=ptrs)
+    assert torch.equal(S[0].cpu(), S0[0])
+    assert (o[:cuts[1]] == 7.0).all()
+    for b in (1, 2):
+        part = slice(cuts[b] - cuts[1], cuts[b + 1] - cuts[1])
+        want_o, want_S = ROWS[op](S0[b], *(x[part] for x in xs))
+        tol = ref.tolerance(cuts[b + 1] - cuts[b])
+        assert ref.relative(o[cuts[b]:cuts[b + 1]], want_o) <= tol
+        assert ref.relative(S[b], want_S) <= tol
+
+
+@pytest.mark.parametrize("op", ["linear", "kda"])
 @pytest.mark.parametrize("B", [64, 65, 300, 4096])
 def test_prompt_many_short_sequences(op, B):
     lens = [(7 * i) % 5 if i % 64 < 50 else 0 for i in range(B)]
