@@ -410,8 +410,8 @@ int kda_copy_batch(const uint64_t* table, int n, long long words, void* stream);
  * session starts from; there is no snapshot and no row limit.
  *   The rows run in chunks (the recurrence is linear in the state, so a chunk
  *   is a few matrix products), which sums in another order than the row scan:
- *   results agree with kda_scan_rows to f32 rounding, not bit for bit.  They
- *   are deterministic, and do not depend on what the other sequences hold (the
+ *   results agree with kda_scan_rows to a few roundings of f32, not bit for bit.
+ *   They are deterministic, and do not depend on what the other sequences hold (the
  *   call's R, B and H choose how it is divided).
  *   s_ptrs      : DEVICE array of B pointers, s_ptrs[b] to sequence b's state
  *                 [H][128][128] f32 (16-byte aligned; zero it for a fresh
@@ -433,8 +433,11 @@ int kda_copy_batch(const uint64_t* table, int n, long long words, void* stream);
  *                 time need different work buffers.
  *   0 <= R <= KDA_PROMPT_ROWS_MAX, 1 <= B <= KDA_PROMPT_SEQS_MAX,
  *   1 <= H <= 65535, R * H <= 2^34, B * H <= 2^20.  With R = 0 nothing is enqueued.
- *   Products keep f32's precision while the values that meet in one chunk of 32
- *   rows (k, q; v and the state by column) lie within 2^16 of the largest.
+ *   The products between the state and k, q hold each factor in 22 bits: k and q
+ *   with the decay from (k: also to) their chunk's edge in them, by row, the state
+ *   by value channel.  A factor under 2^-16 of the largest of its row, or of the
+ *   64 keys that it is held with in its channel, keeps fewer bits.  Rows, value
+ *   channels and heads may differ from each other by any factor.
  */
 int kda_prompt(float* const* s_ptrs, const int32_t* offsets, const void* q, const void* k,
                const void* v, const void* g, const void* beta, float* o, int R, int B, int H,
