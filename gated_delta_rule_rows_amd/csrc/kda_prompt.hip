@@ -271,6 +271,28 @@ __device__ __forceinline__ void patch_words(const Patch<BF16>& p, uint2 (&w)[4][
     }
 }
 
+// True where one of the patch's values is a NaN or an infinity.
+template <bool BF16>
+__device__ __forceinline__ bool not_finite(const Patch<BF16>& p) {
+    if constexpr (BF16) {
+        using u16x2 = __attribute__((ext_vector_type(2))) uint16_t;
+        u16x2 most{0, 0};
+#pragma unroll
+        for (int i = 0; i < 2; ++i)
+#pragma unroll
+            for (const uint32_t u : {p.r[i].x, p.r[i].y, p.r[i].z, p.r[i].w})
+                most = __builtin_elementwise_max(most, __builtin_bit_cast(u16x2, u & 0x7FFF7FFFu));
+        return max(most[0], most[1]) >= 0x7F80;
+    } else {
+        uint32_t most = 0;
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+            most = max(max(max(most, p.r[i].x & 0x7FFFFFFFu), max(p.r[i].y & 0x7FFFFFFFu, p.r[i].z & 0x7FFFFFFFu)),
+                       p.r[i].w & 0x7FFFFFFFu);
+        return most >= 0x7F800000u;
+    }
+}
+
 template <int NS>
 struct LinearTile {
     uint16_t q[NS][kChunk][kRowPitch];
@@ -281,6 +303,7 @@ struct LinearTile {
     double G[kChunk];
     float eG[kChunk];   // e^{G_t}
     float w[kChunk];    // e^{G_C - G_t}
+    __align__(16) uint32_t spoiled[4];   // v has a NaN or infinity: a flag of each wave that brings it
 };
 
 // By channel: word x of four rows of one plane.
@@ -322,6 +345,33 @@ __device__ __forceinline__ void read_columns(const uint16_t (&t)[NS][ROWS][kColP
                                              uint4 (&f)[NS]) {
 #pragma unroll
     for (int s = 0; s < NS; ++s) f[s] = *reinterpret_cast<const uint4*>(&t[s][row][at]);
+}
+
+// Eight rows (8 g4..) of a channel's values a lane: puts 0 in the place of what is
+// not finite, and gives the first row of the chunk that has such a value.
+template <int NS>
+__device__ __forceinline__ int take_out(uint4 (&v)[NS]) {
+    int first = kChunk;
+    const int row = 8 * (threadIdx.x >> 4 & 3);
+    const auto pair = [&](int i, auto part) {   // rows i and i + 1
+#pragma unroll
+        for (int hi = 0; hi < 2; ++hi) {
+            const uint32_t mask = hi ? 0xFFFF0000u : 0xFFFFu;
+            float x = 0.f;
+#pragma unroll
+            for (int s = NS - 1; s >= 0; --s) x += real(hi ? part(v[s]) & mask : part(v[s]) << 16);
+            if (fabsf(x) < __builtin_inff()) continue;
+            first = min(first, row + i + hi);
+#pragma unroll
+            for (int s = 0; s < NS; ++s) part(v[s]) &= ~mask;
+        }
+    };
+    pair(0, [](uint4& u) -> uint32_t& { return u.x; });
+    pair(2, [](uint4& u) -> uint32_t& { return u.y; });
+    pair(4, [](uint4& u) -> uint32_t& { return u.z; });
+    pair(6, [](uint4& u) -> uint32_t& { return u.w; });
+    first = min(first, __shfl_xor(first, 16));
+    return min(first, __shfl_xor(first, 32));
 }
 
 // Parts of a call: slot s of head h has its state at states + (s * H + h) * 128 * 128
@@ -408,6 +458,8 @@ __global__ void __launch_bounds__(512, BF16 ? 4 : 2) linear_chunk_kernel(PromptA
             } else {
                 store_columns<NS>(T.vt, cg, 4 * rg, w);
                 if (out) {
+                    const uint64_t mask = __ballot(not_finite<BF16>(pa));
+                    if (lane == 0) T.spoiled[wave - 4] = mask != 0;
                     patch_words<BF16>(pb, w);
                     store_rows<NS>(T.q, cg, rg, w);
                 }
@@ -476,6 +528,12 @@ __global__ void __launch_bounds__(512, BF16 ? 4 : 2) linear_chunk_kernel(PromptA
             __syncthreads();
             uint4 vf[NS];
             read_columns<NS, kD>(T.vt, col, 8 * g4, vf);
+            // a NaN or infinity in v would reach earlier rows through their weights
+            // of 0: it is left out, and its channel's outputs from its row on are NaN
+            const uint4 flags = *reinterpret_cast<const uint4*>(T.spoiled);
+            const bool spoiled = __builtin_amdgcn_readfirstlane(flags.x | flags.y | flags.z | flags.w);
+            int bad = kChunk;
+            if (spoiled) bad = take_out<NS>(vf);
 #pragma unroll
             for (int tb = 0; tb < 2; ++tb) {
                 const float e = T.eG[16 * tb + l16];
@@ -483,7 +541,11 @@ __global__ void __launch_bounds__(512, BF16 ? 4 : 2) linear_chunk_kernel(PromptA
                 read_columns<3, kChunk>(T.p, 16 * tb + l16, 8 * g4, pf);
                 O[tb] *= e;
                 O[tb] = product<NS, 3>(vf, pf, O[tb]);
-                const f32x4 y = O[tb] * kScale;
+                f32x4 y = O[tb] * kScale;
+                if (spoiled)
+#pragma unroll
+                    for (int r = 0; r < 4; ++r)
+                        if (16 * tb + l16 >= __shfl(bad, 4 * g4 + r)) y[r] = __builtin_nanf("");
                 __builtin_amdgcn_raw_buffer_store_b128(__builtin_bit_cast(u32x4, y), o.buffer,
                                                        (16 * tb + l16) * o.pitch + 4 * (16 * wave + 4 * g4), 0, 0);
             }
