@@ -204,6 +204,9 @@ constexpr int kRowPitch = kD + 8;      // q and k by row: 16 rows of a 16-byte r
 constexpr int kColPitch = kChunk + 8;  // k, v by channel and the chunk's weights: the same
 constexpr float kGateOff = -104.0f;    // exp of it is 0 in f32
 
+// min(g, 0), no lower than kGateOff; a NaN stays one.
+__device__ __forceinline__ float log_decay(float g) { return g < kGateOff ? kGateOff : g > 0.f ? 0.f : g; }
+
 // Up to 32 rows of one head as a buffer: reads past the last row give 0 and
 // writes there are dropped, so that the row loops need no branches.
 struct Rows {
@@ -466,7 +469,7 @@ __global__ void __launch_bounds__(512, BF16 ? 4 : 2) linear_chunk_kernel(PromptA
             }
         }
         if (wave == 0) {
-            double x = lane < kChunk ? fminf(fmaxf(pg, kGateOff), 0.f) : 0.f;
+            double x = lane < kChunk ? log_decay(pg) : 0.f;
 #pragma unroll
             for (int d = 1; d < kChunk; d <<= 1) {
                 const double y = __shfl_up(x, d);
@@ -1459,7 +1462,7 @@ __global__ void __launch_bounds__(256) linear_step_kernel(StepArgs a) {
     else
         ks[tid - kD] = load<BF16>(a.k, kr + tid - kD);
     const long long r = n * a.H + h;
-    const float d = expf(fminf(a.g[r], 0.f));
+    const float d = expf(log_decay(a.g[r]));
     float v[4];
 #pragma unroll
     for (int c = 0; c < 4; ++c) v[c] = load<BF16>(a.v, r * kD + 4 * c4 + c);

@@ -461,9 +461,9 @@ long long kda_prompt_work_bytes(int R, int B, int H);
  *                 -inf is allowed (the state restarts at that row); a decay
  *                 below exp(-104) is 0 in f32.
  *   o           : [R][H][128] ([L][B][H][128]) f32, or NULL.
- *   A NaN or an infinity in a row of q, k or v makes NaN of what it reaches: q
- *   its row's outputs, k the head's outputs from its row on, v those of its
- *   channel.  Earlier rows, other heads and other sequences stay what they are.
+ *   A NaN or an infinity in a row of q, k or v, or a NaN in g, makes NaN of what
+ *   it reaches: q its row's outputs, k and g the head's outputs from its row on, v
+ *   those of its channel.  Earlier rows, other heads and other sequences stay what they are.
  *   s_ptrs, offsets, work : as kda_prompt; for the step s_ptrs[l*B + b] is
  *                 session b's layer-l state, and a NULL entry leaves that
  *                 session out (its row of o is not written).

@@ -130,3 +130,50 @@ def test_states(op):
         S0[1, 1, :, 5] = BAD["nan"]
 
     _check(op, lens, xs, S0, change, at_o, at_S)
+
+
+@pytest.mark.parametrize("lens", LENS, ids=str)
+@pytest.mark.parametrize("row", [0, 13, 31, 32, 77])
+def test_linear_gates(lens, row):
+    # a NaN decay: the head's outputs from the row on and its state
+    xs, S0, at_o, at_S = _inputs("linear", lens, torch.float32)
+    t, end = lens[0] + row, lens[0] + lens[1]
+    at_o[t:end, 1] = True
+    at_S[1, 1] = True
+
+    def change(xs, S0):
+        xs[3][t, 1] = BAD["nan"]
+
+    _check("linear", lens, xs, S0, change, at_o, at_S)
+
+
+@pytest.mark.parametrize("which,bad", [("g", "nan"), ("v", "inf"), ("q", "nan"), ("k", "nan")])
+def test_linear_step(which, bad):
+    xs = [x.view(1, 3, *x.shape[1:]).cuda() for x in ref.linear_inputs(92, 3, H, H)]
+    S0 = ref.states(93, 3, H).cuda()
+
+    def step(xs):
+        S, o = S0.clone(), torch.full((1, 3, H, D), 7.0, device="cuda")
+        kda.kda_linear_step(kda.state_table(S.unsqueeze(0)), *xs, o=o)
+        return o[0], S
+
+    want_o, want_S = step(xs)
+    at_o, at_S = torch.zeros_like(want_o, dtype=torch.bool), torch.zeros_like(want_S, dtype=torch.bool)
+    ys = [x.clone() for x in xs]
+    i = "qkvg".index(which)
+    if which == "g":
+        ys[i][0, 1, 1] = BAD[bad]
+    else:
+        ys[i][0, 1, 1, 9] = BAD[bad]
+    if which == "v":
+        at_o[1, 1, 9] = True
+        at_S[1, 1, :, 9] = True
+    else:
+        at_o[1, 1] = True
+    if which == "k":
+        at_S[1, 1, 9] = True
+    if which == "g":
+        at_S[1, 1] = True
+    o, S = step(ys)
+    assert not o[at_o].isfinite().any() and torch.equal(o[~at_o], want_o[~at_o])
+    assert not S[at_S].isfinite().any() and torch.equal(S[~at_S], want_S[~at_S])
