@@ -803,6 +803,41 @@ __device__ __forceinline__ float eighth_max(float x) {
     return column_max(abs_max(x, neighbour<0x128>(x), 0.f));   // row_ror:8
 }
 
+// The rows of a chunk that a NaN or infinity is in: from first on in k or beta,
+// after which nothing of the state is left, and a bit for each row of q.
+struct Spoiled {
+    int first;
+    uint32_t queries;
+};
+
+// Rows of a patch, one bit each, that have a NaN or infinity.
+template <bool BF16>
+__device__ __forceinline__ uint32_t spoiled_rows(const Patch<BF16>& p) {
+    float x[4][4];
+    patch_values<BF16>(p, x);
+    uint32_t m = 0;
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+#pragma unroll
+        for (int c = 0; c < 4; ++c)
+            if (!(fabsf(x[i][c]) < __builtin_inff())) m |= 1u << i;
+    return m;
+}
+
+template <bool BF16>
+__device__ __forceinline__ void clear_rows(Patch<BF16>& p, uint32_t rows) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        if (!(rows >> i & 1)) continue;
+        if constexpr (BF16) {
+            if (i & 1) p.r[i >> 1].z = p.r[i >> 1].w = 0;
+            else       p.r[i >> 1].x = p.r[i >> 1].y = 0;
+        } else {
+            p.r[i] = make_uint4(0, 0, 0, 0);
+        }
+    }
+}
+
 // Prepares one chunk of one head.
 //
 // e^{G_t-G_j} does not split into a factor of t and one of j over the chunk's
@@ -826,6 +861,8 @@ __global__ void __launch_bounds__(256) kda_prepare_kernel(PromptArgs a, KdaBlock
     __shared__ float A[kChunk][kChunk + 1], B[kChunk][kChunk + 1], T[kChunk][kChunk + 1];
     __shared__ float beta[kChunk];
     __shared__ __align__(16) float top[3][4][kChunk];   // by wave: the rows' largest k e^G, q e^G, k e^{G_C-G}
+    __shared__ __align__(16) uint32_t spoiled[4];
+    __shared__ Spoiled rows_lost;
     const int tid = threadIdx.x, wave = __builtin_amdgcn_readfirstlane(tid >> 6), lane = tid & 63, g4 = lane >> 4, l16 = lane & 15;
     const int h = blockIdx.x % a.H, slot = slot0 + blockIdx.x / a.H;
     const Part f = find_part(a, kChunk, slot);
@@ -854,8 +891,12 @@ __global__ void __launch_bounds__(256) kda_prepare_kernel(PromptArgs a, KdaBlock
     };
 #pragma unroll
     for (int ks = 0; ks < (BF16 ? 4 : 1); ++ks) rows(ks);
-    if (tid < kChunk)
-        beta[tid] = tid < n ? load<BF16>(a.beta, static_cast<long long>(t0 + tid) * a.H + h) : 0.f;
+    bool spoils = false;   // a NaN or infinity in the thread's part of the rows
+    if (tid < kChunk) {
+        const float x = tid < n ? load<BF16>(a.beta, static_cast<long long>(t0 + tid) * a.H + h) : 0.f;
+        beta[tid] = x;
+        spoils = !(fabsf(x) < __builtin_inff());
+    }
 
     float pre[4][4], suf[4][4], keep[4];   // e^{G_t} and e^{G_C-G_t} of the thread's elements
     {
@@ -956,6 +997,10 @@ __global__ void __launch_bounds__(256) kda_prepare_kernel(PromptArgs a, KdaBlock
             for (int i = 0; i < 4; ++i)
                 m[i] = eighth_max(abs_max(x[i][0] * f[i][0], x[i][1] * f[i][1], abs_max(x[i][2] * f[i][2], x[i][3] * f[i][3], 0.f)));
         };
+        spoils = spoils || not_finite<BF16>(pk) || not_finite<BF16>(pq);
+        const uint64_t mask = __ballot(spoils);
+        if (lane == 0) spoiled[wave] = mask != 0;
+        if (tid == 0) rows_lost = Spoiled{kChunk, 0};
         patch_values<BF16>(pk, x);
         largest(pre, most[0]);
         largest(suf, most[2]);
@@ -967,6 +1012,31 @@ __global__ void __launch_bounds__(256) kda_prepare_kernel(PromptArgs a, KdaBlock
                 *reinterpret_cast<float4*>(&top[o][wave][4 * rg]) = make_float4(most[o][0], most[o][1], most[o][2], most[o][3]);
     }
     __syncthreads();
+
+    // A row with a NaN or infinity would reach the rows before it through the zeros
+    // above the diagonals.  Such a row of q, and all rows from the first of k or
+    // beta on, are left out, and NaN comes back by their rows of B and, behind k
+    // and beta, by the state's decay.
+    Spoiled lost{kChunk, 0};
+    const uint4 flags = *reinterpret_cast<const uint4*>(spoiled);
+    if (__builtin_amdgcn_readfirstlane(flags.x | flags.y | flags.z | flags.w)) {
+        uint32_t m = spoiled_rows<BF16>(pk);
+        if (m) atomicMin(&rows_lost.first, 4 * rg + __builtin_ctz(m));
+        if (tid < kChunk && !(fabsf(beta[tid]) < __builtin_inff())) atomicMin(&rows_lost.first, tid);
+        m = spoiled_rows<BF16>(pq);
+        if (m) atomicOr(&rows_lost.queries, m << 4 * rg);
+        __syncthreads();
+        lost = rows_lost;
+        for (int i = tid; i < kChunk * kChunk; i += 256)
+            if (i / kChunk >= lost.first) A[i / kChunk][i % kChunk] = 0.f;
+        if (tid < kChunk && tid >= lost.first) beta[tid] = 0.f;
+        clear_rows<BF16>(pk, 15u << min(max(lost.first - 4 * rg, 0), 4));
+        clear_rows<BF16>(pq, lost.queries >> 4 * rg & 15);
+        if (lost.first < kChunk)
+#pragma unroll
+            for (int c = 0; c < 4; ++c) keep[c] = __builtin_nanf("");
+        __syncthreads();
+    }
 
     // T = (I - A)^-1: the diagonal blocks column by column by the first wave ...
     if (tid < kChunk) {
@@ -1069,6 +1139,7 @@ __global__ void __launch_bounds__(256) kda_prepare_kernel(PromptArgs a, KdaBlock
     for (int i = 0; i < 4; ++i) {
         m[i] = T[t][4 * x + i] * beta[4 * x + i];
         b[i] = B[t][4 * x + i];
+        if (t >= lost.first || lost.queries >> t & 1) b[i] = __builtin_nanf("");
     }
     const int at = 16 * (x & 3) + (t & 15);
     out.m[t >> 4][x >> 2][at] = make_float4(m[0], m[1], m[2], m[3]);
@@ -1122,6 +1193,7 @@ __global__ void __launch_bounds__(512) kda_chunk_kernel(PromptArgs a, const KdaB
     __shared__ uint4 sw[2][2][2][2][64];    // the state: column block, half, 32 channels, word
     __shared__ f32x4 ew[2][2][64];          // the deltas: column block, row block
     __shared__ float si[2][2][64];          // what undoes the state's scales
+    __shared__ int from_row[2][64];         // the row from which a column's outputs are NaN
     constexpr int slices = kD / kKdaCols * (STATES ? 2 : 1), es = BF16 ? 2 : 4;
     const int tid = threadIdx.x, wave = __builtin_amdgcn_readfirstlane(tid >> 6), lane = tid & 63, g4 = lane >> 4, l16 = lane & 15;
     // workgroups go round 8 XCDs: the slices of a head to one of them, whose L2
@@ -1196,7 +1268,9 @@ __global__ void __launch_bounds__(512) kda_chunk_kernel(PromptArgs a, const KdaB
             __syncthreads();
             // the chunk before: its deltas are there now
             f32x4 E[2] = {zero, zero};
+            int bad = kChunk;
             if (OUT && i > begin) {
+                bad = from_row[c][lane];
                 E[0] = ew[c][0][lane];
                 if (tb) E[1] = ew[c][1][lane];
             }
@@ -1225,9 +1299,11 @@ __global__ void __launch_bounds__(512) kda_chunk_kernel(PromptArgs a, const KdaB
                 const int t0 = first + (i - 1) * kChunk;
                 const Rows ro = rows_of(a.o, 4, t0, last - t0, a.H, h);
 #pragma unroll
-                for (int r = 0; r < 4; ++r)
-                    __builtin_amdgcn_raw_buffer_store_b32(bits((y[r] + Q[r]) * kScale), ro.buffer,
-                                                          (16 * tb + 4 * g4 + r) * ro.pitch + 4 * col, 0, 0);
+                for (int r = 0; r < 4; ++r) {
+                    const int t = 16 * tb + 4 * g4 + r;
+                    const float o = t < bad ? (y[r] + Q[r]) * kScale : __builtin_nanf("");
+                    __builtin_amdgcn_raw_buffer_store_b32(bits(o), ro.buffer, t * ro.pitch + 4 * col, 0, 0);
+                }
             }
             if (i == end) break;
             if (i + 1 < end) {
@@ -1295,6 +1371,7 @@ __global__ void __launch_bounds__(512) kda_chunk_kernel(PromptArgs a, const KdaB
 #pragma unroll
                 for (int w = 0; w < 2; ++w) kf[ks][tb][w] = T.k[tb][2 * half + ks][w][lane];
         f32x4 R[2] = {zero, zero}, V[2] = {zero, zero};
+        float z = 0.f;    // NaN if V has a NaN or infinity
         if (half == 0)
 #pragma unroll
             for (int tb = 0; tb < 2; ++tb) V[tb] = xv[c][tb][lane];
@@ -1314,6 +1391,8 @@ __global__ void __launch_bounds__(512) kda_chunk_kernel(PromptArgs a, const KdaB
 #pragma unroll
         for (int tb = 0; tb < 2; ++tb) {
 #pragma unroll
+            for (int r = 0; r < 4; ++r) z = fmaf(V[tb][r], 0.f, z);
+#pragma unroll
             for (int r = 0; r < 4; ++r) R[tb][r] = fmaf(R[tb][r] * ki[tb][r], -s1, V[tb][r]);
             xr[wave][tb][lane] = R[tb];
         }
@@ -1330,17 +1409,50 @@ __global__ void __launch_bounds__(512) kda_chunk_kernel(PromptArgs a, const KdaB
             keep[m] = *reinterpret_cast<const f32x4*>(&T.keep[64 * half + 16 * m + 4 * g4]);
         }
         __builtin_amdgcn_s_setprio(3);
-        f32x4 E[2] = {zero, zero}, x = zero;    // the deltas
+        f32x4 E[2];    // the deltas
+        const auto deltas = [&] {
+            f32x4 x = zero;
+            E[0] = E[1] = zero;
 #pragma unroll
-        for (int r = 0; r < 4; ++r) {
-            E[0] = __builtin_amdgcn_mfma_f32_16x16x4f32(m00[r], R[0][r], E[0], 0, 0, 0);
-            E[1] = __builtin_amdgcn_mfma_f32_16x16x4f32(m10[r], R[0][r], E[1], 0, 0, 0);
-            x = __builtin_amdgcn_mfma_f32_16x16x4f32(m11[r], R[1][r], x, 0, 0, 0);
+            for (int r = 0; r < 4; ++r) {
+                E[0] = __builtin_amdgcn_mfma_f32_16x16x4f32(m00[r], R[0][r], E[0], 0, 0, 0);
+                E[1] = __builtin_amdgcn_mfma_f32_16x16x4f32(m10[r], R[0][r], E[1], 0, 0, 0);
+                x = __builtin_amdgcn_mfma_f32_16x16x4f32(m11[r], R[1][r], x, 0, 0, 0);
+            }
+            E[1] += x;
+        };
+        // A NaN or infinity in v has to reach the state, but not the deltas of earlier
+        // rows, which it meets with M's zeros: those go to the outputs without it.
+        if (OUT && half == 0) {
+            int first = kChunk;
+            if (__ballot(z != z)) {
+                const f32x4 keep_R[2] = {R[0], R[1]};
+#pragma unroll
+                for (int tb = 0; tb < 2; ++tb)
+#pragma unroll
+                    for (int r = 0; r < 4; ++r)
+                        if (!(fabsf(V[tb][r]) < __builtin_inff())) {
+                            first = min(first, 16 * tb + 4 * g4 + r);
+                            R[tb][r] = 0.f;
+                        }
+                first = min(first, __shfl_xor(first, 16));
+                first = min(first, __shfl_xor(first, 32));
+                deltas();
+#pragma unroll
+                for (int tb = 0; tb < 2; ++tb) {
+                    ew[c][tb][lane] = E[tb];
+                    R[tb] = keep_R[tb];
+                }
+                deltas();
+            } else {
+                deltas();
+#pragma unroll
+                for (int tb = 0; tb < 2; ++tb) ew[c][tb][lane] = E[tb];
+            }
+            from_row[c][lane] = first;
+        } else {
+            deltas();
         }
-        E[1] += x;
-        if (OUT && half == 0)
-#pragma unroll
-            for (int tb = 0; tb < 2; ++tb) ew[c][tb][lane] = E[tb];
         float emax = 0.f;
 #pragma unroll
         for (int tb = 0; tb < 2; ++tb) {

@@ -427,6 +427,10 @@ int kda_copy_batch(const uint64_t* table, int n, long long words, void* stream);
  *   q, k, v, g  : [R][H][128] in in_dtype, the sequences packed one after the
  *                 other.  beta: [R][H].
  *   o           : [R][H][128] f32, or NULL for the state only.
+ *   A NaN or an infinity in a row of q, k, v or beta makes NaN of what it
+ *   reaches: q its row's outputs, k and beta the head's outputs from its row on,
+ *   v those of its channel.  Earlier rows, other heads and other sequences stay
+ *   what they are.  (A NaN in g counts as -5, as in kda_scan_rows.)
  *   work        : kda_prompt_work_bytes(R, B, H) bytes (work_bytes says how
  *                 many there are), 16-byte aligned, in any state on entry;
  *                 NULL when none are needed.  Calls that can run at the same

@@ -48,10 +48,10 @@ def _inputs(op, lens, dtype):
 
 
 # one sequence of several chunks behind another; parts of 512 rows with the bad row in the first
-LENS = [[20, 100, 40], [3, 1300, 5]]
+LENS = [[20, 100, 40], [3, 2300, 5]]
 
 
-@pytest.mark.parametrize("op", ["linear"])
+@pytest.mark.parametrize("op", ["linear", "kda"])
 @pytest.mark.parametrize("dtype", list(DTYPES))
 @pytest.mark.parametrize("lens", LENS, ids=str)
 @pytest.mark.parametrize("bad", list(BAD))
@@ -69,7 +69,7 @@ def test_values(op, dtype, lens, bad, row):
     _check(op, lens, xs, S0, change, at_o, at_S)
 
 
-@pytest.mark.parametrize("op", ["linear"])
+@pytest.mark.parametrize("op", ["linear", "kda"])
 @pytest.mark.parametrize("dtype", list(DTYPES))
 def test_values_of_many_channels(op, dtype):
     # other rows for other channels of one chunk, two in one channel, the last row of a sequence
@@ -87,7 +87,7 @@ def test_values_of_many_channels(op, dtype):
     _check(op, lens, xs, S0, change, at_o, at_S)
 
 
-@pytest.mark.parametrize("op", ["linear"])
+@pytest.mark.parametrize("op", ["linear", "kda"])
 @pytest.mark.parametrize("dtype", list(DTYPES))
 @pytest.mark.parametrize("bad", list(BAD))
 @pytest.mark.parametrize("row", [0, 13, 31, 32, 77])
@@ -118,7 +118,7 @@ def test_linear_keys(dtype, row):
     _check("linear", lens, xs, S0, change, at_o, at_S)
 
 
-@pytest.mark.parametrize("op", ["linear"])
+@pytest.mark.parametrize("op", ["linear", "kda"])
 def test_states(op):
     # a channel of one state
     lens = [20, 100, 40]
@@ -177,3 +177,41 @@ def test_linear_step(which, bad):
     o, S = step(ys)
     assert not o[at_o].isfinite().any() and torch.equal(o[~at_o], want_o[~at_o])
     assert not S[at_S].isfinite().any() and torch.equal(S[~at_S], want_S[~at_S])
+
+
+@pytest.mark.parametrize("which", ["k", "beta"])
+@pytest.mark.parametrize("dtype", list(DTYPES))
+@pytest.mark.parametrize("lens", LENS, ids=str)
+@pytest.mark.parametrize("bad", list(BAD))
+@pytest.mark.parametrize("row", [0, 13, 31, 32, 77])
+def test_kda_keys_and_strengths(which, dtype, lens, bad, row):
+    # a delta of every channel, so all of the head's outputs from the row on and its whole state
+    xs, S0, at_o, at_S = _inputs("kda", lens, DTYPES[dtype])
+    t, end = lens[0] + row, lens[0] + lens[1]
+    at_o[t:end, 1] = True
+    at_S[1, 1] = True
+
+    def change(xs, S0):
+        if which == "k":
+            xs[1][t, 1, 99] = BAD[bad]
+        else:
+            xs[4][t, 1] = BAD[bad]
+
+    _check("kda", lens, xs, S0, change, at_o, at_S)
+
+
+def test_kda_several_at_once():
+    # a query before and behind the first bad key of a chunk, and values in two channels
+    lens = [64, 33]
+    xs, S0, at_o, at_S = _inputs("kda", lens, torch.float32)
+    at_o[34, 0] = at_o[40:64, 0] = True
+    at_o[35:, 0, 3] = at_o[38:, 0, 100] = True
+    at_o[64:] = False
+    at_S[0, 0] = True
+
+    def change(xs, S0):
+        xs[0][34, 0, 1] = xs[0][50, 0, 2] = BAD["nan"]
+        xs[1][40, 0, 7] = xs[1][45, 0, 8] = BAD["inf"]
+        xs[2][35, 0, 3], xs[2][38, 0, 100], xs[2][60, 0, 3] = BAD["inf"], BAD["nan"], BAD["nan"]
+
+    _check("kda", lens, xs, S0, change, at_o, at_S)
