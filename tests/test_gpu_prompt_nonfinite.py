@@ -215,3 +215,20 @@ def test_kda_several_at_once():
         xs[2][35, 0, 3], xs[2][38, 0, 100], xs[2][60, 0, 3] = BAD["inf"], BAD["nan"], BAD["nan"]
 
     _check("kda", lens, xs, S0, change, at_o, at_S)
+
+
+def test_kda_nan_gates_count_as_the_lowest():
+    lens = [70]
+    xs, S0, _, _ = _inputs("kda", lens, torch.float32)
+    xs[3][5, 0, 3] = xs[3][40, 1, 100] = -5.0
+    want = _run("kda", lens, xs, S0)
+    rows = [x[:10].unsqueeze(0).cuda() for x in xs]
+    scan = torch.empty(1, H, D, D, device="cuda")
+    kda.kda_scan_rows(S0.cuda(), scan, *rows)
+    xs[3][5, 0, 3] = xs[3][40, 1, 100] = BAD["nan"]
+    got = _run("kda", lens, xs, S0)
+    assert torch.equal(got[0], want[0]) and torch.equal(got[1], want[1])
+    rows[3][0, 5, 0, 3] = BAD["nan"]
+    again = torch.empty_like(scan)
+    kda.kda_scan_rows(S0.cuda(), again, *rows)
+    assert torch.equal(scan, again)
