@@ -175,13 +175,18 @@ __device__ __forceinline__ void take(Sums& s, List& l, const float (&x)[E], uint
     // m need not be the maximum: it follows once a value is well above it
     if (__ballot(top > s.m + kSlack || s.m == -kInf)) move_to(s, fmaxf(s.m, top));
     const float base = s.m == -kInf ? 0.f : s.m;
+    // one add a load to the running sums: each add rounds by their size, and takes
+    // nothing of what is under half a last place of them
+    float z = 0.f, w = 0.f;
 #pragma unroll
     for (int e = 0; e < E; ++e) {
         const float y = x[e] - base;
         const float p = exp_of(y);
-        s.z += p;
-        s.w = fmaf(p, fmaxf(y, -1e30f), s.w);
+        z += p;
+        w = fmaf(p, fmaxf(y, -1e30f), w);
     }
+    s.z += z;
+    s.w += w;
     if constexpr (TOP) {
         if (__ballot(top > l.bar)) {
 #pragma unroll
