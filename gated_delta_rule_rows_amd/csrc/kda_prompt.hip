@@ -377,12 +377,20 @@ __device__ __forceinline__ int take_out(uint4 (&v)[NS]) {
     return min(first, __shfl_xor(first, 32));
 }
 
-// Parts of a call: slot s of head h has its state at states + (s * H + h) * 128 * 128
-// and its summed log-decays at sums[s * H + h].
+// Parts of a call: place s of head h has its state at states + (s * H + h) * 128 * 128
+// and its summed log-decays at sums[s * H + h].  Only sequences of several parts
+// take places, one for each part.  Of many short sequences few can be that long:
+// they begin at twice the rows before them, in parts, which leaves each room for
+// its own (ceil(x) <= floor(2 x) from one part on) and takes 2 R / rows places
+// however many sequences there are.
 struct Parts {
     float* states;
     double* sums;
-    int rows;    // of a part
+    int rows;       // of a part
+    bool twice;     // places by twice the rows, not by R / rows + B slots
+    __device__ long long first_place(int b, int first) const {
+        return twice ? 2 * first / rows : first / rows + b;   // first <= 2^28
+    }
 };
 
 // STATES: the part's own state, from zero, into its slot (all but a sequence's
@@ -411,11 +419,11 @@ __global__ void __launch_bounds__(512, BF16 ? 4 : 2) linear_chunk_kernel(PromptA
 #pragma unroll
         for (int m = 0; m < 8; ++m) S[m] = f32x4{0.f, 0.f, 0.f, 0.f};
     } else {
-        // the chained states lie one slot back; a first part's in the last slot
+        // the chained states lie one place back; a first part's in the last place
         const float* from = state;
         if (f.index > 0 || !last_part) {
-            const int back = f.index > 0 ? slot - 1 : slot + (f.last - f.first - 1) / parts.rows;
-            from = parts.states + (static_cast<long long>(back) * a.H + h) * kD * kD;
+            const int back = f.index > 0 ? f.index - 1 : (f.last - f.first - 1) / parts.rows;
+            from = parts.states + ((parts.first_place(f.b, f.first) + back) * a.H + h) * kD * kD;
         }
         const auto buffer = state_of(from);
 #pragma unroll
@@ -582,19 +590,20 @@ __global__ void __launch_bounds__(512, BF16 ? 4 : 2) linear_chunk_kernel(PromptA
     }
 
     if (STATES || last_part) {
-        float* to = STATES ? parts.states + (static_cast<long long>(slot) * a.H + h) * kD * kD : state;
+        const long long at = (parts.first_place(f.b, f.first) + f.index) * a.H + h;
+        float* to = STATES ? parts.states + at * kD * kD : state;
         const auto buffer = state_of(to);
 #pragma unroll
         for (int m = 0; m < 8; ++m)
 #pragma unroll
             for (int r = 0; r < 4; ++r)
                 __builtin_amdgcn_raw_buffer_store_b32(bits(S[m][r]), buffer, (4 * g4 * kD + col) * 4, (16 * m + r) * kD * 4, 0);
-        if (STATES && tid == 0) parts.sums[static_cast<long long>(slot) * a.H + h] = sum;
+        if (STATES && tid == 0) parts.sums[at] = sum;
     }
 }
 
-// Chains the parts of each (sequence, head): slot i gets the state that part
-// i + 1 starts from, the last slot the one the sequence came with (its first
+// Chains the parts of each (sequence, head): place i gets the state that part
+// i + 1 starts from, the last place the one the sequence came with (its first
 // part reads that copy, since the last part writes the state itself).
 __global__ void __launch_bounds__(256) linear_chain_kernel(PromptArgs a, Parts parts) {
     const int h = blockIdx.x % a.H, b = blockIdx.x / a.H;
@@ -604,9 +613,9 @@ __global__ void __launch_bounds__(256) linear_chain_kernel(PromptArgs a, Parts p
     const int n = (last - first + parts.rows - 1) / parts.rows;
     if (state == nullptr || n < 2) return;
     const long long at = blockIdx.y * 256 + threadIdx.x;
-    const long long slot0 = first / parts.rows + b;
+    const long long place0 = parts.first_place(b, first);
     const long long step = static_cast<long long>(a.H) * kD * kD / 4;
-    f32x4* p = reinterpret_cast<f32x4*>(parts.states) + slot0 * step + static_cast<long long>(h) * (kD * kD / 4) + at;
+    f32x4* p = reinterpret_cast<f32x4*>(parts.states) + place0 * step + static_cast<long long>(h) * (kD * kD / 4) + at;
     f32x4 S = reinterpret_cast<const f32x4*>(state + static_cast<long long>(h) * kD * kD)[at];
     p[(n - 1) * step] = S;
     constexpr int U = 4;
@@ -617,7 +626,7 @@ __global__ void __launch_bounds__(256) linear_chain_kernel(PromptArgs a, Parts p
         for (int u = 0; u < U; ++u)
             if (i + u < n - 1) {
                 x[u] = p[(i + u) * step];
-                e[u] = expf(static_cast<float>(parts.sums[(slot0 + i + u) * a.H + h]));
+                e[u] = expf(static_cast<float>(parts.sums[(place0 + i + u) * a.H + h]));
             }
 #pragma unroll
         for (int u = 0; u < U; ++u)
@@ -1630,9 +1639,21 @@ static int part_rows(int R, int H) {
 
 static long long part_slots(int R, int B, int rows) { return R / rows + static_cast<long long>(B); }
 
+// Places of part states: R / rows + B, or 2 R / rows if that is less.
+static bool places_twice(int R, int B, int rows) { return B > R / rows; }
+
+static long long part_places(int R, int B, int rows) {
+    return places_twice(R, B, rows) ? 2ll * R / rows : part_slots(R, B, rows);
+}
+
+// For calls of up to R, B and H, whose parts can be of any size from 512 rows on:
+// parts under 4096 rows have R * H / rows <= 1024, and there are at most twice as
+// many places.
 long long linear_work_bytes(int R, int B, int H) {
     if (R <= 512) return 0;
-    return part_slots(R, B, 512) * H * (kD * kD * 4ll + 8);
+    const long long longest = static_cast<long long>(R) * H / 2048, shortest = part_places(R, B, 512) * H;
+    const long long places = longest > 2048 ? longest : 2048;
+    return (places < shortest ? places : shortest) * (kD * kD * 4ll + 8);
 }
 
 // The prepared chunks of a call, or of as many slots as fit kWorkCap: longer
@@ -1706,8 +1727,9 @@ static hipError_t launch_linear(const PromptArgs& a, hipStream_t stream) {
     if (blocks > 0x7FFFFFFFll) return hipErrorInvalidValue;
     const dim3 grid(static_cast<unsigned>(blocks));
     if (a.R > parts.rows) {   // a sequence may have several parts
+        parts.twice = places_twice(a.R, a.B, parts.rows);
         parts.states = static_cast<float*>(a.work);
-        parts.sums = reinterpret_cast<double*>(parts.states + blocks * kD * kD);
+        parts.sums = reinterpret_cast<double*>(parts.states + part_places(a.R, a.B, parts.rows) * a.H * kD * kD);
         linear_chunk_kernel<BF16, true><<<grid, dim3(512), 0, stream>>>(a, parts);
         const dim3 chain(static_cast<unsigned>(static_cast<long long>(a.B) * a.H), kD * kD / 4 / 256);
         linear_chain_kernel<<<chain, dim3(256), 0, stream>>>(a, parts);

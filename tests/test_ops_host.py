@@ -265,3 +265,21 @@ def test_grids_beyond_the_launch_limit_are_refused(lib, b):
     _refused(lib, _logprobs(lib, b, t=1 << 26), ERR_RANGE, "t=67108864")
     assert lib.kda_logprobs_work_bytes(1 << 26, 1, 0) == -1
     assert lib.kda_logprobs_work_bytes((1 << 26) - 1, 1, 0) == 0
+
+
+def test_linear_workspace_is_for_long_sequences_only(lib):
+    """Part states take room for at most two parts of 512 rows a 512 rows, however many sequences
+    there are: a batch of short prompts needs no more than one long one."""
+    space, place = lib.kda_linear_prompt_work_bytes, 128 * 128 * 4 + 8
+    for R, B, H in ((513, 4096, 256), (600, 64, 64), (4096, 256, 64), (8192, 256, 64), (100000, 4096, 64)):
+        assert space(R, B, H) <= max(2 * R // 512 * H, 1) * place, (R, B, H)
+        assert space(R, B, H) <= max(R * H // 2048, 2048) * place, (R, B, H)
+    assert space(4096, 1, 64) == 9 * 64 * place
+    # it never shrinks as a count grows, and holds what every smaller call needs
+    counts = [(R, B, H) for R in (1, 512, 513, 1024, 5000, 70000, 1 << 20) for B in (1, 2, 9, 300, 4096)
+              for H in (1, 3, 16, 64, 256)]
+    for R, B, H in counts:
+        n = space(R, B, H)
+        for more in ((R + 1, B, H), (2 * R, B, H), (R, B + 1, H), (R, B, H + 1), (R, B, 2 * H)):
+            if max(more[0] * more[2], 1) <= 1 << 34 and more[1] <= 4096 and more[1] * more[2] <= 1 << 20:
+                assert space(*more) >= n, (R, B, H, more)
