@@ -1681,7 +1681,7 @@ static long long blocks_bytes(int R, int B, int H) {
     return all < most ? all : most;
 }
 
-long long prompt_work_bytes(int R, int B, int H) { return parts_bytes(R) + blocks_bytes(R, B, H); }
+long long prompt_work_bytes(int R, int B, int H) { return R == 0 ? 0 : parts_bytes(R) + blocks_bytes(R, B, H); }
 
 template <bool BF16>
 static hipError_t launch_kda(const PromptArgs& a, hipStream_t stream) {

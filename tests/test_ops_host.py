@@ -283,3 +283,12 @@ def test_linear_workspace_is_for_long_sequences_only(lib):
         for more in ((R + 1, B, H), (2 * R, B, H), (R, B + 1, H), (R, B, H + 1), (R, B, 2 * H)):
             if max(more[0] * more[2], 1) <= 1 << 34 and more[1] <= 4096 and more[1] * more[2] <= 1 << 20:
                 assert space(*more) >= n, (R, B, H, more)
+
+
+@pytest.mark.parametrize("call", [_prompt, _linear])
+def test_prompt_without_rows_needs_no_workspace(lib, b, call):
+    none = dict(R=0, q=None, k=None, v=None, g=None, o=None, work=None, bytes=0)
+    if call is _prompt:
+        none["beta"] = None
+    assert call(lib, b, **none) == OK
+    assert lib.kda_prompt_work_bytes(0, 4096, 64) == lib.kda_linear_prompt_work_bytes(0, 4096, 64) == 0
