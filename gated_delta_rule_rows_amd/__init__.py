@@ -573,7 +573,14 @@ def kda_copy_batch(table, n: int, words: int, stream=None) -> None:
     _check(lib.kda_copy_batch(_dev(table, "table"), int(n), int(words), _stream(stream)))
 
 
+def _int32(*counts) -> None:
+    """Refuses counts that a C int would wrap around."""
+    if max(counts) > 0x7FFFFFFF or min(counts) < -0x80000000:
+        raise KdaError(2, f"counts {counts} do not fit 32 bits")
+
+
 def _work_bytes(fn, *counts) -> int:
+    _int32(*counts)
     n = fn(*counts)
     if n < 0:
         raise KdaError(2, _lib.kda_last_error().decode())
@@ -746,6 +753,7 @@ def kda_logprobs(logits, tokens=None, lp=None, entropy=None, top_ids=None, top_l
     if logits.dim() != 2:
         raise ValueError("logits must be a [t][V] tensor")
     t, V = logits.shape
+    _int32(t, V)   # (other calls' tensors would not fit a GPU first)
     dt = _row_dtype(logits, "logits")
     if V > 1 and logits.stride(1) != 1:
         raise ValueError("logits rows must be contiguous")

@@ -292,3 +292,24 @@ def test_prompt_without_rows_needs_no_workspace(lib, b, call):
         none["beta"] = None
     assert call(lib, b, **none) == OK
     assert lib.kda_prompt_work_bytes(0, 4096, 64) == lib.kda_linear_prompt_work_bytes(0, 4096, 64) == 0
+
+
+@pytest.mark.parametrize("space", [kda.prompt_workspace, kda.linear_workspace, kda.logprobs_workspace])
+def test_counts_past_32_bits_are_refused(space):
+    for at in range(3):
+        counts = [1, 1, 1]
+        counts[at] = 2 ** 32 + 1                   # 1, if it wrapped
+        with pytest.raises(kda.KdaError, match="32 bits"):
+            space(*counts, device="cpu")
+
+
+@pytest.mark.gpu
+def test_logits_past_32_bits_are_refused():
+    lp, ent = torch.zeros(1, device="cuda"), torch.full((1,), 7.0, device="cuda")
+    tok = torch.zeros(1, dtype=torch.int32, device="cuda")
+    logits = torch.empty(1, 2 ** 32 + 8, dtype=torch.bfloat16, device="cuda")
+    with pytest.raises(kda.KdaError, match="32 bits"):
+        kda.kda_logprobs(logits, tok, lp, ent)
+    assert float(ent) == 7.0
+    with pytest.raises(kda.KdaError, match="outside"):
+        kda.kda_logprobs(logits[:, :2 ** 30 + 1].contiguous(), tok, lp, ent)
