@@ -20,9 +20,10 @@
 // are unique, so neither the order of the lists nor the positions that the
 // candidates take change the result; sums are joined in a fixed order.
 //
-// 2048 rows of 150,000 bf16 logits, 8 alternatives: 131 us, 4.7 TB/s, HBM and
-// VALU (0.83) together.  15 rows of 150,000 f32, 20 alternatives: 9 us for the
-// parts and 6 for the join, latency of the lists and of the sums' exchanges.
+// 2048 rows of 150,000 logits, 8 alternatives: bf16 131 us, 4.7 TB/s, bound by
+// VALU (0.85); f32 210 us, 5.85 TB/s.  15 rows of 150,000 f32, 20 alternatives: 9
+// us for the parts and 6 for the join, latency of the lists and of the sums'
+// exchanges.
 
 #include <hip/hip_runtime.h>
 

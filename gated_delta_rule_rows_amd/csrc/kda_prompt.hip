@@ -9,10 +9,10 @@
 //
 // Prompts run in chunks of 32 rows, whose rows meet in matrix products.  On an
 // MI355X, calls in a loop (the bytes that a call cannot do without, at the 4.69
-// TB/s of a large copy, in brackets): KDA 4096 rows x 64 heads bf16 420 us (88),
-// 8192 x 8 bf16 233 us (22), a ragged batch of 2,586 x 32 f32 158 us (52);
-// linear 4096 x 64 bf16 152-158 us (74), 16384 x 8 f32 153-169 us (58); the
-// single-token step over 34 x 15 x 64 states 837 us (919: it writes in place).
+// TB/s of a large copy, in brackets): KDA 4096 rows x 64 heads bf16 423 us (88),
+// 8192 x 8 bf16 236 us (22), a ragged batch of 2,586 x 32 f32 162 us (52);
+// linear 4096 x 64 bf16 155-164 us (74), 16384 x 8 f32 153-161 us (58); the
+// single-token step over 34 x 15 x 64 states 836 us (919: it writes in place).
 
 #include <hip/hip_runtime.h>
 
@@ -151,9 +151,10 @@ __device__ __forceinline__ void sequence(const PromptArgs& a, int b, int& first,
 // own state (from zero), a second chains them to the state each part starts
 // from, and a third computes the outputs.
 //
-// 4096 rows x 64 heads, bf16: states 43 us, chain 12, outputs 105 us (345 MB:
-// 3.3 TB/s), bound by VALU (0.53: the state is taken apart for every chunk) and
-// LDS (0.40) under two workgroups a CU; MFMA 0.27.
+// 4096 rows x 64 heads, bf16: states 43 us, chain 12, outputs 107 us (345 MB:
+// 3.2 TB/s), bound by VALU (0.54: the state is taken apart for every chunk) and
+// LDS (0.40, half of it bank conflicts: a half-wave's 8-byte writes of q and k by
+// row lie on half of the banks) under two workgroups a CU; MFMA 0.27.
 
 using bf16x8 = __attribute__((ext_vector_type(8))) __bf16;
 using f32x4 = __attribute__((ext_vector_type(4))) float;
@@ -651,9 +652,10 @@ __global__ void __launch_bounds__(256) linear_chain_kernel(PromptArgs a, Parts p
 // side by side (M, B, k e^G, q e^G, k e^{G_C-G}, e^{G_C}), and a second walks the
 // chunks of each sequence, where only the products are left.
 //
-// 4096 rows x 64 heads, bf16: prepare 170-185 us, 670 MB read and written at
-// 3.6-3.9 TB/s (a copy: 4.69) beside 0.52 VALU and 0.39 LDS; the walk 250-265 us, 2.0 us a chunk, bound by the dependent chain of a
-// chunk (1.4 us without the copies of its 57 KiB to LDS; MFMA 0.16).
+// 4096 rows x 64 heads, bf16: prepare 165-185 us, 670 MB read and written at
+// 3.6-4.0 TB/s (a copy: 4.69) beside 0.56 VALU and 0.37 LDS; the walk 255-265 us,
+// 2.0 us a chunk, bound by the dependent chain of a chunk (MFMA 0.28, of which
+// the f32 sums over rows are half; VALU 0.35).
 
 using f16x8 = __attribute__((ext_vector_type(8))) _Float16;
 using f16x2 = __attribute__((ext_vector_type(2))) _Float16;
@@ -1663,10 +1665,14 @@ constexpr int kFewHeads = 16, kPartRows = 512, kPartFill = 64;
 constexpr long long kPartBytes = 2ll * (kPartFill + kFewHeads) * kD * kD * 4;
 
 // Rows of a part.  Up to 16 (sequence, head) pairs of four workgroups each leave
-// three CUs of four idle; parts of R * H / 64 rows give each CU a workgroup.
+// three CUs of four idle; parts of R * H / 64 rows give each of 256 CUs a
+// workgroup of the outputs' walk, and two in turn of the walk for U and T, one of
+// which fills a CU's LDS.  (The counts are a whole MI355X's and not the current
+// device's: the workspace follows from R, B and H alone.)
 // In parts every chunk but those of a sequence's last part is walked three times
-// (U, T, outputs), so it takes four parts to gain: 8192 rows x 8 heads 197 us
-// in 8 parts against 399 in one piece; 2048 x 32 would be 125 in 2 against 109.
+// (U, T, outputs), so it takes four parts to gain: the three walks and the chain
+// of 8192 rows x 8 heads 197 us in 8 parts when first measured, against 399 in one
+// piece; 2048 x 32 would be 125 in 2 against 109.
 static int kda_part_rows(int R, int B, int H) {
     if (static_cast<long long>(B) * H > kFewHeads || R < 4 * kPartRows) return kWhole;
     const long long rows = (static_cast<long long>(R) * H / kPartFill + kChunk - 1) / kChunk * kChunk;
