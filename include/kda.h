@@ -441,8 +441,9 @@ int kda_copy_batch(const uint64_t* table, int n, long long words, void* stream);
  *   with the decay from (k: also to) their chunk's edge in them, by row, the state
  *   by value channel.  A factor under 2^-16 of the largest of its row, or of the
  *   64 keys that it is held with in its channel, keeps fewer bits, and one under
- *   2^-38 none.  Rows, value channels and heads may differ from each other by any
- *   factor.
+ *   2^-38 none: a state that nothing is added to, and whose key channels decay at
+ *   very different rates, comes there within some tens of rows.  Rows, value
+ *   channels and heads may differ from each other by any factor.
  */
 int kda_prompt(float* const* s_ptrs, const int32_t* offsets, const void* q, const void* k,
                const void* v, const void* g, const void* beta, float* o, int R, int B, int H,
