@@ -27,6 +27,10 @@ Shapes (D = 128):
                    (the step: [L][B][..] in place of [R][..])
   log probs        logits [t][V], tokens [t], lp and entropy [t] float32,
                    top_ids [t][n] int32 or uint32, top_lp [t][n] float32
+  paged cache      k_pages, v_pages [pages][rows][Hk][D], table [B][n] int32,
+                   lens [B] int32; new rows k, v [R][Hk][D], q, o [R][H][D]
+  sampled accept   logits, probs [R][V], offsets [B+1], drafts and u [R],
+                   temp [B], out [B][2], p_draft [R]
   greedy accept    logits [t][V] (row stride free, elements contiguous),
                    drafts [t-1], vam [t], out2 [2] as int32 or uint32,
                    work = accept_workspace()
@@ -54,6 +58,13 @@ class _PrevRound(ctypes.Structure):
     _fields_ = [("k", ctypes.c_void_p), ("v", ctypes.c_void_p), ("g", ctypes.c_void_p),
                 ("beta", ctypes.c_void_p), ("e", ctypes.c_void_p), ("T", ctypes.c_int),
                 ("keep", ctypes.c_int)]
+
+
+class _Cache(ctypes.Structure):
+    _fields_ = ([(n, ctypes.c_void_p) for n in ("k", "v", "table", "lens")] +
+                [(n, ctypes.c_longlong) for n in ("page_stride", "row_stride", "head_stride")] +
+                [(n, ctypes.c_int) for n in ("pages", "page_rows", "seq_pages")])
+
 
 _LIB_PATH = os.path.join(os.path.dirname(os.path.abspath(__file__)), "libkda.so")
 _lib = None
@@ -110,6 +121,16 @@ def load():
         fn.argtypes = [i, i, i]
         fn.restype = ll
     for fn in (lib.kda_prompt, lib.kda_linear_prompt, lib.kda_linear_step, lib.kda_logprobs):
+        fn.restype = i
+    c = ctypes.POINTER(_Cache)
+    lib.kda_cache_append.argtypes = [p, ll, p, ll, c, p, i, i, i, i, p]
+    lib.kda_attn_rows.argtypes = [p, ll, c, p, p, i, i, i, i, ctypes.c_float, i, i, i, p, ll, p]
+    lib.kda_accept_sampled.argtypes = [p, ll, i, p, ll, p, p, p, p, p, p, i, i, i, p, ll, p]
+    lib.kda_attn_rows_work_bytes.argtypes = [i, i, i, i]
+    lib.kda_accept_sampled_work_bytes.argtypes = [i, i, i]
+    for fn in (lib.kda_attn_rows_work_bytes, lib.kda_accept_sampled_work_bytes):
+        fn.restype = ll
+    for fn in (lib.kda_cache_append, lib.kda_attn_rows, lib.kda_accept_sampled):
         fn.restype = i
     for fn in (lib.kda_scan_rows, lib.kda_snapshot, lib.kda_replay, lib.kda_scan_batched,
                lib.kda_verify_round, lib.kda_accept_greedy, lib.kda_conv_reroll,
@@ -773,6 +794,130 @@ def kda_logprobs(logits, tokens=None, lp=None, entropy=None, top_ids=None, top_l
         _ptr(top_lp, "top_lp", f32, (t, n), dev), wp, wn, st))
 
 
+def attn_workspace(R: int, B: int, H: int, Hk: int, device=None) -> torch.Tensor:
+    """Scratch for kda_attn_rows calls of up to R rows and B sequences, with H heads over Hk
+    key heads (uint8, contents irrelevant).  Calls that may run at the same time need their own."""
+    return _workspace(_work_bytes(load().kda_attn_rows_work_bytes, R, B, H, Hk), device)
+
+
+def accept_sampled_workspace(R: int, B: int, V: int, device=None) -> torch.Tensor:
+    """Scratch for a kda_accept_sampled call of R rows of V logits in B sessions."""
+    return _workspace(_work_bytes(load().kda_accept_sampled_work_bytes, R, B, V), device)
+
+
+def _strided(t, name: str, dtype, shape, device):
+    """Address of rows [R][heads][D] and their stride: each row contiguous."""
+    if t.dtype != dtype:
+        raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
+    if t.shape != shape:
+        raise ValueError(f"{name} has shape {tuple(t.shape)}, expected {tuple(shape)}")
+    if t.device != device:
+        raise ValueError(f"{name} is on {t.device}, expected {device}")
+    if t.stride(2) != 1 or (shape[1] > 1 and t.stride(1) != D):
+        raise ValueError(f"{name}: the heads of a row must be contiguous")
+    return t.data_ptr(), t.stride(0)
+
+
+def _cache(k_pages, v_pages, table, lens, dtype, device):
+    """The cache's description, and its sequences and key heads."""
+    if k_pages.dim() != 4 or k_pages.shape[3] != D:
+        raise ValueError(f"k_pages must be [pages][rows][Hk][{D}], got {tuple(k_pages.shape)}")
+    for t, n in ((k_pages, "k_pages"), (v_pages, "v_pages")):
+        if t.dtype != dtype:
+            raise TypeError(f"{n} must be {dtype}, got {t.dtype}")
+        if t.device != device:
+            raise ValueError(f"{n} is on {t.device}, expected {device}")
+    if v_pages.shape != k_pages.shape or v_pages.stride() != k_pages.stride():
+        raise ValueError("k_pages and v_pages must have the same shape and strides")
+    if k_pages.stride(3) != 1:
+        raise ValueError("the rows of a page must be contiguous")
+    if table.dim() != 2:
+        raise ValueError("table must be a [B][pages of a sequence] tensor")
+    B, seq_pages = table.shape
+    pages, rows, Hk, _ = k_pages.shape
+    _int32(pages, rows, seq_pages)
+    c = _Cache(k_pages.data_ptr(), v_pages.data_ptr(), _ptr(table, "table", torch.int32, (B, seq_pages), device),
+               _ptr(lens, "lens", torch.int32, (B,), device), *k_pages.stride()[:3], pages, rows, seq_pages)
+    return ctypes.byref(c), B, Hk
+
+
+def kda_cache_append(k, v, k_pages, v_pages, table, lens, offsets, stream=None) -> None:
+    """Writes the keys and values of packed new rows to their places in a paged cache.
+
+    k, v [R][Hk][D] (any row stride); k_pages, v_pages [pages][rows][Hk][D] of the same dtype,
+    any strides that keep a head's row contiguous; table [B][pages of a sequence] int32; lens
+    [B] int32, the sequences' lengths with the new rows; offsets [B+1] int32.
+    """
+    lib = load()
+    dev, st = _place(k, stream)
+    dt = _row_dtype(k, "k")
+    c, B, Hk = _cache(k_pages, v_pages, table, lens, k.dtype, dev)
+    R = k.shape[0]
+    kp, k_ld = _strided(k, "k", k.dtype, (R, Hk, D), dev)
+    vp, v_ld = _strided(v, "v", k.dtype, (R, Hk, D), dev)
+    _check(lib.kda_cache_append(kp, k_ld, vp, v_ld, c, _ptr(offsets, "offsets", torch.int32, (B + 1,), dev),
+                                R, B, Hk, dt, st))
+
+
+def kda_attn_rows(q, k_pages, v_pages, table, lens, offsets, o, scale=None, window: int = 0,
+                  sinks: int = 0, work=None, stream=None) -> None:
+    """Attention of packed new rows over a paged cache that holds their keys and values already.
+
+    q [R][H][D] (any row stride) and o [R][H][D] in the cache's dtype, H a multiple of Hk; the
+    cache, table, lens and offsets as kda_cache_append.  A row at position p sees positions up to
+    p; with a window only those > p - window or < sinks.  scale is 1/sqrt(D) unless given.
+    work = attn_workspace(R, B, H, Hk).
+    """
+    lib = load()
+    dev, st = _place(q, stream)
+    if q.dim() != 3:
+        raise ValueError(f"q must be [R][H][{D}], got {tuple(q.shape)}")
+    dt = _row_dtype(q, "q")
+    c, B, Hk = _cache(k_pages, v_pages, table, lens, q.dtype, dev)
+    R, H = q.shape[:2]
+    _int32(R, H, window, sinks)
+    qp, q_ld = _strided(q, "q", q.dtype, (R, H, D), dev)
+    wp, wn = _work(work, dev)
+    _check(lib.kda_attn_rows(qp, q_ld, c, _ptr(offsets, "offsets", torch.int32, (B + 1,), dev),
+                             _ptr(o, "o", q.dtype, (R, H, D), dev), R, B, H, Hk,
+                             D ** -0.5 if scale is None else scale, window, sinks, dt, wp, wn, st))
+
+
+def kda_accept_sampled(logits, offsets, drafts, u, out, probs=None, temp=None, p_draft=None,
+                       work=None, stream=None) -> None:
+    """Sampled accept: drafted tokens verified against the target's probabilities from given
+    random numbers, and the token that follows them (see include/kda.h).
+
+    logits [R][V] float32 or bfloat16 and probs [R][V] float32 (None: drafts that were not
+    drawn), unit element stride; offsets [B+1] int32, the sessions' rows; drafts [R] int32 or
+    uint32; u [R] float32 in [0, 1); temp [B] float32 or None; out [B][2] int32 or uint32
+    receives (accepted drafts, token), p_draft [R] float32 the drafts' probabilities.
+    work = accept_sampled_workspace(R, B, V).
+    """
+    lib = load()
+    dev, st = _place(logits, stream)
+    if logits.dim() != 2:
+        raise ValueError("logits must be a [R][V] tensor")
+    R, V = logits.shape
+    _int32(R, V)
+    dt = _row_dtype(logits, "logits")
+    f32 = torch.float32
+    for t, n in ((logits, "logits"), (probs, "probs")):
+        if t is None:
+            continue
+        if t.shape != (R, V) or t.device != dev or (V > 1 and t.stride(1) != 1):
+            raise ValueError(f"{n} must be [{R}][{V}] on {dev} with contiguous rows")
+    if probs is not None and probs.dtype != f32:
+        raise TypeError(f"probs must be float32, got {probs.dtype}")
+    B = offsets.shape[0] - 1 if offsets.dim() == 1 else -1
+    wp, wn = _work(work, dev)
+    _check(lib.kda_accept_sampled(
+        logits.data_ptr(), logits.stride(0), dt, None if probs is None else probs.data_ptr(),
+        V if probs is None else probs.stride(0), _ptr(offsets, "offsets", torch.int32, (B + 1,), dev),
+        _ids(drafts, "drafts", (R,), dev), _ptr(u, "u", f32, (R,), dev), _ptr(temp, "temp", f32, (B,), dev),
+        _ids(out, "out", (B, 2), dev), _ptr(p_draft, "p_draft", f32, (R,), dev), R, B, V, wp, wn, st))
+
+
 def kda_abi_version() -> int:
     return int(load().kda_abi_version())
 
@@ -789,5 +934,6 @@ __all__ = [
     "kda_verify_round_multi", "MAX_PREV_ROUNDS", "kda_scan_rows_columns", "kda_scan_rows_stash",
     "kda_replay_stash", "kda_accept_greedy_noalloc", "kda_prompt", "prompt_workspace",
     "kda_linear_prompt", "linear_workspace", "kda_linear_step", "kda_logprobs",
-    "logprobs_workspace", "TOP_MAX",
+    "logprobs_workspace", "TOP_MAX", "kda_cache_append", "kda_attn_rows", "attn_workspace",
+    "kda_accept_sampled", "accept_sampled_workspace",
 ]

@@ -22,8 +22,8 @@ CSRC = os.path.join(PKG, "csrc")
 INCLUDE = os.path.join(ROOT, "include")
 LIB = os.path.join(PKG, "libkda.so")
 SOURCES = [os.path.join(CSRC, n) for n in
-           ("kda_kernels.hip", "kda_prompt.hip", "kda_logprobs.hip", "kda_abi.cpp",
-            "kda_ops_abi.cpp")]
+           ("kda_kernels.hip", "kda_prompt.hip", "kda_logprobs.hip", "kda_attn.hip", "kda_sample.hip",
+            "kda_abi.cpp", "kda_ops_abi.cpp", "kda_cache_abi.cpp")]
 
 HIPCC = os.environ.get("HIPCC", "/opt/rocm/bin/hipcc")
 

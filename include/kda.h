@@ -52,7 +52,7 @@ extern "C" {
 #define KDA_HEAD_DIM 128   /* d_k = d_v; glm5_spec_ppn_gate.rs fixture head_dim */
 #define KDA_T_MAX 15       /* verify rows per round: K + 1 <= 15 (glm_spec.rs, WALK-REUSE) */
 #define KDA_B_MAX 15       /* batched-decode sessions per step (same knee) */
-#define KDA_ABI_VERSION 11
+#define KDA_ABI_VERSION 12
 #define KDA_ACCEPT_WORK_BYTES 12288   /* workspace of kda_accept_greedy */
 #define KDA_NO_TOKEN 0xFFFFFFFFu      /* argmax slot of a logits row holding a NaN */
 #define KDA_CONV_RING_ROWS 3          /* short-conv history: kernel size 4 keeps 3 raw rows */
@@ -60,6 +60,7 @@ extern "C" {
 #define KDA_PROMPT_ROWS_MAX 268435456 /* packed rows of one prompt call */
 #define KDA_PROMPT_SEQS_MAX 4096      /* sequences of one prompt call */
 #define KDA_TOP_MAX 32                /* alternatives kda_logprobs lists for a row */
+#define KDA_PAGE_ROWS_MAX 65536       /* rows of a page of the attention cache */
 
 enum { KDA_IN_F32 = 0, KDA_IN_BF16 = 1 };
 
@@ -513,6 +514,138 @@ int kda_logprobs(const void* logits, int t, int V, long long ld, int in_dtype,
                  float* top_lp, void* work, long long work_bytes, void* stream);
 /* Workspace bytes of kda_logprobs; -1 on a bad count. */
 long long kda_logprobs_work_bytes(int t, int V, int n_top);
+
+/*
+ * The paged cache of an attention layer beside the KDA layers: the keys and
+ * values of B sequences, in pages of page_rows rows, each row Hk heads of
+ * KDA_HEAD_DIM.  A HOST struct; the pointers in it are device pointers.
+ *   k, v      : row r of page n, head h, starts at element n * page_stride +
+ *               r * row_stride + h * head_stride.  16-byte aligned, strides too,
+ *               so that [page][row][head][128] and [page][head][row][128] both
+ *               fit, and k and v may lie in one buffer, page by page or row by
+ *               row.  No two rows may overlap.
+ *   table     : [B][seq_pages] int32, the pages of each sequence in order.  An
+ *               entry outside 0..pages-1 names no page: nothing is written there,
+ *               and no row sees its keys (a page that a window has left behind,
+ *               for example).  Sequences may share pages that are only read.
+ *   lens      : B int32, the rows of each sequence WITH the call's new rows: new
+ *               row i of n is at position lens[b] - n + i.  (Below zero counts as
+ *               zero.)  A rollback is a smaller length: glm_spec.rs (0.123.0),
+ *               module doc ROLLBACK, truncates the attention layers' rows so.
+ *   pages     : pages in k and v, >= 1.   page_rows : a power of two up to
+ *               KDA_PAGE_ROWS_MAX.   seq_pages * page_rows <= 2^31 - 1.
+ */
+typedef struct {
+    void* k;
+    void* v;
+    const int32_t* table;
+    const int32_t* lens;
+    long long page_stride;
+    long long row_stride;
+    long long head_stride;
+    int pages;
+    int page_rows;
+    int seq_pages;
+} kda_cache;
+
+/*
+ * Writes the keys and values of packed new rows to their places in the cache.
+ *   k, v      : R rows of [Hk][128] in in_dtype (the cache's type), k_ld and v_ld
+ *               elements apart (>= Hk*128; 16-byte aligned rows): slices of one
+ *               projection's output will do.
+ *   offsets   : as kda_prompt.  Rows at positions below zero or behind the
+ *               table, or whose entry names no page, are not written; nor is any
+ *               other row of the cache.
+ *   Two new rows that go to one place (a page that two entries name) leave one
+ *   of them, or pieces of both.
+ *   0 <= R, R + B < 2^24, 1 <= B <= KDA_PROMPT_SEQS_MAX, 1 <= Hk <= 65535.
+ */
+int kda_cache_append(const void* k, long long k_ld, const void* v, long long v_ld,
+                     const kda_cache* cache, const int32_t* offsets, int R, int B, int Hk,
+                     int in_dtype, void* stream);
+
+/*
+ * Attention of packed new rows (one token of each session, a verify round's
+ * rows, a prompt's chunk) over the paged cache, which holds the new rows' own
+ * keys and values already (kda_cache_append).  Row i of sequence b, at position
+ * p = lens[b] - n + i, head h, which reads key head h / (H / Hk):
+ *     o = sum_j softmax_j(scale q . k_j) v_j
+ * over the positions 0 <= j <= p whose entry names a page; with a window, only
+ * those with j > p - window or j < sinks (first tokens that stay visible).
+ *   glm_spec.rs (0.123.0), module doc WALK-REUSE: the attention layers' verify
+ *   rows run as one call over the cached rows, each at its own position.
+ *   q         : R rows of [H][128] in in_dtype, q_ld elements apart (>= H*128;
+ *               16-byte aligned rows).
+ *   o         : [R][H][128] in in_dtype, contiguous.  (Not f32 for bf16 rows, as
+ *               the scans' outputs are: it goes into a projection as it is.)  Rows that
+ *               no sequence covers are not written.
+ *   scale     : > 0, finite; 1/sqrt(128) as a rule.
+ *   window    : 0 for none; sinks >= 0, and 0 without a window.
+ *   A row that sees no key gives 0.  A score of -inf counts as not seen; a NaN or
+ *   +inf score makes NaN of its row's head.  A NaN or an infinity in a value makes
+ *   a NaN or an infinity of its channel for the rows that see it; what lies in keys and
+ *   values that a row does not see has no effect on it.
+ *   Sums are f32.  The weights of bf16 rows are rounded to bf16 for their product
+ *   with the values.  Results are deterministic; they depend on R, B, H and Hk, and on
+ *   the lengths of all sequences, only in how sums are divided.
+ *   work      : kda_attn_rows_work_bytes(R, B, H, Hk) bytes, 16-byte aligned, in any
+ *               state on entry.  Calls that can run at the same time need
+ *               different work buffers.
+ *   0 <= R <= KDA_PROMPT_ROWS_MAX, 1 <= B <= KDA_PROMPT_SEQS_MAX, Hk divides H <= 65535,
+ *   as long as the grid holds them (refused beyond).  With R = 0 nothing is enqueued.
+ */
+int kda_attn_rows(const void* q, long long q_ld, const kda_cache* cache, const int32_t* offsets,
+                  void* o, int R, int B, int H, int Hk, float scale, int window, int sinks,
+                  int in_dtype, void* work, long long work_bytes, void* stream);
+/* Workspace bytes of kda_attn_rows (they never shrink as R or B grow); -1 on a bad count. */
+long long kda_attn_rows_work_bytes(int R, int B, int H, int Hk);
+
+/*
+ * Sampled accept of B sessions' verify rounds: drafted tokens verified against
+ * the target's probabilities from given random numbers.
+ *   glm_spec.rs (0.123.0), the sampled accept: a rejection walk u * q < p, a draw
+ *   from the residual at the first rejected row, a bonus draw if none is.
+ * Session b has rows offsets[b] .. offsets[b+1]-1 (as kda_prompt; n of them, the
+ * last without a draft).  With p_r = softmax(x_r / T) of row r's logits:
+ *     draft r is accepted while u_r q_r(d_r) < p_r(d_r);  j = accepted drafts
+ *     j < n-1 : weights max(p_j - q_j, 0) of row j (if all are 0: p_j)
+ *     j = n-1 : weights p_j (the bonus token; the only draw of a session with one row)
+ *     token   = the lowest v with  sum_{w <= v} weight > u_last * sum of all
+ *               (u_last: of the session's last row, independent of the others)
+ *   logits    : R rows of V logits in in_dtype, ld elements apart (>= V), element
+ *               alignment.  -inf: a masked token.
+ *   probs     : R rows of V f32, the probabilities q that the drafts were drawn
+ *               from, probs_ld elements apart; the last row of a session is not
+ *               read.  NULL: the drafts were not drawn (q = 1 at the draft, 0
+ *               elsewhere).
+ *   drafts    : R u32, drafts[r] verified by row r (the last row's is not read).
+ *               A draft >= V is never accepted.
+ *   u         : R f32 in [0, 1).
+ *   temp      : B f32, the sessions' temperatures, or NULL for 1.
+ *   out       : [B][2] u32, {j, token}: for one session what kda_accept_greedy
+ *               writes to out2, so that kda_verify_round_dev and
+ *               kda_conv_reroll_dev read j from it.  A session without rows is
+ *               left as it was.
+ *   p_draft   : R f32, p_r(d_r) of the rows with a draft (others are left as they
+ *               were), or NULL.
+ *   A row that holds a NaN or +inf, or whose logits are all -inf, has no
+ *   distribution: no draft is accepted there, its p_draft is NaN, and if the walk ends
+ *   there the token is KDA_NO_TOKEN.  A temperature that is no positive finite
+ *   number: j = 0, KDA_NO_TOKEN and NaN.
+ *   Weights and running sums are f64, and so is the sum of a row's exponentials,
+ *   which are f32: p is good to about 1e-6 of itself.
+ *   work      : kda_accept_sampled_work_bytes(R, B, V) bytes, 16-byte aligned, in
+ *               any state on entry.  Calls that can run at the same time need
+ *               different work buffers.
+ *   0 <= R, 1 <= B <= KDA_PROMPT_SEQS_MAX, 1 <= V <= 2^30, R * ld <= 2^40.  With R = 0
+ *   nothing is enqueued.
+ */
+int kda_accept_sampled(const void* logits, long long ld, int in_dtype, const float* probs,
+                       long long probs_ld, const int32_t* offsets, const uint32_t* drafts,
+                       const float* u, const float* temp, uint32_t* out, float* p_draft, int R,
+                       int B, int V, void* work, long long work_bytes, void* stream);
+/* Workspace bytes of kda_accept_sampled; -1 on a bad count. */
+long long kda_accept_sampled_work_bytes(int R, int B, int V);
 
 /* Message for the last nonzero status returned on the calling thread. */
 const char* kda_last_error(void);
