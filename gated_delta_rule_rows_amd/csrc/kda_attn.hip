@@ -190,21 +190,22 @@ __device__ __forceinline__ Item find_item(const AttnArgs& a, const Plan& p, int 
     return f;
 }
 
-// Keys of a tile and where its 16-byte pieces lie in LDS.
+// The tile of keys.
 template <bool BF16, int WAVES>
 struct Shape {
     static constexpr int kEs = BF16 ? 2 : 4;
     static constexpr int kKeys = BF16 && WAVES == 4 ? 64 : 32;
     static constexpr int kBlocks = kKeys / 32;
-    static constexpr int kPieces = kD * kEs / 16;              // of a row
+    static constexpr int kPieces = kD * kEs / 16;              // 16-byte pieces of a row
+    // Pitches of the rows in LDS.  K: 16 rows of a 16-byte read lie on all banks.  V: four rows of 64
+    // bytes (bf16), or rows 4 apart of 128 bytes (f32).
+    static constexpr int kPitchK = kD * kEs + 16;
+    static constexpr int kPitchV = kD * kEs + (BF16 ? 64 : 32);
+    static constexpr int kTile = kKeys * (kPitchK + kPitchV);  // K, then V
     static constexpr int kThreads = WAVES * 64;
     static constexpr int kRowsAtOnce = kThreads / kPieces;     // rows that a load of all threads covers
     static constexpr int kLoads = kKeys / kRowsAtOnce;         // 16-byte loads a thread, for K and for V
 };
-
-// Piece c of row `key` lies at c ^ turn(key): eight rows that follow each other
-// spread a piece over eight 16-byte columns, four rows a pair of them over four pairs.
-__device__ __forceinline__ int turn(int key) { return (key & 3) << 1 | (key >> 2 & 1) | (key & 8); }
 
 __device__ __forceinline__ uint32_t bits(float x) { return __builtin_bit_cast(uint32_t, x); }
 __device__ __forceinline__ float real(uint32_t x) { return __builtin_bit_cast(float, x); }
@@ -222,20 +223,6 @@ __device__ __forceinline__ void halves(float x, float& a, float& b) {
     b = real(p[1]);
 }
 
-template <bool BF16>
-__device__ __forceinline__ bool not_finite(uint4 u) {
-    const uint32_t w[4] = {u.x, u.y, u.z, u.w};
-    bool bad = false;
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-        if constexpr (BF16)
-            bad |= (w[i] & 0x7F80u) == 0x7F80u || (w[i] & 0x7F800000u) == 0x7F800000u;
-        else
-            bad |= (w[i] & 0x7F800000u) == 0x7F800000u;
-    }
-    return bad;
-}
-
 __device__ __forceinline__ f32x16 mfma(uint4 a, uint4 b, f32x16 c) {
     return __builtin_amdgcn_mfma_f32_32x32x16_bf16(__builtin_bit_cast(bf16x8, a), __builtin_bit_cast(bf16x8, b), c, 0, 0, 0);
 }
@@ -244,19 +231,11 @@ __device__ __forceinline__ f32x16 mfma(float a, float b, f32x16 c) {
     return __builtin_amdgcn_mfma_f32_32x32x2f32(a, b, c, 0, 0, 0);
 }
 
-// The V operand of 16 keys (from key0 on) and 32 channels (block db): a lane's channel, its keys
-// in the accumulators' order: key0 + 4 half + 0..3, then 8 further on.
-__device__ __forceinline__ uint4 values_of(const uint4* v, int key0, int db) {
-    const int lane = threadIdx.x & 63, i = lane & 15;
-    const int key = key0 + 4 * (lane >> 5) + (i >> 2), c = 4 * db + 2 * (lane >> 4 & 1) + (i >> 1 & 1);
-    const char* base = reinterpret_cast<const char*>(v);
+// Four keys of the lane's channel, from V by row (transposed on the way): lane i of 16 brings piece
+// i & 3 of row i >> 2, of 4 channels, and gets channel i.
+__device__ __forceinline__ uint2 four_keys(const char* at) {
     using Lds = __attribute__((address_space(3))) s16x4;
-    const auto read = [&](int k) {
-        return __builtin_bit_cast(uint2, __builtin_amdgcn_ds_read_tr16_b64_v4i16(
-            (Lds*)(base + (k * 16 + (c ^ turn(k))) * 16 + (i & 1) * 8)));
-    };
-    const uint2 x = read(key), y = read(key + 8);
-    return make_uint4(x.x, x.y, y.x, y.y);
+    return __builtin_bit_cast(uint2, __builtin_amdgcn_ds_read_tr16_b64_v4i16((Lds*)at));
 }
 
 // The workspace: for each tile of columns its first item and its splits, then
@@ -275,71 +254,71 @@ struct Partials {
     }
 };
 
-// One bf16 pair: what is finite, and 1 where a value is not.
-__device__ __forceinline__ void part_finite(uint32_t& x, uint32_t& bad) {
-    const uint32_t lo = (x & 0x7F80u) == 0x7F80u ? 0xFFFFu : 0u, hi = (x & 0x7F800000u) == 0x7F800000u ? 0xFFFF0000u : 0u;
-    bad = (lo | hi) & 0x3F803F80u;
-    x &= ~(lo | hi);
+// Makes what is not finite 0, and says in a bit a channel where that was.
+template <bool BF16>
+__device__ __forceinline__ uint32_t part_finite(uint4& u) {
+    uint32_t w[4] = {u.x, u.y, u.z, u.w}, bad = 0;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        if constexpr (BF16) {
+            const bool lo = (w[i] & 0x7F80u) == 0x7F80u, hi = (w[i] & 0x7F800000u) == 0x7F800000u;
+            bad |= (lo ? 1u : 0u) << 2 * i | (hi ? 2u : 0u) << 2 * i;
+            w[i] &= (lo ? 0u : 0xFFFFu) | (hi ? 0u : 0xFFFF0000u);
+        } else {
+            const bool all = (w[i] & 0x7F800000u) == 0x7F800000u;
+            bad |= (all ? 1u : 0u) << i;
+            w[i] = all ? 0u : w[i];
+        }
+    }
+    u = make_uint4(w[0], w[1], w[2], w[3]);
+    return bad;
 }
 
-// O^T += V^T P^T over a tile.  SPOILED: V holds a NaN or an infinity, and not every row sees every
-// key.  A product would carry 0 x NaN into rows that do not see it, so the finite part is multiplied
-// by itself, and the channels that a row sees such a value of are found by a product of ones.
-// P is rounded to bf16 there, by half a step of 2^-8 at most, and l sums it unrounded.
-template <bool BF16, int NB, bool SPOILED>
-__device__ __forceinline__ void add_values(f32x16 (&acc)[4], const f32x16 (&s)[NB], const uint4* v, uint32_t seen) {
-    const int lane = threadIdx.x & 63, half = lane >> 5, col = lane & 31;
+// O^T += V^T P^T over a tile; v: the lane's place in its V.  P is rounded to bf16 for a bf16 cache, by
+// half a step of 2^-8 at most; l sums it unrounded.
+template <bool BF16, int NB, int PITCH>
+__device__ __forceinline__ void add_values(f32x16 (&acc)[4], const f32x16 (&s)[NB], const char* v) {
+    if constexpr (BF16) {
 #pragma unroll
-    for (int d = 0; d < 4; ++d) {
-        f32x16 hit;
-        if constexpr (SPOILED)
+        for (int b = 0; b < NB; ++b)
 #pragma unroll
-            for (int r = 0; r < 16; ++r) hit[r] = 0.f;
-        if constexpr (BF16) {
+            for (int step = 0; step < 2; ++step) {
+                const auto p = [&](int i) { return pack(s[b][8 * step + i], s[b][8 * step + i + 1]); };
+                const uint4 w = make_uint4(p(0), p(2), p(4), p(6));
 #pragma unroll
-            for (int b = 0; b < NB; ++b)
-#pragma unroll
-                for (int step = 0; step < 2; ++step) {
-                    const auto p = [&](int i) { return pack(s[b][8 * step + i], s[b][8 * step + i + 1]); };
-                    uint4 u = values_of(v, 32 * b + 16 * step, d);
-                    if constexpr (SPOILED) {
-                        uint4 bad;
-                        part_finite(u.x, bad.x);
-                        part_finite(u.y, bad.y);
-                        part_finite(u.z, bad.z);
-                        part_finite(u.w, bad.w);
-                        const uint32_t at = seen >> (16 * b + 8 * step);
-                        const auto one = [&](int i) { return (at >> i & 1) * 0x3F80u | (at >> (i + 1) & 1) * 0x3F800000u; };
-                        hit = mfma(bad, make_uint4(one(0), one(2), one(4), one(6)), hit);
-                    }
-                    acc[d] = mfma(u, make_uint4(p(0), p(2), p(4), p(6)), acc[d]);
+                for (int d = 0; d < 4; ++d) {
+                    const char* at = v + (32 * b + 16 * step) * PITCH + 64 * d;
+                    const uint2 x = four_keys(at), y = four_keys(at + 8 * PITCH);
+                    acc[d] = mfma(make_uint4(x.x, x.y, y.x, y.y), w, acc[d]);
                 }
-        } else {
-#pragma unroll
-            for (int r = 0; r < 16; ++r) {
-                const int key = 8 * (r >> 2) + 4 * half + (r & 3);
-                float u = reinterpret_cast<const float*>(v)[key * kD + (((8 * d + (col >> 2)) ^ turn(key)) * 4) + (col & 3)];
-                if constexpr (SPOILED) {
-                    const bool bad = (bits(u) & 0x7F800000u) == 0x7F800000u;
-                    hit = mfma(bad ? 1.f : 0.f, seen >> r & 1 ? 1.f : 0.f, hit);
-                    u = bad ? 0.f : u;
-                }
-                acc[d] = mfma(u, s[0][r], acc[d]);
             }
-        }
-        if constexpr (SPOILED)
+    } else {
 #pragma unroll
-            for (int r = 0; r < 16; ++r) acc[d][r] = hit[r] > 0.f ? __builtin_nanf("") : acc[d][r];
+        for (int r = 0; r < 16; ++r)
+#pragma unroll
+            for (int d = 0; d < 4; ++d)
+                acc[d] = mfma(*reinterpret_cast<const float*>(v + (8 * (r >> 2) + (r & 3)) * PITCH + 128 * d), s[0][r], acc[d]);
     }
 }
 
+// Where a lane reads V: bf16, by four_keys, rows 4 half + (i >> 2), channels 16 (lane >> 4 & 1) + 4 (i & 3)
+// on; f32, row 4 half, channel col.
+template <bool BF16, int PITCH>
+__device__ __forceinline__ int value_place() {
+    const int lane = threadIdx.x & 63, i = lane & 15;
+    if constexpr (BF16) return (4 * (lane >> 5) + (i >> 2)) * PITCH + 32 * (lane >> 4 & 1) + 8 * (i & 3);
+    return 4 * (lane >> 5) * PITCH + 4 * (lane & 31);
+}
+
 template <bool BF16, int WAVES, bool SPLIT>
-__global__ void __launch_bounds__(WAVES * 64) attn_kernel(AttnArgs a, Plan p) {
+__global__ void __launch_bounds__(WAVES * 64, WAVES == 4 ? 2 : 1) attn_kernel(AttnArgs a, Plan p) {
     using Sh = Shape<BF16, WAVES>;
     constexpr int KT = Sh::kKeys, ES = Sh::kEs, NB = Sh::kBlocks, PIECES = Sh::kPieces, LOADS = Sh::kLoads;
     constexpr int NQ = BF16 ? 8 : 16;   // 16-byte pieces of q a lane
-    __shared__ uint4 tile_k[2][KT * PIECES], tile_v[2][KT * PIECES];
-    __shared__ uint32_t spoiled[2][WAVES];
+    constexpr int PK = Sh::kPitchK, PV = Sh::kPitchV;
+    __shared__ __align__(16) char tiles[2][Sh::kTile];
+    __shared__ uint32_t spoiled[2][WAVES];          // whether a row of V that the wave brought is in odd
+    __shared__ uint8_t odd[2][KT * PIECES];
 
     const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6, half = lane >> 5, col = lane & 31;
     const int n_heads = a.Hk * p.groups;
@@ -395,18 +374,21 @@ __global__ void __launch_bounds__(WAVES * 64) attn_kernel(AttnArgs a, Plan p) {
         return t < t1 && key < keys ? table[key >> a.c.page_shift] : -1;
     };
     const int piece = tid % PIECES, row0 = tid / PIECES;
+    const int key_place = col * PK + half * 16, place_v = KT * PK + value_place<BF16, PV>();
     const char* k_base = static_cast<const char*>(a.c.k) + kh * a.c.head_stride * ES + piece * 16;
     const char* v_base = static_cast<const char*>(a.c.v) + kh * a.c.head_stride * ES + piece * 16;
     uint4 nk[LOADS], nv[LOADS];
     uint64_t there = 0, next_there = 0;   // the tile's rows that are
+    // A row that is not there is read as the cache's first row: no row sees it.
     const auto fetch = [&](int t, int entry) {
         const long long off = cache_at(a.c, entry, key_of(t) + lane % KT);
         next_there = __ballot(off >= 0);
+        const long long from = off >= 0 ? off * ES : 0;
 #pragma unroll
         for (int j = 0; j < LOADS; ++j) {
-            const long long at = __shfl(off, row0 + j * Sh::kRowsAtOnce) * ES;
-            nk[j] = at >= 0 ? *reinterpret_cast<const uint4*>(k_base + at) : make_uint4(0, 0, 0, 0);
-            nv[j] = at >= 0 ? *reinterpret_cast<const uint4*>(v_base + at) : make_uint4(0, 0, 0, 0);
+            const long long at = __shfl(from, row0 + j * Sh::kRowsAtOnce);
+            nk[j] = *reinterpret_cast<const uint4*>(k_base + at);
+            nv[j] = *reinterpret_cast<const uint4*>(v_base + at);
         }
     };
     // whether a row at positions from .. to does not see all of the tile's keys
@@ -414,18 +396,28 @@ __global__ void __launch_bounds__(WAVES * 64) attn_kernel(AttnArgs a, Plan p) {
         const int key = key_of(t);
         return key + KT - 1 > from || (a.window > 0 && to - key >= a.window && key + KT > a.sinks);
     };
+    const uint64_t all = KT == 64 ? ~0ull : 0xFFFFFFFFull;
+    // A NaN or an infinity in V that some row does not see (0 x NaN would carry it there) is made 0 in
+    // the tile, and its rows get a NaN afterwards: odd[] says which channels of which key.
     const auto keep = [&](int t, int buf) {
-        bool bad = false;
+        there = next_there;
+        if ((there & all) != all || partly(t, lo, hi)) {
+            uint32_t bad[LOADS], any = 0;
+#pragma unroll
+            for (int j = 0; j < LOADS; ++j) any |= bad[j] = part_finite<BF16>(nv[j]);
+            const bool some = __ballot(any != 0) != 0;
+            if (some)
+#pragma unroll
+                for (int j = 0; j < LOADS; ++j) odd[buf][(row0 + j * Sh::kRowsAtOnce) * PIECES + piece] = static_cast<uint8_t>(bad[j]);
+            if (lane == 0) spoiled[buf][wave] = some;
+        }
 #pragma unroll
         for (int j = 0; j < LOADS; ++j) {
-            const int key = row0 + j * Sh::kRowsAtOnce, at = key * PIECES + (piece ^ turn(key));
-            tile_k[buf][at] = nk[j];
-            tile_v[buf][at] = nv[j];
-            bad |= not_finite<BF16>(nv[j]);
+            char* at = tiles[buf] + j * Sh::kRowsAtOnce * PK;
+            *reinterpret_cast<uint4*>(at + row0 * PK + piece * 16) = nk[j];
+            at = tiles[buf] + KT * PK + j * Sh::kRowsAtOnce * PV;
+            *reinterpret_cast<uint4*>(at + row0 * PV + piece * 16) = nv[j];
         }
-        const bool any = __ballot(bad) != 0;
-        if (lane == 0) spoiled[buf][wave] = any;
-        there = next_there;
     };
 
     int entry = entry_of(t0);
@@ -449,10 +441,9 @@ __global__ void __launch_bounds__(WAVES * 64) attn_kernel(AttnArgs a, Plan p) {
             for (int b = 0; b < NB; ++b) {
 #pragma unroll
                 for (int r = 0; r < 16; ++r) s[b][r] = 0.f;
-                const int key = 32 * b + col;
 #pragma unroll
                 for (int x = 0; x < NQ; ++x) {
-                    const uint4 u = tile_k[buf][key * PIECES + ((2 * x + half) ^ turn(key))];
+                    const uint4 u = *reinterpret_cast<const uint4*>(tiles[buf] + key_place + 32 * b * PK + 32 * x);
                     if constexpr (BF16) {
                         s[b] = mfma(u, q[x], s[b]);
                     } else {
@@ -463,20 +454,17 @@ __global__ void __launch_bounds__(WAVES * 64) attn_kernel(AttnArgs a, Plan p) {
                     }
                 }
             }
-            const uint64_t all = KT == 64 ? ~0ull : 0xFFFFFFFFull;
             const bool masked = (now & all) != all || partly(t, wave_lo, wave_hi);
-            uint32_t seen = 0;
+            const auto sees = [&](int i) {   // key i of the tile, by this lane's column
+                const int key = key0 + i;
+                return (now >> i & 1) && key <= pos && (a.window <= 0 || pos - key < a.window || key < a.sinks);
+            };
             if (masked) {
 #pragma unroll
                 for (int b = 0; b < NB; ++b)
 #pragma unroll
-                    for (int r = 0; r < 16; ++r) {
-                        const int i = 32 * b + 8 * (r >> 2) + 4 * half + (r & 3), key = key0 + i;
-                        const bool sees = (now >> i & 1) && key <= pos &&
-                                          (a.window <= 0 || pos - key < a.window || key < a.sinks);
-                        s[b][r] = sees ? s[b][r] : -kInf;
-                        seen |= (sees ? 1u : 0u) << (16 * b + r);
-                    }
+                    for (int r = 0; r < 16; ++r)
+                        s[b][r] = sees(32 * b + 8 * (r >> 2) + 4 * half + (r & 3)) ? s[b][r] : -kInf;
             }
             float top = s[0][0];
 #pragma unroll
@@ -505,14 +493,26 @@ __global__ void __launch_bounds__(WAVES * 64) attn_kernel(AttnArgs a, Plan p) {
                     s[b][r] = __builtin_amdgcn_exp2f(fmaf(s[b][r], c, -base));
                     l += s[b][r];
                 }
-            bool spoil = false;
-            if (masked)
+            add_values<BF16, NB, PV>(acc, s, tiles[buf] + place_v);
+            uint32_t some = 0;
+            if ((now & all) != all || partly(t, lo, hi))   // as in keep
 #pragma unroll
-                for (int w = 0; w < WAVES; ++w) spoil |= spoiled[buf][w] != 0;
-            if (spoil)
-                add_values<BF16, NB, true>(acc, s, tile_v[buf], seen);
-            else
-                add_values<BF16, NB, false>(acc, s, tile_v[buf], seen);
+                for (int w = 0; w < WAVES; ++w) some |= spoiled[buf][w];
+            if (some) {
+                constexpr int ROWS = 64 / PIECES;   // of a wave in each load
+#pragma unroll 1
+                for (int i = 0; i < KT; ++i) {
+                    if (spoiled[buf][i / ROWS % WAVES] == 0 || !sees(i)) continue;
+#pragma unroll
+                    for (int d = 0; d < 4; ++d)
+#pragma unroll
+                        for (int r = 0; r < 16; ++r) {
+                            const uint32_t x = BF16 ? odd[buf][i * PIECES + 4 * d + (r >> 2)] >> (4 * half + (r & 3))
+                                                    : odd[buf][i * PIECES + 8 * d + 2 * (r >> 2) + half] >> (r & 3);
+                            acc[d][r] = x & 1 ? __builtin_nanf("") : acc[d][r];
+                        }
+                }
+            }
         }
         if (t + 1 < t1) keep(t + 1, buf ^ 1);
         __syncthreads();
