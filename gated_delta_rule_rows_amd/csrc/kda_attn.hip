@@ -39,9 +39,9 @@ constexpr float kInf = __builtin_inff();
 constexpr float kLog2e = 1.44269504088896340736f;
 constexpr float kSlack = 8.0f;        // the carried maximum may lag by this much (base 2)
 constexpr int kColumns = 32;          // columns of a wave
-constexpr int kTargetNarrow = 1024;   // workgroups that fill the chip: one wave each
+constexpr int kTargetNarrow = 2048;   // workgroups that fill the chip: one wave each
 constexpr int kTargetWide = 512;      // four waves each
-constexpr int kLeastTiles = 4;        // a split has this many tiles at least
+constexpr int kLeastTiles = 1;        // a split has this many tiles at least
 constexpr int kSplitKeys = 256;       // a cache of no more keys a sequence is never split
 constexpr int kAppendThreads = 256;
 constexpr int kJoinThreads = 256;
@@ -123,35 +123,38 @@ __device__ __forceinline__ Item find_item(const AttnArgs& a, const Plan& p, int 
     for (int b = from; b < to; ++b) most = max(most, row(b));
     int before = __shfl_up(running_max(most), 1);
     if (lane == 0) before = 0;
-    // tiles of columns and of keys of sequence b, whose rows are first .. last-1
-    const auto tiles = [&](int b, int first, int last, int& across, int& along) {
-        across = div_up(last - first, p.rows);
-        along = 0;
-        if (across == 0) return;
-        const int hi = cache_pos(a.c.lens[b], last - 1, last);
-        along = key_tiles(max(hi - p.rows + 1, hi - (last - first) + 1), hi, capacity, a.window, a.sinks, kt).count;
+    // Calls back for each of the lane's sequences: its rows, tiles of columns and tiles of keys.
+    const auto visit = [&](auto&& with) {
+        int run = before;
+        for (int b = from; b < to; ++b) {
+            const int first = max(run, row(b)), last = min(max(a.offsets[b + 1], first), a.R);
+            run = first;
+            const int across = div_up(last - first, p.rows);
+            int along = 0;
+            if (across > 0) {
+                const int hi = cache_pos(a.c.lens[b], last - 1, last);
+                along = key_tiles(max(hi - p.rows + 1, hi - (last - first) + 1), hi, capacity, a.window, a.sinks, kt).count;
+            }
+            with(b, first, last, across, along);
+        }
+    };
+    // up to 64 sequences, one a lane, are read once
+    int b1 = -1, first1 = 0, last1 = 0, across1 = 0, along1 = 0;
+    if (each == 1)
+        visit([&](int b, int first, int last, int across, int along) {
+            b1 = b; first1 = first; last1 = last; across1 = across; along1 = along;
+        });
+    const auto again = [&](auto&& with) {
+        if (each > 1) visit(with);
+        else if (b1 >= 0) with(b1, first1, last1, across1, along1);
     };
     long long units = 0;
-    int run = before;
-    for (int b = from; b < to; ++b) {
-        const int first = max(run, row(b)), last = min(max(a.offsets[b + 1], first), a.R);
-        run = first;
-        int across, along;
-        tiles(b, first, last, across, along);
-        units += static_cast<long long>(across) * along;
-    }
+    again([&](int, int, int, int across, int along) { units += static_cast<long long>(across) * along; });
 #pragma unroll
     for (int d = 32; d >= 1; d >>= 1) units += __shfl_xor(units, d);
     const int unit = max(kLeastTiles, static_cast<int>(min((units + p.parts - 1) / p.parts, 1ll << 30)));
     int mine = 0;
-    run = before;
-    for (int b = from; b < to; ++b) {
-        const int first = max(run, row(b)), last = min(max(a.offsets[b + 1], first), a.R);
-        run = first;
-        int across, along;
-        tiles(b, first, last, across, along);
-        mine += across * max(1, div_up(along, unit));
-    }
+    again([&](int, int, int, int across, int along) { mine += across * max(1, div_up(along, unit)); });
     int upto = mine;
 #pragma unroll
     for (int d = 1; d < 64; d <<= 1) {
@@ -163,12 +166,7 @@ __device__ __forceinline__ Item find_item(const AttnArgs& a, const Plan& p, int 
     if (mask == 0) return f;
     const int owner = __builtin_ctzll(mask);
     int base = upto - mine;
-    run = before;
-    for (int b = from; b < to; ++b) {
-        const int first = max(run, row(b)), last = min(max(a.offsets[b + 1], first), a.R);
-        run = first;
-        int across, along;
-        tiles(b, first, last, across, along);
+    again([&](int b, int first, int last, int across, int along) {
         const int splits = max(1, div_up(along, unit));
         if (item >= base && item < base + across * splits) {
             f.b = b;
@@ -179,7 +177,7 @@ __device__ __forceinline__ Item find_item(const AttnArgs& a, const Plan& p, int 
             f.splits = splits;
         }
         base += across * splits;
-    }
+    });
     f.b = __builtin_amdgcn_readlane(f.b, owner);
     f.first = __builtin_amdgcn_readlane(f.first, owner);
     f.index = __builtin_amdgcn_readlane(f.index, owner);
@@ -310,246 +308,408 @@ __device__ __forceinline__ int value_place() {
     return 4 * (lane >> 5) * PITCH + 4 * (lane & 31);
 }
 
-template <bool BF16, int WAVES, bool SPLIT>
-__global__ void __launch_bounds__(WAVES * 64, WAVES == 4 ? 2 : 1) attn_kernel(AttnArgs a, Plan p) {
-    using Sh = Shape<BF16, WAVES>;
-    constexpr int KT = Sh::kKeys, ES = Sh::kEs, NB = Sh::kBlocks, PIECES = Sh::kPieces, LOADS = Sh::kLoads;
-    constexpr int NQ = BF16 ? 8 : 16;   // 16-byte pieces of q a lane
-    constexpr int PK = Sh::kPitchK, PV = Sh::kPitchV;
-    __shared__ __align__(16) char tiles[2][Sh::kTile];
-    __shared__ uint32_t spoiled[2][WAVES];          // whether a row of V that the wave brought is in odd
-    __shared__ uint8_t odd[2][KT * PIECES];
-
-    const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6, half = lane >> 5, col = lane & 31;
-    const int n_heads = a.Hk * p.groups;
-    const int hd = blockIdx.x % n_heads, place = blockIdx.x / n_heads;
+// What a workgroup computes: rows x heads columns, keys of tiles t0 .. t1-1.
+struct Work {
     Item f;
+    int hd;          // head part: key head and part of its query heads
+    int kh;
+    int heads;       // query heads of the part
+    int rows;        // rows of the tile of columns
+    int lo, hi;      // their positions
+    int t0, t1;
+    int keys;        // no row sees a key from here on
+    KeyTiles tiles;
+    long long head;  // first query head
+};
+
+template <int KT, bool SPLIT>
+__device__ __forceinline__ Work work_of(const AttnArgs& a, const Plan& p) {
+    Work w;
+    const int n_heads = a.Hk * p.groups, place = blockIdx.x / n_heads;
+    w.hd = blockIdx.x % n_heads;
     if constexpr (SPLIT) {
-        f = find_item(a, p, KT, place);
+        w.f = find_item(a, p, KT, place);
     } else {
         const Part part = find_part(a, p.rows, place);
-        f = Item{part.b, part.first + part.index * p.rows, part.last, 0, 1, part.index, part.first};
+        w.f = Item{part.b, part.first + part.index * p.rows, part.last, 0, 1, part.index, part.first};
     }
-    if (f.b < 0) return;
-    const int capacity = a.c.seq_pages << a.c.page_shift;
-    const int len = a.c.lens[f.b];
-    const int kh = hd / p.groups, g0 = hd % p.groups * p.heads, G = a.H / a.Hk;
-    const int heads = min(p.heads, G - g0), rows = min(p.rows, f.last - f.row);
-    // the tile's positions, and this wave's
-    const int lo = cache_pos(len, f.row, f.last), hi = lo + rows - 1;
-    const int c0 = wave * kColumns, row_lo = c0 / p.heads, row_hi = min((c0 + kColumns - 1) / p.heads, rows - 1);
-    const int wave_lo = lo + row_lo, wave_hi = lo + row_hi;
-    const bool active = row_lo < rows;
-    const int my_row = (c0 + col) / p.heads, my_head = (c0 + col) % p.heads;
-    const bool mine = my_row < rows && my_head < heads;
-    const int pos = mine ? lo + my_row : -1;
-    const long long q_head = static_cast<long long>(kh) * G + g0 + my_head;
+    if (w.f.b < 0) return w;
+    const int G = a.H / a.Hk, capacity = a.c.seq_pages << a.c.page_shift, g0 = w.hd % p.groups * p.heads;
+    w.kh = w.hd / p.groups;
+    w.head = static_cast<long long>(w.kh) * G + g0;
+    w.heads = min(p.heads, G - g0);
+    w.rows = min(p.rows, w.f.last - w.f.row);
+    w.lo = cache_pos(a.c.lens[w.f.b], w.f.row, w.f.last);
+    w.hi = w.lo + w.rows - 1;
+    w.tiles = key_tiles(w.lo, w.hi, capacity, a.window, a.sinks, KT);
+    w.t0 = static_cast<int>(static_cast<long long>(w.tiles.count) * w.f.split / w.f.splits);
+    w.t1 = static_cast<int>(static_cast<long long>(w.tiles.count) * (w.f.split + 1) / w.f.splits);
+    w.keys = min(w.hi + 1, capacity);
+    return w;
+}
 
-    // which of the tiles
-    const KeyTiles kt = key_tiles(lo, hi, capacity, a.window, a.sinks, KT);
-    const int t0 = static_cast<int>(static_cast<long long>(kt.count) * f.split / f.splits);
-    const int t1 = static_cast<int>(static_cast<long long>(kt.count) * (f.split + 1) / f.splits);
-    const int keys = min(hi + 1, capacity);   // no row sees a key from here on
-    const auto key_of = [&](int t) { return (t < kt.first ? t : t - kt.first + kt.from) * KT; };
+// First key of tile t.
+template <int KT>
+__device__ __forceinline__ int key_of(const Work& w, int t) {
+    return (t < w.tiles.first ? t : t - w.tiles.first + w.tiles.from) * KT;
+}
 
-    uint4 q[NQ];
-    {
-        const char* at = static_cast<const char*>(a.q) + ((f.row + my_row) * a.q_ld + q_head * kD) * ES + half * 16;
-#pragma unroll
-        for (int s = 0; s < NQ; ++s) q[s] = mine ? *reinterpret_cast<const uint4*>(at + s * 32) : make_uint4(0, 0, 0, 0);
-    }
+// The table entry of the lane's key of tile t; -1: none.
+template <int KT>
+__device__ __forceinline__ int entry_of(const AttnArgs& a, const Work& w, int t) {
+    const int key = key_of<KT>(w, t) + static_cast<int>(threadIdx.x & 63) % KT;
+    return t < w.t1 && key < w.keys ? a.c.table[static_cast<long long>(w.f.b) * a.c.seq_pages + (key >> a.c.page_shift)] : -1;
+}
 
-    f32x16 acc[4];
-#pragma unroll
-    for (int d = 0; d < 4; ++d)
-#pragma unroll
-        for (int r = 0; r < 16; ++r) acc[d][r] = 0.f;
-    float m = -kInf, l = 0.f;   // m in base 2
-    const float c = a.scale * kLog2e;
+// Whether a row at positions from .. to does not see all keys of the tile that begins at key.
+template <int KT>
+__device__ __forceinline__ bool partly(const AttnArgs& a, int key, int from, int to) {
+    return key + KT - 1 > from || (a.window > 0 && to - key >= a.window && key + KT > a.sinks);
+}
 
-    // The table entry of a lane's key of tile t (-1: none), and where the row lies.
-    const int32_t* table = a.c.table + static_cast<long long>(f.b) * a.c.seq_pages;
-    const auto entry_of = [&](int t) {
-        const int key = key_of(t) + lane % KT;
-        return t < t1 && key < keys ? table[key >> a.c.page_shift] : -1;
-    };
-    const int piece = tid % PIECES, row0 = tid / PIECES;
-    const int key_place = col * PK + half * 16, place_v = KT * PK + value_place<BF16, PV>();
-    const char* k_base = static_cast<const char*>(a.c.k) + kh * a.c.head_stride * ES + piece * 16;
-    const char* v_base = static_cast<const char*>(a.c.v) + kh * a.c.head_stride * ES + piece * 16;
-    uint4 nk[LOADS], nv[LOADS];
-    uint64_t there = 0, next_there = 0;   // the tile's rows that are
-    // A row that is not there is read as the cache's first row: no row sees it.
-    const auto fetch = [&](int t, int entry) {
-        const long long off = cache_at(a.c, entry, key_of(t) + lane % KT);
-        next_there = __ballot(off >= 0);
-        const long long from = off >= 0 ? off * ES : 0;
-#pragma unroll
-        for (int j = 0; j < LOADS; ++j) {
-            const long long at = __shfl(from, row0 + j * Sh::kRowsAtOnce);
-            nk[j] = *reinterpret_cast<const uint4*>(k_base + at);
-            nv[j] = *reinterpret_cast<const uint4*>(v_base + at);
-        }
-    };
-    // whether a row at positions from .. to does not see all of the tile's keys
-    const auto partly = [&](int t, int from, int to) {
-        const int key = key_of(t);
-        return key + KT - 1 > from || (a.window > 0 && to - key >= a.window && key + KT > a.sinks);
-    };
-    const uint64_t all = KT == 64 ? ~0ull : 0xFFFFFFFFull;
-    // A NaN or an infinity in V that some row does not see (0 x NaN would carry it there) is made 0 in
-    // the tile, and its rows get a NaN afterwards: odd[] says which channels of which key.
-    const auto keep = [&](int t, int buf) {
-        there = next_there;
-        if ((there & all) != all || partly(t, lo, hi)) {
-            uint32_t bad[LOADS], any = 0;
-#pragma unroll
-            for (int j = 0; j < LOADS; ++j) any |= bad[j] = part_finite<BF16>(nv[j]);
-            const bool some = __ballot(any != 0) != 0;
-            if (some)
-#pragma unroll
-                for (int j = 0; j < LOADS; ++j) odd[buf][(row0 + j * Sh::kRowsAtOnce) * PIECES + piece] = static_cast<uint8_t>(bad[j]);
-            if (lane == 0) spoiled[buf][wave] = some;
-        }
-#pragma unroll
-        for (int j = 0; j < LOADS; ++j) {
-            char* at = tiles[buf] + j * Sh::kRowsAtOnce * PK;
-            *reinterpret_cast<uint4*>(at + row0 * PK + piece * 16) = nk[j];
-            at = tiles[buf] + KT * PK + j * Sh::kRowsAtOnce * PV;
-            *reinterpret_cast<uint4*>(at + row0 * PV + piece * 16) = nv[j];
-        }
-    };
+// The lowest n bits.
+__device__ __forceinline__ uint32_t low_bits(int n) { return n <= 0 ? 0u : n >= 32 ? ~0u : (1u << n) - 1; }
 
-    int entry = entry_of(t0);
-    if (t0 < t1) {
-        fetch(t0, entry);
-        entry = entry_of(t0 + 1);
-        keep(t0, 0);
-    }
-    __syncthreads();
-    for (int t = t0; t < t1; ++t) {
-        const int buf = (t - t0) & 1;
-        const uint64_t now = there;
-        if (t + 1 < t1) {
-            fetch(t + 1, entry);
-            entry = entry_of(t + 2);
-        }
-        const int key0 = key_of(t);
-        if (active && key0 <= wave_hi) {
-            f32x16 s[NB];
-#pragma unroll
-            for (int b = 0; b < NB; ++b) {
-#pragma unroll
-                for (int r = 0; r < 16; ++r) s[b][r] = 0.f;
-#pragma unroll
-                for (int x = 0; x < NQ; ++x) {
-                    const uint4 u = *reinterpret_cast<const uint4*>(tiles[buf] + key_place + 32 * b * PK + 32 * x);
-                    if constexpr (BF16) {
-                        s[b] = mfma(u, q[x], s[b]);
-                    } else {
-                        s[b] = mfma(real(u.x), real(q[x].x), s[b]);
-                        s[b] = mfma(real(u.y), real(q[x].y), s[b]);
-                        s[b] = mfma(real(u.z), real(q[x].z), s[b]);
-                        s[b] = mfma(real(u.w), real(q[x].w), s[b]);
-                    }
-                }
-            }
-            const bool masked = (now & all) != all || partly(t, wave_lo, wave_hi);
-            const auto sees = [&](int i) {   // key i of the tile, by this lane's column
-                const int key = key0 + i;
-                return (now >> i & 1) && key <= pos && (a.window <= 0 || pos - key < a.window || key < a.sinks);
-            };
-            if (masked) {
-#pragma unroll
-                for (int b = 0; b < NB; ++b)
-#pragma unroll
-                    for (int r = 0; r < 16; ++r)
-                        s[b][r] = sees(32 * b + 8 * (r >> 2) + 4 * half + (r & 3)) ? s[b][r] : -kInf;
-            }
-            float top = s[0][0];
-#pragma unroll
-            for (int b = 0; b < NB; ++b)
-#pragma unroll
-                for (int r = 0; r < 16; ++r) top = fmaxf(top, s[b][r]);
-            float x, y;
-            halves(top, x, y);
-            top = fmaxf(x, y) * c;
-            const bool up = top > m + kSlack || (m == -kInf && top > m);
-            if (__ballot(up)) {   // each column by itself: no other column's values move its maximum
-                const float to = up ? top : m;
-                const float by = m == -kInf ? 0.f : __builtin_amdgcn_exp2f(m - to);
-                m = to;
-                l *= by;
-#pragma unroll
-                for (int d = 0; d < 4; ++d)
-#pragma unroll
-                    for (int r = 0; r < 16; ++r) acc[d][r] *= by;
-            }
-            const float base = m == -kInf ? 0.f : m;
-#pragma unroll
-            for (int b = 0; b < NB; ++b)
-#pragma unroll
-                for (int r = 0; r < 16; ++r) {
-                    s[b][r] = __builtin_amdgcn_exp2f(fmaf(s[b][r], c, -base));
-                    l += s[b][r];
-                }
-            add_values<BF16, NB, PV>(acc, s, tiles[buf] + place_v);
-            uint32_t some = 0;
-            if ((now & all) != all || partly(t, lo, hi))   // as in keep
-#pragma unroll
-                for (int w = 0; w < WAVES; ++w) some |= spoiled[buf][w];
-            if (some) {
-                constexpr int ROWS = 64 / PIECES;   // of a wave in each load
-#pragma unroll 1
-                for (int i = 0; i < KT; ++i) {
-                    if (spoiled[buf][i / ROWS % WAVES] == 0 || !sees(i)) continue;
-#pragma unroll
-                    for (int d = 0; d < 4; ++d)
-#pragma unroll
-                        for (int r = 0; r < 16; ++r) {
-                            const uint32_t x = BF16 ? odd[buf][i * PIECES + 4 * d + (r >> 2)] >> (4 * half + (r & 3))
-                                                    : odd[buf][i * PIECES + 8 * d + 2 * (r >> 2) + half] >> (r & 3);
-                            acc[d][r] = x & 1 ? __builtin_nanf("") : acc[d][r];
-                        }
-                }
-            }
-        }
-        if (t + 1 < t1) keep(t + 1, buf ^ 1);
-        __syncthreads();
-    }
+// Which of the 32 keys from key0 on a row at pos (-1: none) sees, of those that exist.
+__device__ __forceinline__ uint32_t seen_by(const AttnArgs& a, uint32_t there, int pos, int key0) {
+    uint32_t seen = there & low_bits(pos - key0 + 1);
+    // (where the first difference wraps around, pos is before key0: nothing is seen)
+    if (a.window > 0)
+        seen &= ~low_bits(static_cast<int>(static_cast<uint32_t>(pos) - static_cast<uint32_t>(a.window) + 1u - static_cast<uint32_t>(key0))) |
+                low_bits(a.sinks - key0);
+    return seen;
+}
 
-    float x, y;
-    halves(l, x, y);
-    l = x + y;
-    if (SPLIT && f.split == 0 && hd == 0 && tid == 0)
-        Partials(a.work, p, n_heads).tiles[f.first / p.rows + f.b + f.index] = make_int2(place, f.splits);
-    if (!mine) return;
-    if (SPLIT && f.splits > 1) {
-        const Partials w(a.work, p, n_heads);
-        const long long at = (static_cast<long long>(place) * n_heads + hd) * p.cols + c0 + col;
-        if (half == 0) w.ml[at] = make_float2(m, l);
-        float* o = w.o + at * kD;
+// A wave's columns: a lane's column, in both halves, and what it carries.
+template <bool BF16>
+struct Columns {
+    static constexpr int kQ = BF16 ? 8 : 16;   // 16-byte pieces of q a lane
+    bool mine;       // the column exists
+    int row, head;   // within the tile
+    int pos;
+    uint4 q[kQ];
+    f32x16 acc[4];   // O^T
+    float m, l;      // m in base 2; l of the half's keys
+
+    __device__ __forceinline__ void begin(const AttnArgs& a, const Plan& p, const Work& w, int c0) {
+        constexpr int ES = BF16 ? 2 : 4;
+        const int lane = threadIdx.x & 63, half = lane >> 5, c = c0 + (lane & 31);
+        row = c / p.heads;
+        head = c % p.heads;
+        mine = row < w.rows && head < w.heads;
+        pos = mine ? w.lo + row : -1;
+        const char* at = static_cast<const char*>(a.q) + ((w.f.row + row) * a.q_ld + (w.head + head) * kD) * ES + half * 16;
+#pragma unroll
+        for (int x = 0; x < kQ; ++x) q[x] = mine ? *reinterpret_cast<const uint4*>(at + x * 32) : make_uint4(0, 0, 0, 0);
 #pragma unroll
         for (int d = 0; d < 4; ++d)
 #pragma unroll
-            for (int r = 0; r < 16; r += 4)
-                *reinterpret_cast<float4*>(o + 32 * d + 2 * r + 4 * half) =
-                    make_float4(acc[d][r], acc[d][r + 1], acc[d][r + 2], acc[d][r + 3]);
-        return;
+            for (int r = 0; r < 16; ++r) acc[d][r] = 0.f;
+        m = -kInf;
+        l = 0.f;
     }
-    const float by = l == 0.f ? 0.f : 1.f / l;
-    char* o = static_cast<char*>(a.o) + ((f.row + my_row) * static_cast<long long>(a.H) + q_head) * kD * ES;
+
+    // S^T of 32 keys; k: the lane's place in their K, rows PITCH bytes apart.
+    __device__ __forceinline__ f32x16 scores(const char* k) const {
+        f32x16 s;
 #pragma unroll
-    for (int d = 0; d < 4; ++d)
+        for (int r = 0; r < 16; ++r) s[r] = 0.f;
 #pragma unroll
-        for (int r = 0; r < 16; r += 4) {
-            const float z[4] = {acc[d][r] * by, acc[d][r + 1] * by, acc[d][r + 2] * by, acc[d][r + 3] * by};
-            char* at = o + (32 * d + 2 * r + 4 * half) * ES;
-            if constexpr (BF16)
-                *reinterpret_cast<uint2*>(at) = make_uint2(pack(z[0], z[1]), pack(z[2], z[3]));
-            else
-                *reinterpret_cast<float4*>(at) = make_float4(z[0], z[1], z[2], z[3]);
+        for (int x = 0; x < kQ; ++x) {
+            const uint4 u = *reinterpret_cast<const uint4*>(k + 32 * x);
+            if constexpr (BF16) {
+                s = mfma(u, q[x], s);
+            } else {
+                s = mfma(real(u.x), real(q[x].x), s);
+                s = mfma(real(u.y), real(q[x].y), s);
+                s = mfma(real(u.z), real(q[x].z), s);
+                s = mfma(real(u.w), real(q[x].w), s);
+            }
         }
+        return s;
+    }
+
+    // Scores of keys that the column does not see (bits of `seen`) to -inf.
+    __device__ __forceinline__ static void mask(f32x16& s, uint32_t seen) {
+        const int here = static_cast<int>(seen >> (threadIdx.x & 32 ? 4 : 0));
+#pragma unroll
+        for (int r = 0; r < 16; ++r) {
+            const uint32_t on = static_cast<uint32_t>(__builtin_amdgcn_sbfe(here, 8 * (r >> 2) + (r & 3), 1));   // all ones or 0
+            s[r] = real((bits(s[r]) & on) | (0xFF800000u & ~on));
+        }
+    }
+
+    // Scores to weights 2^{c s - m}; O, l and m follow a new maximum.  Each column by itself: no other
+    // column's values move its maximum.
+    template <int NB>
+    __device__ __forceinline__ void weights(f32x16 (&s)[NB], float c) {
+        float top = s[0][0];
+#pragma unroll
+        for (int b = 0; b < NB; ++b)
+#pragma unroll
+            for (int r = 0; r < 16; ++r) top = fmaxf(top, s[b][r]);
+        float x, y;
+        halves(top, x, y);
+        top = fmaxf(x, y) * c;
+        const bool up = top > m + kSlack || (m == -kInf && top > m);
+        if (__ballot(up)) {
+            const float to = up ? top : m;
+            const float by = m == -kInf ? 0.f : __builtin_amdgcn_exp2f(m - to);
+            m = to;
+            l *= by;
+#pragma unroll
+            for (int d = 0; d < 4; ++d)
+#pragma unroll
+                for (int r = 0; r < 16; ++r) acc[d][r] *= by;
+        }
+        const float base = m == -kInf ? 0.f : m;
+#pragma unroll
+        for (int b = 0; b < NB; ++b)
+#pragma unroll
+            for (int r = 0; r < 16; ++r) {
+                s[b][r] = __builtin_amdgcn_exp2f(fmaf(s[b][r], c, -base));
+                l += s[b][r];
+            }
+    }
+
+    // A NaN in the channels of `odd` (a byte a piece).
+    __device__ __forceinline__ void spoil(const uint8_t* odd) {
+        const int half = (threadIdx.x & 63) >> 5;
+#pragma unroll
+        for (int d = 0; d < 4; ++d)
+#pragma unroll
+            for (int r = 0; r < 16; ++r) {
+                const uint32_t x = BF16 ? odd[4 * d + (r >> 2)] >> (4 * half + (r & 3)) : odd[8 * d + 2 * (r >> 2) + half] >> (r & 3);
+                acc[d][r] = x & 1 ? __builtin_nanf("") : acc[d][r];
+            }
+    }
+
+    // The result, or a split's part of it.
+    template <bool SPLIT>
+    __device__ __forceinline__ void finish(const AttnArgs& a, const Plan& p, const Work& w, int c0) {
+        constexpr int ES = BF16 ? 2 : 4;
+        const int lane = threadIdx.x & 63, half = lane >> 5, n_heads = a.Hk * p.groups, place = blockIdx.x / n_heads;
+        float x, y;
+        halves(l, x, y);
+        l = x + y;
+        if (SPLIT && w.f.split == 0 && w.hd == 0 && threadIdx.x == 0)
+            Partials(a.work, p, n_heads).tiles[w.f.first / p.rows + w.f.b + w.f.index] = make_int2(place, w.f.splits);
+        if (!mine) return;
+        if (SPLIT && w.f.splits > 1) {
+            const Partials parts(a.work, p, n_heads);
+            const long long at = (static_cast<long long>(place) * n_heads + w.hd) * p.cols + c0 + (lane & 31);
+            if (half == 0) parts.ml[at] = make_float2(m, l);
+            float* o = parts.o + at * kD;
+#pragma unroll
+            for (int d = 0; d < 4; ++d)
+#pragma unroll
+                for (int r = 0; r < 16; r += 4)
+                    *reinterpret_cast<float4*>(o + 32 * d + 2 * r + 4 * half) =
+                        make_float4(acc[d][r], acc[d][r + 1], acc[d][r + 2], acc[d][r + 3]);
+            return;
+        }
+        const float by = l == 0.f ? 0.f : 1.f / l;
+        char* o = static_cast<char*>(a.o) + ((w.f.row + row) * static_cast<long long>(a.H) + w.head + head) * kD * ES;
+#pragma unroll
+        for (int d = 0; d < 4; ++d)
+#pragma unroll
+            for (int r = 0; r < 16; r += 4) {
+                const float z[4] = {acc[d][r] * by, acc[d][r + 1] * by, acc[d][r + 2] * by, acc[d][r + 3] * by};
+                char* at = o + (32 * d + 2 * r + 4 * half) * ES;
+                if constexpr (BF16)
+                    *reinterpret_cast<uint2*>(at) = make_uint2(pack(z[0], z[1]), pack(z[2], z[3]));
+                else
+                    *reinterpret_cast<float4*>(at) = make_float4(z[0], z[1], z[2], z[3]);
+            }
+    }
+};
+
+// Rows of a tile that a thread brings to LDS: 16 bytes of row row0 + j * kRowsAtOnce in load j.
+template <typename Sh, bool BF16>
+struct Loader {
+    int piece, row0;
+    const char* base;   // K's or V's, of the key head and piece
+
+    __device__ __forceinline__ Loader(const void* p, const CacheView& c, int kh)
+        : piece(threadIdx.x % Sh::kPieces), row0(threadIdx.x / Sh::kPieces),
+          base(static_cast<const char*>(p) + kh * c.head_stride * Sh::kEs + piece * 16) {}
+
+    // off: byte offset of the lane's key's row; -1: none, read as the cache's first row (no row sees it).
+    __device__ __forceinline__ void load(uint4 (&u)[Sh::kLoads], long long off) const {
+        const long long from = off >= 0 ? off : 0;
+#pragma unroll
+        for (int j = 0; j < Sh::kLoads; ++j)
+            u[j] = *reinterpret_cast<const uint4*>(base + __shfl(from, row0 + j * Sh::kRowsAtOnce));
+    }
+
+    template <int PITCH>
+    __device__ __forceinline__ void store(const uint4 (&u)[Sh::kLoads], char* to) const {
+#pragma unroll
+        for (int j = 0; j < Sh::kLoads; ++j)
+            *reinterpret_cast<uint4*>(to + row0 * PITCH + piece * 16 + j * Sh::kRowsAtOnce * PITCH) = u[j];
+    }
+
+    // Of V, where some row does not see all keys: 0 x NaN would carry a NaN or an infinity into rows that
+    // do not see it, so it is made 0, odd says which channels of which key it was, and the rows that see
+    // it get a NaN afterwards.  Whether the wave brought any.
+    __device__ __forceinline__ bool part(uint4 (&u)[Sh::kLoads], uint8_t* odd) const {
+        uint32_t bad[Sh::kLoads], any = 0;
+#pragma unroll
+        for (int j = 0; j < Sh::kLoads; ++j) any |= bad[j] = part_finite<BF16>(u[j]);
+        if (__ballot(any != 0) == 0) return false;
+#pragma unroll
+        for (int j = 0; j < Sh::kLoads; ++j) odd[(row0 + j * Sh::kRowsAtOnce) * Sh::kPieces + piece] = static_cast<uint8_t>(bad[j]);
+        return true;
+    }
+};
+
+// Byte offset of the row of the lane's key; -1: none.
+template <int KT, int ES>
+__device__ __forceinline__ long long offset_of(const AttnArgs& a, const Work& w, int t, int entry) {
+    const long long at = cache_at(a.c, entry, key_of<KT>(w, t) + static_cast<int>(threadIdx.x & 63) % KT);
+    return at < 0 ? -1 : at * ES;
+}
+
+template <int KT>
+constexpr uint64_t kAll = KT == 64 ? ~0ull : (1ull << KT) - 1;
+
+// 128 columns: four waves share the tiles of keys, two of which lie in LDS.
+template <bool BF16, bool SPLIT>
+__global__ void __launch_bounds__(256, 2) attn_wide_kernel(AttnArgs a, Plan p) {
+    using Sh = Shape<BF16, 4>;
+    constexpr int KT = Sh::kKeys, NB = Sh::kBlocks, PK = Sh::kPitchK, PV = Sh::kPitchV, ROWS = 64 / Sh::kPieces;
+    __shared__ __align__(16) char tiles[2][Sh::kTile];
+    __shared__ uint32_t spoiled[2][4];   // whether the wave's rows of V are in odd
+    __shared__ uint8_t odd[2][KT * Sh::kPieces];
+    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, c0 = wave * kColumns;
+    const Work w = work_of<KT, SPLIT>(a, p);
+    if (w.f.b < 0) return;
+    // the wave's positions
+    const int row_lo = c0 / p.heads, wave_lo = w.lo + row_lo, wave_hi = w.lo + min((c0 + kColumns - 1) / p.heads, w.rows - 1);
+    Columns<BF16> x;
+    x.begin(a, p, w, c0);
+    const float c = a.scale * kLog2e;
+    const Loader<Sh, BF16> from_k(a.c.k, a.c, w.kh), from_v(a.c.v, a.c, w.kh);
+    const int key_place = (lane & 31) * PK + (lane >> 5) * 16, value_at = KT * PK + value_place<BF16, PV>();
+    uint4 nk[Sh::kLoads], nv[Sh::kLoads];
+    uint64_t there = 0, next_there = 0;   // the tile's rows that exist
+    const auto fetch = [&](int t, int entry) {
+        const long long off = offset_of<KT, Sh::kEs>(a, w, t, entry);
+        next_there = __ballot(off >= 0) & kAll<KT>;
+        from_k.load(nk, off);
+        from_v.load(nv, off);
+    };
+    const auto uneven = [&](int t) { return there != kAll<KT> || partly<KT>(a, key_of<KT>(w, t), w.lo, w.hi); };
+    const auto keep = [&](int t, int buf) {
+        there = next_there;
+        if (uneven(t)) {
+            const bool any = from_v.part(nv, odd[buf]);
+            if (lane == 0) spoiled[buf][wave] = any;
+        }
+        from_k.template store<PK>(nk, tiles[buf]);
+        from_v.template store<PV>(nv, tiles[buf] + KT * PK);
+    };
+    int entry = entry_of<KT>(a, w, w.t0);
+    if (w.t0 < w.t1) {
+        fetch(w.t0, entry);
+        entry = entry_of<KT>(a, w, w.t0 + 1);
+        keep(w.t0, 0);
+    }
+    __syncthreads();
+    for (int t = w.t0; t < w.t1; ++t) {
+        const int buf = (t - w.t0) & 1, key0 = key_of<KT>(w, t);
+        const uint64_t now = there;
+        const bool any_masked = uneven(t);
+        if (t + 1 < w.t1) {
+            fetch(t + 1, entry);
+            entry = entry_of<KT>(a, w, t + 2);
+        }
+        if (row_lo < w.rows && key0 <= wave_hi) {
+            f32x16 s[NB];
+#pragma unroll
+            for (int b = 0; b < NB; ++b) s[b] = x.scores(tiles[buf] + key_place + 32 * b * PK);
+            if (now != kAll<KT> || partly<KT>(a, key0, wave_lo, wave_hi))
+#pragma unroll
+                for (int b = 0; b < NB; ++b) x.mask(s[b], seen_by(a, static_cast<uint32_t>(now >> 32 * b), x.pos, key0 + 32 * b));
+            x.weights(s, c);
+            add_values<BF16, NB, PV>(x.acc, s, tiles[buf] + value_at);
+            if (any_masked && (spoiled[buf][0] | spoiled[buf][1] | spoiled[buf][2] | spoiled[buf][3])) {
+#pragma unroll 1
+                for (int i = 0; i < KT; ++i)
+                    if (spoiled[buf][i / ROWS % 4] && seen_by(a, static_cast<uint32_t>(now >> (i & 32)), x.pos, key0 + (i & 32)) >> (i & 31) & 1)
+                        x.spoil(odd[buf] + i * Sh::kPieces);
+            }
+        }
+        if (t + 1 < w.t1) keep(t + 1, buf ^ 1);
+        __syncthreads();
+    }
+    x.template finish<SPLIT>(a, p, w, c0);
+}
+
+// 32 columns: a wave by itself, many a CU.  K and V of a tile take turns in one region of LDS and in the
+// registers that hold what is on its way: V comes while the scores are computed, the next K behind them.
+template <bool BF16, bool SPLIT>
+__global__ void __launch_bounds__(64, 2) attn_narrow_kernel(AttnArgs a, Plan p) {
+    using Sh = Shape<BF16, 1>;
+    constexpr int KT = Sh::kKeys, PK = Sh::kPitchK, PV = Sh::kPitchV;
+    __shared__ __align__(16) char tile[KT * (PK > PV ? PK : PV)];
+    __shared__ uint8_t odd[KT * Sh::kPieces];
+    const int lane = threadIdx.x & 63;
+    const Work w = work_of<KT, SPLIT>(a, p);
+    if (w.f.b < 0) return;
+    const Loader<Sh, BF16> from_k(a.c.k, a.c, w.kh), from_v(a.c.v, a.c, w.kh);
+    long long off = offset_of<KT, Sh::kEs>(a, w, w.t0, entry_of<KT>(a, w, w.t0));
+    int entry = entry_of<KT>(a, w, w.t0 + 1);
+    uint4 u[Sh::kLoads];
+    if (w.t0 < w.t1) from_k.load(u, off);
+    Columns<BF16> x;
+    x.begin(a, p, w, 0);
+    const float c = a.scale * kLog2e;
+    const int key_place = (lane & 31) * PK + (lane >> 5) * 16, value_at = value_place<BF16, PV>();
+    // (one wave: its LDS accesses are done in order)
+    const auto order = [] {
+        __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+        __builtin_amdgcn_wave_barrier();
+    };
+    if (w.t0 < w.t1) {
+        from_k.template store<PK>(u, tile);
+        from_v.load(u, off);
+    }
+    for (int t = w.t0; t < w.t1; ++t) {
+        const int key0 = key_of<KT>(w, t);
+        const uint64_t there = __ballot(off >= 0) & kAll<KT>;
+        const bool masked = there != kAll<KT> || partly<KT>(a, key0, w.lo, w.hi);
+        order();
+        f32x16 s[1] = {x.scores(tile + key_place)};
+        order();
+        bool odds = false;
+        uint32_t seen = 0;
+        if (masked) {
+            seen = seen_by(a, static_cast<uint32_t>(there), x.pos, key0);
+            x.mask(s[0], seen);
+            odds = from_v.part(u, odd);
+        }
+        from_v.template store<PV>(u, tile);
+        if (t + 1 < w.t1) {
+            off = offset_of<KT, Sh::kEs>(a, w, t + 1, entry);
+            from_k.load(u, off);
+            entry = entry_of<KT>(a, w, t + 2);
+        }
+        x.weights(s, c);
+        order();
+        add_values<BF16, 1, PV>(x.acc, s, tile + value_at);
+        if (odds) {
+#pragma unroll 1
+            for (int i = 0; i < KT; ++i)
+                if (seen >> i & 1) x.spoil(odd + i * Sh::kPieces);
+        }
+        order();
+        if (t + 1 < w.t1) {
+            from_k.template store<PK>(u, tile);
+            from_v.load(u, off);
+        }
+    }
+    x.template finish<SPLIT>(a, p, w, 0);
 }
 
 // Joins the splits of a column (row and head): a workgroup each, whose waves take every fourth
@@ -627,16 +787,23 @@ __global__ void __launch_bounds__(kJoinThreads) attn_join_kernel(AttnArgs a, Pla
 // Four waves a tile where a sequence fills more than one wave's columns on average.
 bool is_wide(int R, int B, int H, int Hk) { return static_cast<long long>(R) * (H / Hk) > static_cast<long long>(B) * kColumns; }
 
-template <bool BF16, int WAVES>
+template <bool BF16, bool WIDE>
 hipError_t launch(const AttnArgs& a, hipStream_t stream) {
-    Plan p = plan_of(a.R, a.B, a.H, a.Hk, WAVES == 4);
+    Plan p = plan_of(a.R, a.B, a.H, a.Hk, WIDE);
     const int n_heads = a.Hk * p.groups;
     if (static_cast<long long>(a.c.seq_pages) << a.c.page_shift <= kSplitKeys) p.parts = 0;
+    const dim3 grid(static_cast<unsigned>(p.parts + p.slots) * n_heads), block(WIDE ? 256 : 64);
     if (p.parts == 0) {
-        attn_kernel<BF16, WAVES, false><<<dim3(static_cast<unsigned>(p.slots) * n_heads), dim3(WAVES * 64), 0, stream>>>(a, p);
+        if constexpr (WIDE)
+            attn_wide_kernel<BF16, false><<<grid, block, 0, stream>>>(a, p);
+        else
+            attn_narrow_kernel<BF16, false><<<grid, block, 0, stream>>>(a, p);
         return hipGetLastError();
     }
-    attn_kernel<BF16, WAVES, true><<<dim3(static_cast<unsigned>(p.parts + p.slots) * n_heads), dim3(WAVES * 64), 0, stream>>>(a, p);
+    if constexpr (WIDE)
+        attn_wide_kernel<BF16, true><<<grid, block, 0, stream>>>(a, p);
+    else
+        attn_narrow_kernel<BF16, true><<<grid, block, 0, stream>>>(a, p);
     const hipError_t e = hipGetLastError();
     if (e != hipSuccess) return e;
     const int columns = (a.R < p.rows ? a.R : p.rows) * p.heads;
@@ -677,8 +844,8 @@ long long attn_work_bytes(int R, int B, int H, int Hk) {
 }
 
 hipError_t launch_attn(const AttnArgs& a, bool bf16, hipStream_t stream) {
-    if (is_wide(a.R, a.B, a.H, a.Hk)) return bf16 ? launch<true, 4>(a, stream) : launch<false, 4>(a, stream);
-    return bf16 ? launch<true, 1>(a, stream) : launch<false, 1>(a, stream);
+    if (is_wide(a.R, a.B, a.H, a.Hk)) return bf16 ? launch<true, true>(a, stream) : launch<false, true>(a, stream);
+    return bf16 ? launch<true, false>(a, stream) : launch<false, false>(a, stream);
 }
 
 }  // namespace kda
