@@ -33,6 +33,7 @@ namespace {
 
 using bf16x8 = __attribute__((ext_vector_type(8))) __bf16;
 using s16x4 = __attribute__((ext_vector_type(4))) short;
+using u32x4 = __attribute__((ext_vector_type(4))) uint32_t;
 using f32x16 = __attribute__((ext_vector_type(16))) float;
 
 constexpr float kInf = __builtin_inff();
@@ -254,21 +255,21 @@ struct Partials {
 
 // Makes what is not finite 0, and says in a bit a channel where that was.
 template <bool BF16>
-__device__ __forceinline__ uint32_t part_finite(uint4& u) {
-    uint32_t w[4] = {u.x, u.y, u.z, u.w}, bad = 0;
+__device__ __forceinline__ uint32_t part_finite(u32x4& u) {
+    uint32_t bad = 0;
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
+        const uint32_t x = u[i];
         if constexpr (BF16) {
-            const bool lo = (w[i] & 0x7F80u) == 0x7F80u, hi = (w[i] & 0x7F800000u) == 0x7F800000u;
+            const bool lo = (x & 0x7F80u) == 0x7F80u, hi = (x & 0x7F800000u) == 0x7F800000u;
             bad |= (lo ? 1u : 0u) << 2 * i | (hi ? 2u : 0u) << 2 * i;
-            w[i] &= (lo ? 0u : 0xFFFFu) | (hi ? 0u : 0xFFFF0000u);
+            u[i] = x & ((lo ? 0u : 0xFFFFu) | (hi ? 0u : 0xFFFF0000u));
         } else {
-            const bool all = (w[i] & 0x7F800000u) == 0x7F800000u;
+            const bool all = (x & 0x7F800000u) == 0x7F800000u;
             bad |= (all ? 1u : 0u) << i;
-            w[i] = all ? 0u : w[i];
+            u[i] = all ? 0u : x;
         }
     }
-    u = make_uint4(w[0], w[1], w[2], w[3]);
     return bad;
 }
 
@@ -451,7 +452,7 @@ struct Columns {
         float x, y;
         halves(top, x, y);
         top = fmaxf(x, y) * c;
-        const bool up = top > m + kSlack || (m == -kInf && top > m);
+        const bool up = (top > m + kSlack) | ((m == -kInf) & (top > m));
         if (__ballot(up)) {
             const float to = up ? top : m;
             const float by = m == -kInf ? 0.f : __builtin_amdgcn_exp2f(m - to);
@@ -463,13 +464,15 @@ struct Columns {
                 for (int r = 0; r < 16; ++r) acc[d][r] *= by;
         }
         const float base = m == -kInf ? 0.f : m;
+        float sum[4] = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
         for (int b = 0; b < NB; ++b)
 #pragma unroll
             for (int r = 0; r < 16; ++r) {
                 s[b][r] = __builtin_amdgcn_exp2f(fmaf(s[b][r], c, -base));
-                l += s[b][r];
+                sum[r & 3] += s[b][r];
             }
+        l += (sum[0] + sum[1]) + (sum[2] + sum[3]);
     }
 
     // A NaN in the channels of `odd` (a byte a piece).
@@ -527,6 +530,9 @@ struct Columns {
 // Rows of a tile that a thread brings to LDS: 16 bytes of row row0 + j * kRowsAtOnce in load j.
 template <typename Sh, bool BF16>
 struct Loader {
+    struct Rows {
+        u32x4 r[Sh::kLoads];
+    };
     int piece, row0;
     const char* base;   // K's or V's, of the key head and piece
 
@@ -535,27 +541,29 @@ struct Loader {
           base(static_cast<const char*>(p) + kh * c.head_stride * Sh::kEs + piece * 16) {}
 
     // off: byte offset of the lane's key's row; -1: none, read as the cache's first row (no row sees it).
-    __device__ __forceinline__ void load(uint4 (&u)[Sh::kLoads], long long off) const {
+    __device__ __forceinline__ Rows load(long long off) const {
         const long long from = off >= 0 ? off : 0;
+        Rows u;
 #pragma unroll
         for (int j = 0; j < Sh::kLoads; ++j)
-            u[j] = *reinterpret_cast<const uint4*>(base + __shfl(from, row0 + j * Sh::kRowsAtOnce));
+            u.r[j] = *reinterpret_cast<const u32x4*>(base + __shfl(from, row0 + j * Sh::kRowsAtOnce));
+        return u;
     }
 
     template <int PITCH>
-    __device__ __forceinline__ void store(const uint4 (&u)[Sh::kLoads], char* to) const {
+    __device__ __forceinline__ void store(Rows u, char* to) const {
 #pragma unroll
         for (int j = 0; j < Sh::kLoads; ++j)
-            *reinterpret_cast<uint4*>(to + row0 * PITCH + piece * 16 + j * Sh::kRowsAtOnce * PITCH) = u[j];
+            *reinterpret_cast<u32x4*>(to + row0 * PITCH + piece * 16 + j * Sh::kRowsAtOnce * PITCH) = u.r[j];
     }
 
     // Of V, where some row does not see all keys: 0 x NaN would carry a NaN or an infinity into rows that
     // do not see it, so it is made 0, odd says which channels of which key it was, and the rows that see
     // it get a NaN afterwards.  Whether the wave brought any.
-    __device__ __forceinline__ bool part(uint4 (&u)[Sh::kLoads], uint8_t* odd) const {
+    __device__ __forceinline__ bool part(Rows& u, uint8_t* odd) const {
         uint32_t bad[Sh::kLoads], any = 0;
 #pragma unroll
-        for (int j = 0; j < Sh::kLoads; ++j) any |= bad[j] = part_finite<BF16>(u[j]);
+        for (int j = 0; j < Sh::kLoads; ++j) any |= bad[j] = part_finite<BF16>(u.r[j]);
         if (__ballot(any != 0) == 0) return false;
 #pragma unroll
         for (int j = 0; j < Sh::kLoads; ++j) odd[(row0 + j * Sh::kRowsAtOnce) * Sh::kPieces + piece] = static_cast<uint8_t>(bad[j]);
@@ -572,6 +580,9 @@ __device__ __forceinline__ long long offset_of(const AttnArgs& a, const Work& w,
 
 template <int KT>
 constexpr uint64_t kAll = KT == 64 ? ~0ull : (1ull << KT) - 1;
+
+// Waits for all loads: what a loop only reads would else be waited for in every turn, with what the turn loads.
+__device__ __forceinline__ void arrived() { __builtin_amdgcn_s_waitcnt(0x0F70); }
 
 // 128 columns: four waves share the tiles of keys, two of which lie in LDS.
 template <bool BF16, bool SPLIT>
@@ -591,13 +602,13 @@ __global__ void __launch_bounds__(256, 2) attn_wide_kernel(AttnArgs a, Plan p) {
     const float c = a.scale * kLog2e;
     const Loader<Sh, BF16> from_k(a.c.k, a.c, w.kh), from_v(a.c.v, a.c, w.kh);
     const int key_place = (lane & 31) * PK + (lane >> 5) * 16, value_at = KT * PK + value_place<BF16, PV>();
-    uint4 nk[Sh::kLoads], nv[Sh::kLoads];
+    typename Loader<Sh, BF16>::Rows nk, nv;
     uint64_t there = 0, next_there = 0;   // the tile's rows that exist
     const auto fetch = [&](int t, int entry) {
         const long long off = offset_of<KT, Sh::kEs>(a, w, t, entry);
         next_there = __ballot(off >= 0) & kAll<KT>;
-        from_k.load(nk, off);
-        from_v.load(nv, off);
+        nk = from_k.load(off);
+        nv = from_v.load(off);
     };
     const auto uneven = [&](int t) { return there != kAll<KT> || partly<KT>(a, key_of<KT>(w, t), w.lo, w.hi); };
     const auto keep = [&](int t, int buf) {
@@ -616,6 +627,7 @@ __global__ void __launch_bounds__(256, 2) attn_wide_kernel(AttnArgs a, Plan p) {
         keep(w.t0, 0);
     }
     __syncthreads();
+    arrived();
     for (int t = w.t0; t < w.t1; ++t) {
         const int buf = (t - w.t0) & 1, key0 = key_of<KT>(w, t);
         const uint64_t now = there;
@@ -660,8 +672,8 @@ __global__ void __launch_bounds__(64, 2) attn_narrow_kernel(AttnArgs a, Plan p) 
     const Loader<Sh, BF16> from_k(a.c.k, a.c, w.kh), from_v(a.c.v, a.c, w.kh);
     long long off = offset_of<KT, Sh::kEs>(a, w, w.t0, entry_of<KT>(a, w, w.t0));
     int entry = entry_of<KT>(a, w, w.t0 + 1);
-    uint4 u[Sh::kLoads];
-    if (w.t0 < w.t1) from_k.load(u, off);
+    typename Loader<Sh, BF16>::Rows u;
+    if (w.t0 < w.t1) u = from_k.load(off);
     Columns<BF16> x;
     x.begin(a, p, w, 0);
     const float c = a.scale * kLog2e;
@@ -673,8 +685,9 @@ __global__ void __launch_bounds__(64, 2) attn_narrow_kernel(AttnArgs a, Plan p) 
     };
     if (w.t0 < w.t1) {
         from_k.template store<PK>(u, tile);
-        from_v.load(u, off);
+        u = from_v.load(off);
     }
+    arrived();
     for (int t = w.t0; t < w.t1; ++t) {
         const int key0 = key_of<KT>(w, t);
         const uint64_t there = __ballot(off >= 0) & kAll<KT>;
@@ -692,7 +705,7 @@ __global__ void __launch_bounds__(64, 2) attn_narrow_kernel(AttnArgs a, Plan p) 
         from_v.template store<PV>(u, tile);
         if (t + 1 < w.t1) {
             off = offset_of<KT, Sh::kEs>(a, w, t + 1, entry);
-            from_k.load(u, off);
+            u = from_k.load(off);
             entry = entry_of<KT>(a, w, t + 2);
         }
         x.weights(s, c);
@@ -706,7 +719,7 @@ __global__ void __launch_bounds__(64, 2) attn_narrow_kernel(AttnArgs a, Plan p) 
         order();
         if (t + 1 < w.t1) {
             from_k.template store<PK>(u, tile);
-            from_v.load(u, off);
+            u = from_v.load(off);
         }
     }
     x.template finish<SPLIT>(a, p, w, 0);
