@@ -46,6 +46,7 @@ constexpr int kLeastTiles = 1;        // a split has this many tiles at least
 constexpr int kSplitKeys = 256;       // a cache of no more keys a sequence is never split
 constexpr int kAppendThreads = 256;
 constexpr int kJoinThreads = 256;
+constexpr int kJoinAlone = 2048;      // columns that take a workgroup each in the join
 
 // ------------------------------------------------------------------ append
 
@@ -725,76 +726,81 @@ __global__ void __launch_bounds__(64, 2) attn_narrow_kernel(AttnArgs a, Plan p) 
     x.template finish<SPLIT>(a, p, w, 0);
 }
 
-// Joins the splits of a column (row and head): a workgroup each, whose waves take every fourth
-// split; a lane has two channels.
-template <bool BF16>
-__global__ void __launch_bounds__(kJoinThreads) attn_join_kernel(AttnArgs a, Plan p) {
+// Joins the splits of columns (row and head).  TEAM waves take a column, each every TEAM-th split; a lane
+// has two channels.
+template <bool BF16, int TEAM>
+__global__ void __launch_bounds__(kJoinThreads) attn_join_kernel(AttnArgs a, Plan p, int columns, int per) {
     constexpr int WAVES = kJoinThreads / 64, AHEAD = 4;
     __shared__ float2 sums[WAVES][64];
     __shared__ float2 ml[WAVES];
-    const int n_heads = a.Hk * p.groups, hd = blockIdx.x % n_heads, slot = blockIdx.x / n_heads, c = blockIdx.y;
-    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+    const int n_heads = a.Hk * p.groups, hd = blockIdx.x % n_heads, slot = blockIdx.x / n_heads;
+    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, mate = wave % TEAM;
     const Part f = find_part(a, p.rows, slot);
     if (f.b < 0) return;
-    const int row = f.first + f.index * p.rows + c / p.heads, kh = hd / p.groups, G = a.H / a.Hk;
-    const int head = hd % p.groups * p.heads + c % p.heads;
-    if (row >= f.last || head >= G) return;
     const Partials w(a.work, p, n_heads);
     const int2 tile = w.tiles[slot];
     if (tile.y <= 1) return;
+    const int first = f.first + f.index * p.rows, kh = hd / p.groups, G = a.H / a.Hk, g0 = hd % p.groups * p.heads;
     const long long step = static_cast<long long>(n_heads) * p.cols;
-    const long long at = (static_cast<long long>(tile.x) * n_heads + hd) * p.cols + c;
-    const float2* o = reinterpret_cast<const float2*>(w.o) + at * (kD / 2) + lane;
-    float m = -kInf, l = 0.f;
-    float2 x = make_float2(0.f, 0.f);
-    for (int i0 = wave; i0 < tile.y; i0 += WAVES * AHEAD) {
-        float2 part[AHEAD], got[AHEAD];
+    const int begin = blockIdx.y * per, end = min(begin + per, columns);
+    for (int c = begin + wave / TEAM; c - wave / TEAM < end; c += WAVES / TEAM) {
+        const int row = first + c / p.heads, head = g0 + c % p.heads;
+        const bool there = c < end && row < f.last && head < G;
+        const long long at = (static_cast<long long>(tile.x) * n_heads + hd) * p.cols + c;
+        const float2* o = reinterpret_cast<const float2*>(w.o) + at * (kD / 2) + lane;
+        float m = -kInf, l = 0.f;
+        float2 x = make_float2(0.f, 0.f);
+        for (int i0 = mate; there && i0 < tile.y; i0 += TEAM * AHEAD) {
+            float2 part[AHEAD], got[AHEAD];
 #pragma unroll
-        for (int i = 0; i < AHEAD; ++i) {
-            const int n = i0 + i * WAVES;
-            part[i] = n < tile.y ? w.ml[at + n * step] : make_float2(-kInf, 0.f);
-            got[i] = n < tile.y ? o[n * step * (kD / 2)] : make_float2(0.f, 0.f);
+            for (int i = 0; i < AHEAD; ++i) {
+                const int n = i0 + i * TEAM;
+                part[i] = n < tile.y ? w.ml[at + n * step] : make_float2(-kInf, 0.f);
+                got[i] = n < tile.y ? o[n * step * (kD / 2)] : make_float2(0.f, 0.f);
+            }
+            float top = m;
+#pragma unroll
+            for (int i = 0; i < AHEAD; ++i) top = fmaxf(top, part[i].x);
+            const float base = top == -kInf ? 0.f : top;
+            const float by = __builtin_amdgcn_exp2f(m - base);
+            l *= by;
+            x.x *= by;
+            x.y *= by;
+            m = top;
+#pragma unroll
+            for (int i = 0; i < AHEAD; ++i) {
+                const float e = __builtin_amdgcn_exp2f(part[i].x - base);
+                l = fmaf(part[i].y, e, l);
+                x.x = fmaf(got[i].x, e, x.x);
+                x.y = fmaf(got[i].y, e, x.y);
+            }
         }
-        float top = m;
+        if constexpr (TEAM > 1) {   // (a column a workgroup: one turn)
+            sums[wave][lane] = x;
+            if (lane == 0) ml[wave] = make_float2(m, l);
+            __syncthreads();
+            m = ml[0].x;
 #pragma unroll
-        for (int i = 0; i < AHEAD; ++i) top = fmaxf(top, part[i].x);
-        const float base = top == -kInf ? 0.f : top;
-        const float by = __builtin_amdgcn_exp2f(m - base);
-        l *= by;
-        x.x *= by;
-        x.y *= by;
-        m = top;
+            for (int i = 1; i < TEAM; ++i) m = fmaxf(m, ml[i].x);
+            const float base = m == -kInf ? 0.f : m;
+            l = 0.f;
+            x = make_float2(0.f, 0.f);
 #pragma unroll
-        for (int i = 0; i < AHEAD; ++i) {
-            const float e = __builtin_amdgcn_exp2f(part[i].x - base);
-            l = fmaf(part[i].y, e, l);
-            x.x = fmaf(got[i].x, e, x.x);
-            x.y = fmaf(got[i].y, e, x.y);
+            for (int i = 0; i < TEAM; ++i) {
+                const float e = __builtin_amdgcn_exp2f(ml[i].x - base);
+                l = fmaf(ml[i].y, e, l);
+                x.x = fmaf(sums[i][lane].x, e, x.x);
+                x.y = fmaf(sums[i][lane].y, e, x.y);
+            }
         }
+        if (!there || mate != 0) continue;
+        const float by = l == 0.f ? 0.f : 1.f / l;
+        const long long to = (row * static_cast<long long>(a.H) + static_cast<long long>(kh) * G + head) * kD + 2 * lane;
+        if constexpr (BF16)
+            *reinterpret_cast<uint32_t*>(static_cast<uint16_t*>(a.o) + to) = pack(x.x * by, x.y * by);
+        else
+            *reinterpret_cast<float2*>(static_cast<float*>(a.o) + to) = make_float2(x.x * by, x.y * by);
     }
-    sums[wave][lane] = x;
-    if (lane == 0) ml[wave] = make_float2(m, l);
-    __syncthreads();
-    if (wave != 0) return;
-    m = ml[0].x;
-#pragma unroll
-    for (int i = 1; i < WAVES; ++i) m = fmaxf(m, ml[i].x);
-    const float base = m == -kInf ? 0.f : m;
-    l = 0.f;
-    x = make_float2(0.f, 0.f);
-#pragma unroll
-    for (int i = 0; i < WAVES; ++i) {
-        const float e = __builtin_amdgcn_exp2f(ml[i].x - base);
-        l = fmaf(ml[i].y, e, l);
-        x.x = fmaf(sums[i][lane].x, e, x.x);
-        x.y = fmaf(sums[i][lane].y, e, x.y);
-    }
-    const float by = l == 0.f ? 0.f : 1.f / l;
-    const long long to = (row * static_cast<long long>(a.H) + static_cast<long long>(kh) * G + head) * kD + 2 * lane;
-    if constexpr (BF16)
-        *reinterpret_cast<uint32_t*>(static_cast<uint16_t*>(a.o) + to) = pack(x.x * by, x.y * by);
-    else
-        *reinterpret_cast<float2*>(static_cast<float*>(a.o) + to) = make_float2(x.x * by, x.y * by);
 }
 
 // Four waves a tile where a sequence fills more than one wave's columns on average.
@@ -819,8 +825,17 @@ hipError_t launch(const AttnArgs& a, hipStream_t stream) {
         attn_narrow_kernel<BF16, true><<<grid, block, 0, stream>>>(a, p);
     const hipError_t e = hipGetLastError();
     if (e != hipSuccess) return e;
+    // Few columns have many splits: four waves each.  Many have few: a wave each, and enough of them a
+    // workgroup for some thousand workgroups (each begins with a search for its rows).
     const int columns = (a.R < p.rows ? a.R : p.rows) * p.heads;
-    attn_join_kernel<BF16><<<dim3(static_cast<unsigned>(p.slots) * n_heads, static_cast<unsigned>(columns)), dim3(kJoinThreads), 0, stream>>>(a, p);
+    const long long n = static_cast<long long>(p.slots) * n_heads * columns;
+    const unsigned tiles = static_cast<unsigned>(p.slots) * n_heads;
+    if (n <= kJoinAlone) {
+        attn_join_kernel<BF16, kJoinThreads / 64><<<dim3(tiles, static_cast<unsigned>(columns)), dim3(kJoinThreads), 0, stream>>>(a, p, columns, 1);
+    } else {
+        const int per = 4 * static_cast<int>((n + 4 * kJoinAlone - 1) / (4 * kJoinAlone));
+        attn_join_kernel<BF16, 1><<<dim3(tiles, static_cast<unsigned>(div_up(columns, per))), dim3(kJoinThreads), 0, stream>>>(a, p, columns, per);
+    }
     return hipGetLastError();
 }
 

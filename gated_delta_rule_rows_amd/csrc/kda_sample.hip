@@ -7,15 +7,18 @@
 // lowest v whose running sum passes u_last times the whole sum.
 //
 // Three launches.  The first reads the logits once: of every part of a row the
-// maximum m and z = sum e^{(x - m) / T}, the exponentials in f32, their sums in
-// f64.  The second joins a session's rows, finds j and sums the weights of row j
-// by parts; the third finds the part that holds the place, and the token in it.
-// The weights are computed in f64: p - q cancels, and a running sum decides
-// which of two tokens a random number near their border gives.
+// maximum m and z = sum e^{(x - m) / T}.  In the second each workgroup joins its
+// session's rows, finds j and sums the weights of a piece of row j; the third
+// finds the piece that holds the place, and the token in it.  (As the work of the
+// second's last workgroup the third's cost more than a launch: release and acquire
+// over the chip's eight L2 caches, 28 us for 15 rows of 50,001 against 18.)
+// The exponentials are f32; their sums, p - q (which cancels) and the running
+// sums (which decide between two tokens near their border) are f64.
 
 #include <hip/hip_runtime.h>
 
 #include <cstdint>
+#include <type_traits>
 
 #include "kda.h"
 #include "kda_cache.h"
@@ -30,6 +33,9 @@ constexpr double kLog2e = 1.44269504088896340736;
 constexpr float kSlack = 4.0f;       // the carried maximum may lag by this much
 constexpr int kThreads = 256;
 constexpr int kMostParts = 64;       // of a row: a lane joins a part
+constexpr int kChunk = 4096;         // tokens of a piece, if that makes no more than 64 pieces
+constexpr int kAcceptThreads = 512;
+constexpr int kTokenThreads = 512;
 
 // m, and z relative to it; z is NaN where a value is NaN or +inf.
 struct Stat {
@@ -38,7 +44,7 @@ struct Stat {
     int pad;
 };
 
-// A session's row j, as the second launch leaves it for the third.
+// A session's row j.
 struct Found {
     double z;
     double scale;  // 1 / T; 0: no token
@@ -56,10 +62,11 @@ struct Mass {
 
 struct Split {
     Stat* stats;     // [R][parts]
-    Found* found;    // [B]
     Mass* mass;      // [B][pieces]
+    Found* found;    // [B]
     int parts;       // of a row in the first launch
-    int pieces;      // of row j in the second
+    int pieces;      // of row j, each with a sum
+    int groups;      // workgroups of a session in the second launch
 };
 
 template <bool BF16>
@@ -136,18 +143,35 @@ __global__ void __launch_bounds__(kThreads) sample_stats_kernel(SampledArgs a, S
     const int begin = min(part * each, loads), end = min(begin + each, loads);
     const uint4* body = reinterpret_cast<const uint4*>(static_cast<const char*>(row) + head * (BF16 ? 2 : 4));
     Stat s{0.0, -kInf, 0};
-    for (int i = begin + tid; i < end; i += kThreads) {
-        const uint4 u = body[i];
-        const uint32_t v[4] = {u.x, u.y, u.z, u.w};
-        float x[E];
+    constexpr int U = 4;   // loads ahead
+    const uint32_t low = BF16 ? 0xFF80FF80u : 0xFF800000u;   // -inf
+    const auto fetch = [&](int i0, uint4 (&u)[U]) {
 #pragma unroll
-        for (int e = 0; e < E; ++e) {
-            if constexpr (BF16)
-                x[e] = __builtin_bit_cast(float, e & 1 ? v[e >> 1] & 0xFFFF0000u : v[e >> 1] << 16);
-            else
-                x[e] = __builtin_bit_cast(float, v[e]);
+        for (int k = 0; k < U; ++k) {
+            const int i = i0 + k * kThreads + tid;
+            u[k] = i < end ? body[i] : make_uint4(low, low, low, low);
         }
-        take<E>(s, x, scale);
+    };
+    uint4 u[U], next[U];
+    fetch(begin, next);
+    for (int i0 = begin; i0 < end; i0 += U * kThreads) {
+#pragma unroll
+        for (int k = 0; k < U; ++k) u[k] = next[k];
+        if (i0 + U * kThreads < end) fetch(i0 + U * kThreads, next);
+#pragma unroll
+        for (int k = 0; k < U; ++k) {
+            if (i0 + k * kThreads + (tid & ~63) >= end) break;
+            const uint32_t v[4] = {u[k].x, u[k].y, u[k].z, u[k].w};
+            float x[E];
+#pragma unroll
+            for (int e = 0; e < E; ++e) {
+                if constexpr (BF16)
+                    x[e] = __builtin_bit_cast(float, e & 1 ? v[e >> 1] & 0xFFFF0000u : v[e >> 1] << 16);
+                else
+                    x[e] = __builtin_bit_cast(float, v[e]);
+            }
+            take<E>(s, x, scale);
+        }
     }
     if (wave == 0) {
         const bool first = part == 0 && lane < head, last = part == w.parts - 1 && lane < tail;
@@ -179,112 +203,76 @@ __device__ __forceinline__ Stat row_stat(const Split& w, long long r, double sca
     return Stat{wave_sum(moved(s, m, scale)), m, 0};
 }
 
-// Weight of token v in row j, times z, and e = p z.
-template <bool BF16>
-__device__ __forceinline__ double weight(const SampledArgs& a, const Found& f, const void* row, int v, uint32_t draft, double& e) {
-    e = exp((static_cast<double>(logit<BF16>(row, v)) - f.m) * f.scale);
-    if (!f.drafted) return e;
-    if (!a.probs) return static_cast<uint32_t>(v) == draft ? 0.0 : e;
-    return fmax(e - f.z * a.probs[f.row * a.probs_ld + v], 0.0);
-}
+// Weights of a row, times z.
+struct Weights {
+    const void* row;
+    const float* probs;
+    double z;
+    float m, by;             // e = 2^{(x - m) by}
+    uint32_t draft;
+};
 
-// The tokens of a thread: contiguous, so that running sums go by thread.
-__device__ __forceinline__ void range_of(const SampledArgs& a, const Split& w, int piece, int& from, int& to) {
-    const int each = (a.V + w.pieces - 1) / w.pieces, begin = min(piece * each, a.V), end = min(begin + each, a.V);
-    const int mine = (each + kThreads - 1) / kThreads;
-    from = min(begin + static_cast<int>(threadIdx.x) * mine, end);
-    to = min(from + mine, end);
-}
+// What they are: p, p without the draft, or max(p - q, 0).
+enum { kWhole, kOthers, kLeft };
+
+__device__ __forceinline__ int kind_of(const SampledArgs& a, const Found& f) { return !f.drafted ? kWhole : a.probs ? kLeft : kOthers; }
 
 template <bool BF16>
-__global__ void __launch_bounds__(kThreads) sample_accept_kernel(SampledArgs a, Split w) {
-    __shared__ int stop;
-    __shared__ Found shared;
-    __shared__ Mass waves[kThreads / 64];
-    const int piece = blockIdx.x % w.pieces, b = blockIdx.x / w.pieces;
-    const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
-    int first, last;
-    sequence(a, b, first, last);
-    const int n = last - first;
-    if (n == 0) {
-        if (piece == 0 && tid == 0) w.found[b].row = -1;
-        return;
-    }
-    const double scale = scale_of(a, b);
-    if (tid == 0) stop = scale == 0.0 ? 0 : n - 1;
-    __syncthreads();
-    for (int i = wave; i < n - 1; i += kThreads / 64) {
-        const long long r = first + i;
-        double p = __builtin_nan("");
-        if (scale != 0.0) {
-            const Stat s = row_stat(w, r, scale);
-            const uint32_t d = a.drafts[r];
-            p = s.m == -kInf ? __builtin_nan("") : 0.0;
-            if (d < static_cast<uint32_t>(a.V) && s.m != -kInf)
-                p = exp((static_cast<double>(logit<BF16>(row_at<BF16>(a, r), d)) - s.m) * scale) / s.z;
-            else if (s.z != s.z)
-                p = s.z;
-            if (lane == 0) {
-                const double q = !a.probs ? 1.0 : d < static_cast<uint32_t>(a.V) ? a.probs[r * a.probs_ld + d] : 1.0;
-                if (!(static_cast<double>(a.u[r]) * q < p)) atomicMin(&stop, i);
-            }
-        }
-        if (lane == 0 && piece == 0 && a.p_draft) a.p_draft[r] = static_cast<float>(p);
-    }
-    __syncthreads();
-    if (wave == 0) {
-        const int j = stop;
-        const long long r = first + j;
-        Stat s{0.0, -kInf, 0};
-        if (scale != 0.0) s = row_stat(w, r, scale);
-        if (lane == 0) {
-            const bool bad = s.m == -kInf || !(s.z < __builtin_inf());
-            shared = Found{s.z, bad ? 0.0 : scale, s.m, static_cast<int>(r), j, j < n - 1, last - 1};
-            if (piece == 0) w.found[b] = shared;
-        }
-    }
-    __syncthreads();
-    const Found f = shared;
-    if (f.scale == 0.0) return;
-    const void* row = row_at<BF16>(a, f.row);
-    const uint32_t draft = f.drafted && !a.probs ? a.drafts[f.row] : KDA_NO_TOKEN;
-    int from, to;
-    range_of(a, w, piece, from, to);
-    Mass sum{0.0, 0.0};
-    for (int v = from; v < to; ++v) {
-        double e;
-        sum.w += weight<BF16>(a, f, row, v, draft, e);
-        sum.p += e;
-    }
-    sum.w = wave_sum(sum.w);
-    sum.p = wave_sum(sum.p);
-    if (lane == 0) waves[wave] = sum;
-    __syncthreads();
-    if (tid == 0) {
-        sum = waves[0];
+__device__ __forceinline__ Weights weights_of(const SampledArgs& a, const Found& f) {
+    return Weights{row_at<BF16>(a, f.row), a.probs ? a.probs + f.row * a.probs_ld : nullptr, f.z, f.m,
+                   static_cast<float>(f.scale * kLog2e), a.probs ? KDA_NO_TOKEN : a.drafts[f.row]};
+}
+
+// Weights w and e = p z of tokens v0, v0 + step, ... below end (> v0 - step N); 0 behind it.
+template <bool BF16, int KIND, int N>
+__device__ __forceinline__ void weigh(const Weights& of, int v0, int step, int end, double (&w)[N], double (&e)[N]) {
+    float x[N], q[N];
 #pragma unroll
-        for (int i = 1; i < kThreads / 64; ++i) {
-            sum.w += waves[i].w;
-            sum.p += waves[i].p;
-        }
-        w.mass[b * w.pieces + piece] = sum;
+    for (int i = 0; i < N; ++i) {
+        const int v = min(v0 + i * step, end - 1);
+        x[i] = logit<BF16>(of.row, v);
+        if constexpr (KIND == kLeft) q[i] = of.probs[v];
+    }
+#pragma unroll
+    for (int i = 0; i < N; ++i) {
+        const int v = v0 + i * step;
+        e[i] = v < end ? __builtin_amdgcn_exp2f((x[i] - of.m) * of.by) : 0.f;
+        w[i] = e[i];
+        if constexpr (KIND == kOthers) w[i] = static_cast<uint32_t>(v) == of.draft ? 0.0 : e[i];
+        if constexpr (KIND == kLeft) w[i] = v < end ? fmax(fma(-of.z, static_cast<double>(q[i]), e[i]), 0.0) : 0.0;
     }
 }
 
+// f(KIND) for a kind known on the device, the same for all lanes.
+template <typename F>
+__device__ __forceinline__ void by_kind(int kind, F&& f) {
+    if (kind == kWhole)
+        f(std::integral_constant<int, kWhole>{});
+    else if (kind == kOthers)
+        f(std::integral_constant<int, kOthers>{});
+    else
+        f(std::integral_constant<int, kLeft>{});
+}
+
+__device__ __forceinline__ int piece_tokens(const SampledArgs& a, const Split& w) { return (a.V + w.pieces - 1) / w.pieces; }
+
+// The token of a session.
 template <bool BF16>
-__global__ void __launch_bounds__(kThreads) sample_token_kernel(SampledArgs a, Split w) {
-    __shared__ double waves[kThreads / 64];
-    __shared__ int token, behind;
-    const int b = blockIdx.x, tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
+__global__ void __launch_bounds__(kTokenThreads) sample_token_kernel(SampledArgs a, Split w) {
+    const int b = blockIdx.x;
     Found f = w.found[b];
     if (f.row < 0) return;
     if (f.scale == 0.0) {
-        if (tid == 0) {
+        if (threadIdx.x == 0) {
             a.out[2 * b] = f.j;
             a.out[2 * b + 1] = KDA_NO_TOKEN;
         }
         return;
     }
+    __shared__ double tokens[kChunk];
+    __shared__ double waves[kTokenThreads / 64];
+    __shared__ int token, behind;
+    const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
     // the piece: the first whose running sum passes the place (every wave finds it)
     Mass mass{0.0, 0.0};
     if (lane < w.pieces) mass = w.mass[b * w.pieces + lane];
@@ -303,45 +291,146 @@ __global__ void __launch_bounds__(kThreads) sample_token_kernel(SampledArgs a, S
         mask = mask ? 1ull << (63 - __builtin_clzll(mask)) : 1ull;
     }
     const int piece = __builtin_ctzll(mask);
-    const double before = __shfl(upto - mine, piece);
-    // the token in it
-    const void* row = row_at<BF16>(a, f.row);
-    const uint32_t draft = f.drafted && !a.probs ? a.drafts[f.row] : KDA_NO_TOKEN;
-    int from, to;
-    range_of(a, w, piece, from, to);
-    double sum = 0.0, e;
-    for (int v = from; v < to; ++v) sum += weight<BF16>(a, f, row, v, draft, e);
-    double run = sum;
-#pragma unroll
-    for (int d = 1; d < 64; d <<= 1) {
-        const double y = __shfl_up(run, d);
-        if (lane >= d) run += y;
-    }
-    if (lane == 63) waves[wave] = run;
+    double at = __shfl(upto - mine, piece);
+    // the token in it, chunk by chunk: weights to LDS, then running sums by thread
+    const Weights weights = weights_of<BF16>(a, f);
+    const int kind = kind_of(a, f);
+    const int each = piece_tokens(a, w), begin = min(piece * each, a.V), end = min(begin + each, a.V);
     if (tid == 0) {
         token = a.V;
         behind = -1;
     }
-    __syncthreads();
-    double at = before + run - sum;
-    for (int i = 0; i < wave; ++i) at += waves[i];
-    if (sum > 0.0) {
+    for (int v0 = begin; v0 < end; v0 += kChunk) {
+        __syncthreads();
+        by_kind(kind, [&](auto k) {
+            constexpr int N = 8;
+#pragma unroll
+            for (int i = 0; i < kChunk / kTokenThreads; i += N) {
+                double x[N], e[N];
+                weigh<BF16, k.value>(weights, v0 + i * kTokenThreads + tid, kTokenThreads, end, x, e);
+#pragma unroll
+                for (int n = 0; n < N; ++n) tokens[(i + n) * kTokenThreads + tid] = x[n];
+            }
+        });
+        __syncthreads();
+        constexpr int MINE = kChunk / kTokenThreads;
+        double x[MINE], sum = 0.0;
+#pragma unroll
+        for (int i = 0; i < MINE; ++i) sum += x[i] = tokens[tid * MINE + i];
+        double run = sum;
+#pragma unroll
+        for (int d = 1; d < 64; d <<= 1) {
+            const double y = __shfl_up(run, d);
+            if (lane >= d) run += y;
+        }
+        if (lane == 63) waves[wave] = run;
+        __syncthreads();
+        double here = at + run - sum;
+#pragma unroll
+        for (int i = 0; i < kTokenThreads / 64; ++i) {
+            if (i < wave) here += waves[i];
+            at += waves[i];
+        }
         int lowest = a.V, highest = -1;
-        for (int v = from; v < to; ++v) {
-            const double x = weight<BF16>(a, f, row, v, draft, e);
-            at += x;
-            if (x > 0.0) {
-                highest = v;
-                if (at > place && lowest == a.V) lowest = v;
+#pragma unroll
+        for (int i = 0; i < MINE; ++i) {
+            here += x[i];
+            if (x[i] > 0.0) {
+                highest = v0 + tid * MINE + i;
+                if (here > place) lowest = min(lowest, highest);
             }
         }
         if (lowest < a.V) atomicMin(&token, lowest);
         if (highest >= 0) atomicMax(&behind, highest);
+        __syncthreads();
+        if (token < a.V) break;
     }
-    __syncthreads();
     if (tid == 0) {
         a.out[2 * b] = f.j;
         a.out[2 * b + 1] = static_cast<uint32_t>(token < a.V ? token : behind);
+    }
+}
+
+template <bool BF16>
+__global__ void __launch_bounds__(kAcceptThreads) sample_accept_kernel(SampledArgs a, Split w) {
+    constexpr int WAVES = kAcceptThreads / 64;
+    __shared__ int stop;
+    __shared__ Found shared;
+    __shared__ Mass waves[2][WAVES];
+    const int group = blockIdx.x % w.groups, b = blockIdx.x / w.groups;
+    const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
+    int first, last;
+    sequence(a, b, first, last);
+    const int n = last - first;
+    if (n == 0) {
+        if (group == 0 && tid == 0) w.found[b].row = -1;
+        return;
+    }
+    const double scale = scale_of(a, b);
+    if (tid == 0) stop = scale == 0.0 ? 0 : n - 1;
+    __syncthreads();
+    for (int i = wave; i < n - 1; i += WAVES) {
+        const long long r = first + i;
+        double p = __builtin_nan("");
+        if (scale != 0.0) {
+            const uint32_t d = a.drafts[r];
+            const bool real = d < static_cast<uint32_t>(a.V);
+            const float x = real ? logit<BF16>(row_at<BF16>(a, r), d) : -kInf;
+            const double q = a.probs && real ? a.probs[r * a.probs_ld + d] : 1.0, u = a.u[r];
+            const Stat s = row_stat(w, r, scale);
+            if (s.m != -kInf) p = exp((static_cast<double>(x) - s.m) * scale) / s.z;
+            if (lane == 0 && !(u * q < p)) atomicMin(&stop, i);
+        }
+        if (lane == 0 && group == 0 && a.p_draft) a.p_draft[r] = static_cast<float>(p);
+    }
+    __syncthreads();
+    if (wave == 0) {
+        const int j = stop;
+        Stat s{0.0, -kInf, 0};
+        if (scale != 0.0) s = row_stat(w, first + j, scale);
+        const bool bad = s.m == -kInf || !(s.z < __builtin_inf());
+        if (lane == 0) {
+            shared = Found{s.z, bad ? 0.0 : scale, s.m, first + j, j, j < n - 1, last - 1};
+            if (group == 0) w.found[b] = shared;
+        }
+    }
+    __syncthreads();
+    const Found f = shared;
+    if (f.scale == 0.0) return;
+    const Weights weights = weights_of<BF16>(a, f);
+    const int kind = kind_of(a, f);
+    const int each = piece_tokens(a, w);
+    const int p0 = static_cast<int>(static_cast<long long>(w.pieces) * group / w.groups);
+    const int p1 = static_cast<int>(static_cast<long long>(w.pieces) * (group + 1) / w.groups);
+    for (int piece = p0; piece < p1; ++piece) {
+        const int begin = min(piece * each, a.V), end = min(begin + each, a.V);
+        Mass sum{0.0, 0.0};
+        by_kind(kind, [&](auto k) {
+            constexpr int N = 8;
+            for (int v = begin + tid; v < end; v += N * kAcceptThreads) {
+                double x[N], e[N];
+                weigh<BF16, k.value>(weights, v, kAcceptThreads, end, x, e);
+#pragma unroll
+                for (int n = 0; n < N; ++n) {
+                    sum.w += x[n];
+                    sum.p += e[n];
+                }
+            }
+        });
+        sum.w = wave_sum(sum.w);
+        sum.p = wave_sum(sum.p);
+        Mass* mine = waves[piece & 1];
+        if (lane == 0) mine[wave] = sum;
+        __syncthreads();   // (the next piece's sums go to the other half)
+        if (tid == 0) {
+            sum = mine[0];
+#pragma unroll
+            for (int i = 1; i < WAVES; ++i) {
+                sum.w += mine[i].w;
+                sum.p += mine[i].p;
+            }
+            w.mass[b * w.pieces + piece] = sum;
+        }
     }
 }
 
@@ -354,28 +443,33 @@ int parts_of(int R, int V, int es) {
     return static_cast<int>(p > kMostParts ? kMostParts : p);
 }
 
-int pieces_of(int B, int V) {
-    long long p = (static_cast<long long>(V) + 4 * kThreads - 1) / (4 * kThreads);
-    const long long fill = (1024 + B - 1) / B;
-    p = p < fill ? p : fill;
-    return static_cast<int>(p > kMostParts ? kMostParts : p);
+int pieces_of(int V) {
+    const int p = (V + kChunk - 1) / kChunk;
+    return p > kMostParts ? kMostParts : p;
+}
+
+// Two workgroups a CU: each repeats its session's walk.
+int groups_of(int B, int V) {
+    const int p = pieces_of(V), fill = (512 + B - 1) / B;
+    return p < fill ? p : fill;
 }
 
 template <bool BF16>
 hipError_t launch(const SampledArgs& a, hipStream_t stream) {
     Split w{};
     w.parts = parts_of(a.R, a.V, BF16 ? 2 : 4);
-    w.pieces = pieces_of(a.B, a.V);
+    w.pieces = pieces_of(a.V);
+    w.groups = groups_of(a.B, a.V);
     w.stats = static_cast<Stat*>(a.work);
     w.mass = reinterpret_cast<Mass*>(w.stats + static_cast<long long>(a.R) * w.parts);
     w.found = reinterpret_cast<Found*>(w.mass + static_cast<long long>(a.B) * w.pieces);
     sample_stats_kernel<BF16><<<dim3(static_cast<unsigned>(a.R + a.B) * w.parts), dim3(kThreads), 0, stream>>>(a, w);
     hipError_t e = hipGetLastError();
     if (e != hipSuccess) return e;
-    sample_accept_kernel<BF16><<<dim3(static_cast<unsigned>(a.B) * w.pieces), dim3(kThreads), 0, stream>>>(a, w);
+    sample_accept_kernel<BF16><<<dim3(static_cast<unsigned>(a.B) * w.groups), dim3(kAcceptThreads), 0, stream>>>(a, w);
     e = hipGetLastError();
     if (e != hipSuccess) return e;
-    sample_token_kernel<BF16><<<dim3(static_cast<unsigned>(a.B)), dim3(kThreads), 0, stream>>>(a, w);
+    sample_token_kernel<BF16><<<dim3(static_cast<unsigned>(a.B)), dim3(kTokenThreads), 0, stream>>>(a, w);
     return hipGetLastError();
 }
 
@@ -384,13 +478,13 @@ hipError_t launch(const SampledArgs& a, hipStream_t stream) {
 long long sampled_work_bytes(int R, int B, int V) {
     // f32 rows are the longer ones: never fewer parts than bf16 rows
     return static_cast<long long>(R) * parts_of(R, V, 4) * static_cast<long long>(sizeof(Stat)) +
-           static_cast<long long>(B) * (pieces_of(B, V) * static_cast<long long>(sizeof(Mass)) + static_cast<long long>(sizeof(Found)));
+           static_cast<long long>(B) * (pieces_of(V) * static_cast<long long>(sizeof(Mass)) + static_cast<long long>(sizeof(Found)));
 }
 
 long long sampled_workgroups(int R, int B, int V) {
     if (R < 1) return 0;
-    const long long rows = (static_cast<long long>(R) + B) * parts_of(R, V, 4), pieces = static_cast<long long>(B) * pieces_of(B, V);
-    return rows > pieces ? rows : pieces;
+    const long long rows = (static_cast<long long>(R) + B) * parts_of(R, V, 4), groups = 2ll * B * groups_of(B, V);   // (of twice the threads)
+    return rows > groups ? rows : groups;
 }
 
 hipError_t launch_sampled(const SampledArgs& a, bool bf16, hipStream_t stream) {
