@@ -48,11 +48,11 @@ struct Stat {
 struct Found {
     double z;
     double scale;  // 1 / T; 0: no token
+    double u;      // of the session's last row
     float m;
     int row;       // -1: the session has no rows
     int j;
     int drafted;   // weights max(p - q, 0) unless these are all 0; else p
-    int last;      // the session's last row
 };
 
 // Sums of a part's weights and probabilities (times z).
@@ -256,35 +256,40 @@ __device__ __forceinline__ void by_kind(int kind, F&& f) {
 
 __device__ __forceinline__ int piece_tokens(const SampledArgs& a, const Split& w) { return (a.V + w.pieces - 1) / w.pieces; }
 
+// Inclusive running sum over the lanes.
+__device__ __forceinline__ double running_sum(double x) {
+    const int lane = threadIdx.x & 63;
+#pragma unroll
+    for (int d = 1; d < 64; d <<= 1) {
+        const double y = __shfl_up(x, d);
+        if (lane >= d) x += y;
+    }
+    return x;
+}
+
 // The token of a session.
 template <bool BF16>
 __global__ void __launch_bounds__(kTokenThreads) sample_token_kernel(SampledArgs a, Split w) {
-    const int b = blockIdx.x;
+    constexpr int WAVES = kTokenThreads / 64, N = kChunk / kTokenThreads;
+    static_assert(WAVES * N == 64, "a lane for each 64 tokens of a chunk");
+    __shared__ double sums[64];
+    __shared__ int token, behind;
+    const int b = blockIdx.x, tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
     Found f = w.found[b];
+    Mass mass{0.0, 0.0};
+    if (lane < w.pieces) mass = w.mass[b * w.pieces + lane];
     if (f.row < 0) return;
     if (f.scale == 0.0) {
-        if (threadIdx.x == 0) {
+        if (tid == 0) {
             a.out[2 * b] = f.j;
             a.out[2 * b + 1] = KDA_NO_TOKEN;
         }
         return;
     }
-    __shared__ double tokens[kChunk];
-    __shared__ double waves[kTokenThreads / 64];
-    __shared__ int token, behind;
-    const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
     // the piece: the first whose running sum passes the place (every wave finds it)
-    Mass mass{0.0, 0.0};
-    if (lane < w.pieces) mass = w.mass[b * w.pieces + lane];
-    if (f.drafted && !(wave_sum(mass.w) > 0.0)) f.drafted = 0;
-    const double mine = f.drafted ? mass.w : mass.p;
-    double upto = mine;
-#pragma unroll
-    for (int d = 1; d < 64; d <<= 1) {
-        const double y = __shfl_up(upto, d);
-        if (lane >= d) upto += y;
-    }
-    const double place = static_cast<double>(a.u[f.last]) * __shfl(upto, 63);
+    if (f.drafted && __ballot(mass.w > 0.0) == 0) f.drafted = 0;
+    const double mine = f.drafted ? mass.w : mass.p, upto = running_sum(mine);
+    const double place = f.u * __shfl(upto, 63);
     uint64_t mask = __ballot(mine > 0.0 && upto > place);
     if (mask == 0) {   // a place at or behind the end: the last piece with weight
         mask = __ballot(mine > 0.0);
@@ -292,58 +297,42 @@ __global__ void __launch_bounds__(kTokenThreads) sample_token_kernel(SampledArgs
     }
     const int piece = __builtin_ctzll(mask);
     double at = __shfl(upto - mine, piece);
-    // the token in it, chunk by chunk: weights to LDS, then running sums by thread
+    // the token in it: sums of each 64 tokens, their running sums, and those of the tokens where the
+    // place lies
     const Weights weights = weights_of<BF16>(a, f);
-    const int kind = kind_of(a, f);
     const int each = piece_tokens(a, w), begin = min(piece * each, a.V), end = min(begin + each, a.V);
     if (tid == 0) {
         token = a.V;
         behind = -1;
     }
     for (int v0 = begin; v0 < end; v0 += kChunk) {
+        double x[N], e[N];
+        by_kind(kind_of(a, f), [&](auto k) { weigh<BF16, k.value>(weights, v0 + tid, kTokenThreads, end, x, e); });
+#pragma unroll
+        for (int i = 0; i < N; ++i) e[i] = wave_sum(x[i]);
+        __syncthreads();   // (behind the reads of the chunk before)
+#pragma unroll
+        for (int i = 0; i < N; ++i)
+            if (lane == 0) sums[i * WAVES + wave] = e[i];
         __syncthreads();
-        by_kind(kind, [&](auto k) {
-            constexpr int N = 8;
+        const double part = sums[lane], run = at + running_sum(part);
+        const uint64_t parts = __ballot(part > 0.0), passed = __ballot(part > 0.0 && run > place);
+        const int found = passed ? __builtin_ctzll(passed) : parts ? 63 - __builtin_clzll(parts) : -1;
+        if (found >= 0 && found % WAVES == wave) {
+            const double before = __shfl(run - part, found);
+            double mine64 = 0.0;
 #pragma unroll
-            for (int i = 0; i < kChunk / kTokenThreads; i += N) {
-                double x[N], e[N];
-                weigh<BF16, k.value>(weights, v0 + i * kTokenThreads + tid, kTokenThreads, end, x, e);
-#pragma unroll
-                for (int n = 0; n < N; ++n) tokens[(i + n) * kTokenThreads + tid] = x[n];
-            }
-        });
-        __syncthreads();
-        constexpr int MINE = kChunk / kTokenThreads;
-        double x[MINE], sum = 0.0;
-#pragma unroll
-        for (int i = 0; i < MINE; ++i) sum += x[i] = tokens[tid * MINE + i];
-        double run = sum;
-#pragma unroll
-        for (int d = 1; d < 64; d <<= 1) {
-            const double y = __shfl_up(run, d);
-            if (lane >= d) run += y;
+            for (int i = 0; i < N; ++i)
+                if (found / WAVES == i) mine64 = x[i];
+            const double here = before + running_sum(mine64);
+            const int v = v0 + found * 64 + lane;
+            const uint64_t some = __ballot(mine64 > 0.0), hit = __ballot(mine64 > 0.0 && here > place);
+            if (hit && lane == __builtin_ctzll(hit)) token = v;
+            if (some && lane == 63 - __builtin_clzll(some)) behind = v;
         }
-        if (lane == 63) waves[wave] = run;
-        __syncthreads();
-        double here = at + run - sum;
-#pragma unroll
-        for (int i = 0; i < kTokenThreads / 64; ++i) {
-            if (i < wave) here += waves[i];
-            at += waves[i];
-        }
-        int lowest = a.V, highest = -1;
-#pragma unroll
-        for (int i = 0; i < MINE; ++i) {
-            here += x[i];
-            if (x[i] > 0.0) {
-                highest = v0 + tid * MINE + i;
-                if (here > place) lowest = min(lowest, highest);
-            }
-        }
-        if (lowest < a.V) atomicMin(&token, lowest);
-        if (highest >= 0) atomicMax(&behind, highest);
         __syncthreads();
         if (token < a.V) break;
+        at = __shfl(run, 63);
     }
     if (tid == 0) {
         a.out[2 * b] = f.j;
@@ -366,7 +355,7 @@ __global__ void __launch_bounds__(kAcceptThreads) sample_accept_kernel(SampledAr
         if (group == 0 && tid == 0) w.found[b].row = -1;
         return;
     }
-    const double scale = scale_of(a, b);
+    const double scale = scale_of(a, b), u_last = a.u[last - 1];
     if (tid == 0) stop = scale == 0.0 ? 0 : n - 1;
     __syncthreads();
     for (int i = wave; i < n - 1; i += WAVES) {
@@ -390,7 +379,7 @@ __global__ void __launch_bounds__(kAcceptThreads) sample_accept_kernel(SampledAr
         if (scale != 0.0) s = row_stat(w, first + j, scale);
         const bool bad = s.m == -kInf || !(s.z < __builtin_inf());
         if (lane == 0) {
-            shared = Found{s.z, bad ? 0.0 : scale, s.m, first + j, j, j < n - 1, last - 1};
+            shared = Found{s.z, bad ? 0.0 : scale, u_last, s.m, first + j, j, j < n - 1};
             if (group == 0) w.found[b] = shared;
         }
     }
@@ -438,7 +427,7 @@ __global__ void __launch_bounds__(kAcceptThreads) sample_accept_kernel(SampledAr
 int parts_of(int R, int V, int es) {
     const long long loads = (static_cast<long long>(V) * es + 15) / 16;
     long long p = (loads + 4 * kThreads - 1) / (4 * kThreads);
-    const long long fill = (1024 + R - 1) / R;
+    const long long fill = (2048 + R - 1) / R;
     p = p < fill ? p : fill;
     return static_cast<int>(p > kMostParts ? kMostParts : p);
 }
