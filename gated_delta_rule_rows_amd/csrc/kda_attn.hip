@@ -46,7 +46,8 @@ constexpr int kLeastTiles = 1;        // a split has this many tiles at least
 constexpr int kSplitKeys = 256;       // a cache of no more keys a sequence is never split
 constexpr int kAppendThreads = 256;
 constexpr int kJoinThreads = 256;
-constexpr int kJoinAlone = 2048;      // columns that take a workgroup each in the join
+constexpr int kManySplits = 32;       // of a column: joined by four waves
+constexpr int kJoinGroups = 2048;     // workgroups of the join, about
 
 // ------------------------------------------------------------------ append
 
@@ -99,7 +100,9 @@ Plan plan_of(int R, int B, int H, int Hk, bool wide) {
     p.slots = R / p.rows + B;
     const long long n = static_cast<long long>(p.slots) * Hk * p.groups;
     const int target = wide ? kTargetWide : kTargetNarrow;
-    p.parts = n < target ? div_up(target, Hk * p.groups) : 0;
+    // parts + slots workgroups at most: as many as run side by side
+    const int side = target / (Hk * p.groups);
+    p.parts = n >= target ? 0 : side > p.slots ? side - p.slots : 1;
     return p;
 }
 
@@ -730,7 +733,7 @@ __global__ void __launch_bounds__(64, 2) attn_narrow_kernel(AttnArgs a, Plan p) 
 // has two channels.
 template <bool BF16, int TEAM>
 __global__ void __launch_bounds__(kJoinThreads) attn_join_kernel(AttnArgs a, Plan p, int columns, int per) {
-    constexpr int WAVES = kJoinThreads / 64, AHEAD = 4;
+    constexpr int WAVES = kJoinThreads / 64, AHEAD = TEAM > 1 ? 4 : 8;
     __shared__ float2 sums[WAVES][64];
     __shared__ float2 ml[WAVES];
     const int n_heads = a.Hk * p.groups, hd = blockIdx.x % n_heads, slot = blockIdx.x / n_heads;
@@ -825,15 +828,15 @@ hipError_t launch(const AttnArgs& a, hipStream_t stream) {
         attn_narrow_kernel<BF16, true><<<grid, block, 0, stream>>>(a, p);
     const hipError_t e = hipGetLastError();
     if (e != hipSuccess) return e;
-    // Few columns have many splits: four waves each.  Many have few: a wave each, and enough of them a
-    // workgroup for some thousand workgroups (each begins with a search for its rows).
+    // Columns of many splits take four waves each.  Of few, a wave each, and some of them a workgroup
+    // where there are many (it begins with a search for its rows).
     const int columns = (a.R < p.rows ? a.R : p.rows) * p.heads;
-    const long long n = static_cast<long long>(p.slots) * n_heads * columns;
     const unsigned tiles = static_cast<unsigned>(p.slots) * n_heads;
-    if (n <= kJoinAlone) {
+    if (p.parts > kManySplits * p.slots) {
         attn_join_kernel<BF16, kJoinThreads / 64><<<dim3(tiles, static_cast<unsigned>(columns)), dim3(kJoinThreads), 0, stream>>>(a, p, columns, 1);
     } else {
-        const int per = 4 * static_cast<int>((n + 4 * kJoinAlone - 1) / (4 * kJoinAlone));
+        const long long n = static_cast<long long>(tiles) * columns;
+        const int per = 4 * static_cast<int>((n + 4 * kJoinGroups - 1) / (4 * kJoinGroups));
         attn_join_kernel<BF16, 1><<<dim3(tiles, static_cast<unsigned>(div_up(columns, per))), dim3(kJoinThreads), 0, stream>>>(a, p, columns, per);
     }
     return hipGetLastError();
@@ -863,9 +866,9 @@ long long attn_work_bytes(int R, int B, int H, int Hk) {
     long long most = 0;
     for (const bool wide : {false, true}) {
         const Plan p = plan_of(R, B, H, Hk, wide);
-        const int n_heads = Hk * p.groups, target = wide ? kTargetWide : kTargetNarrow;
-        const long long parts = div_up(target, n_heads), slots = p.slots < parts ? p.slots : parts;
-        const long long n = (parts + slots) * n_heads * p.cols * (kD + 2) * 4 + slots * 8;
+        const int n_heads = Hk * p.groups, side = div_up(wide ? kTargetWide : kTargetNarrow, n_heads);
+        const long long slots = p.slots < side ? p.slots : side;
+        const long long n = (side + 1ll) * n_heads * p.cols * (kD + 2) * 4 + slots * 8;
         if (n > most) most = n;
     }
     return most;
