@@ -39,6 +39,7 @@ from __future__ import annotations
 
 import ctypes
 import os
+import struct
 
 import torch
 
@@ -58,13 +59,6 @@ class _PrevRound(ctypes.Structure):
     _fields_ = [("k", ctypes.c_void_p), ("v", ctypes.c_void_p), ("g", ctypes.c_void_p),
                 ("beta", ctypes.c_void_p), ("e", ctypes.c_void_p), ("T", ctypes.c_int),
                 ("keep", ctypes.c_int)]
-
-
-class _Cache(ctypes.Structure):
-    _fields_ = ([(n, ctypes.c_void_p) for n in ("k", "v", "table", "lens")] +
-                [(n, ctypes.c_longlong) for n in ("page_stride", "row_stride", "head_stride")] +
-                [(n, ctypes.c_int) for n in ("pages", "page_rows", "seq_pages")])
-
 
 _LIB_PATH = os.path.join(os.path.dirname(os.path.abspath(__file__)), "libkda.so")
 _lib = None
@@ -122,9 +116,8 @@ def load():
         fn.restype = ll
     for fn in (lib.kda_prompt, lib.kda_linear_prompt, lib.kda_linear_step, lib.kda_logprobs):
         fn.restype = i
-    c = ctypes.POINTER(_Cache)
-    lib.kda_cache_append.argtypes = [p, ll, p, ll, c, p, i, i, i, i, p]
-    lib.kda_attn_rows.argtypes = [p, ll, c, p, p, i, i, i, i, ctypes.c_float, i, i, i, p, ll, p]
+    lib.kda_cache_append.argtypes = [p, ll, p, ll, p, p, i, i, i, i, p]
+    lib.kda_attn_rows.argtypes = [p, ll, p, p, p, i, i, i, i, ctypes.c_float, i, i, i, p, ll, p]
     lib.kda_accept_sampled.argtypes = [p, ll, i, p, ll, p, p, p, p, p, p, i, i, i, p, ll, p]
     lib.kda_attn_rows_work_bytes.argtypes = [i, i, i, i]
     lib.kda_accept_sampled_work_bytes.argtypes = [i, i, i]
@@ -805,40 +798,55 @@ def accept_sampled_workspace(R: int, B: int, V: int, device=None) -> torch.Tenso
     return _workspace(_work_bytes(load().kda_accept_sampled_work_bytes, R, B, V), device)
 
 
+def _at(t, name: str, dtype, shape, device):
+    """_ptr, in a few accesses where nothing is to be refused."""
+    if (t is not None and t.dtype is dtype and t.shape == shape and t.get_device() == device.index
+            and t.is_contiguous()):
+        return t.data_ptr()
+    return _ptr(t, name, dtype, shape, device)
+
+
 def _strided(t, name: str, dtype, shape, device):
     """Address of rows [R][heads][D] and their stride: each row contiguous."""
-    if t.dtype != dtype:
+    if t.dtype is not dtype:
         raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
     if t.shape != shape:
         raise ValueError(f"{name} has shape {tuple(t.shape)}, expected {tuple(shape)}")
-    if t.device != device:
+    if t.get_device() != device.index:
         raise ValueError(f"{name} is on {t.device}, expected {device}")
-    if t.stride(2) != 1 or (shape[1] > 1 and t.stride(1) != D):
+    ld, head, one = t.stride()
+    if one != 1 or (head != D and shape[1] > 1):
         raise ValueError(f"{name}: the heads of a row must be contiguous")
-    return t.data_ptr(), t.stride(0)
+    return t.data_ptr(), ld
+
+
+# kda_cache: k, v, table, lens, three strides, pages, page_rows, seq_pages
+_pack_cache = struct.Struct("@4P3q3i0P").pack
 
 
 def _cache(k_pages, v_pages, table, lens, dtype, device):
-    """The cache's description, and its sequences and key heads."""
-    if k_pages.dim() != 4 or k_pages.shape[3] != D:
-        raise ValueError(f"k_pages must be [pages][rows][Hk][{D}], got {tuple(k_pages.shape)}")
-    for t, n in ((k_pages, "k_pages"), (v_pages, "v_pages")):
-        if t.dtype != dtype:
-            raise TypeError(f"{n} must be {dtype}, got {t.dtype}")
-        if t.device != device:
-            raise ValueError(f"{n} is on {t.device}, expected {device}")
-    if v_pages.shape != k_pages.shape or v_pages.stride() != k_pages.stride():
+    """The cache's description (a kda_cache), and its sequences and key heads."""
+    shape, strides, dev = k_pages.shape, k_pages.stride(), device.index
+    if len(shape) != 4 or shape[3] != D:
+        raise ValueError(f"k_pages must be [pages][rows][Hk][{D}], got {tuple(shape)}")
+    if v_pages.shape != shape or v_pages.stride() != strides:
         raise ValueError("k_pages and v_pages must have the same shape and strides")
-    if k_pages.stride(3) != 1:
+    if k_pages.dtype is not dtype or v_pages.dtype is not dtype:
+        raise TypeError(f"k_pages and v_pages must be {dtype}, got {k_pages.dtype} and {v_pages.dtype}")
+    if k_pages.get_device() != dev or v_pages.get_device() != dev:
+        raise ValueError(f"k_pages and v_pages are on {k_pages.device} and {v_pages.device}, expected {device}")
+    if strides[3] != 1:
         raise ValueError("the rows of a page must be contiguous")
-    if table.dim() != 2:
+    of = table.shape
+    if len(of) != 2:
         raise ValueError("table must be a [B][pages of a sequence] tensor")
-    B, seq_pages = table.shape
-    pages, rows, Hk, _ = k_pages.shape
-    _int32(pages, rows, seq_pages)
-    c = _Cache(k_pages.data_ptr(), v_pages.data_ptr(), _ptr(table, "table", torch.int32, (B, seq_pages), device),
-               _ptr(lens, "lens", torch.int32, (B,), device), *k_pages.stride()[:3], pages, rows, seq_pages)
-    return ctypes.byref(c), B, Hk
+    pages, rows, Hk, _ = shape
+    if pages > 0x7FFFFFFF or rows > 0x7FFFFFFF or of[1] > 0x7FFFFFFF:
+        _int32(pages, rows, of[1])
+    c = _pack_cache(k_pages.data_ptr(), v_pages.data_ptr(), _at(table, "table", torch.int32, of, device),
+                    _at(lens, "lens", torch.int32, of[:1], device), strides[0], strides[1], strides[2], pages, rows,
+                    of[1])
+    return c, of[0], Hk
 
 
 def kda_cache_append(k, v, k_pages, v_pages, table, lens, offsets, stream=None) -> None:
@@ -850,12 +858,14 @@ def kda_cache_append(k, v, k_pages, v_pages, table, lens, offsets, stream=None) 
     """
     lib = load()
     dev, st = _place(k, stream)
+    dtype = k.dtype
     dt = _row_dtype(k, "k")
-    c, B, Hk = _cache(k_pages, v_pages, table, lens, k.dtype, dev)
+    c, B, Hk = _cache(k_pages, v_pages, table, lens, dtype, dev)
     R = k.shape[0]
-    kp, k_ld = _strided(k, "k", k.dtype, (R, Hk, D), dev)
-    vp, v_ld = _strided(v, "v", k.dtype, (R, Hk, D), dev)
-    _check(lib.kda_cache_append(kp, k_ld, vp, v_ld, c, _ptr(offsets, "offsets", torch.int32, (B + 1,), dev),
+    shape = (R, Hk, D)
+    kp, k_ld = _strided(k, "k", dtype, shape, dev)
+    vp, v_ld = _strided(v, "v", dtype, shape, dev)
+    _check(lib.kda_cache_append(kp, k_ld, vp, v_ld, c, _at(offsets, "offsets", torch.int32, (B + 1,), dev),
                                 R, B, Hk, dt, st))
 
 
@@ -870,16 +880,19 @@ def kda_attn_rows(q, k_pages, v_pages, table, lens, offsets, o, scale=None, wind
     """
     lib = load()
     dev, st = _place(q, stream)
-    if q.dim() != 3:
-        raise ValueError(f"q must be [R][H][{D}], got {tuple(q.shape)}")
+    shape, dtype = q.shape, q.dtype
+    if len(shape) != 3:
+        raise ValueError(f"q must be [R][H][{D}], got {tuple(shape)}")
     dt = _row_dtype(q, "q")
-    c, B, Hk = _cache(k_pages, v_pages, table, lens, q.dtype, dev)
-    R, H = q.shape[:2]
-    _int32(R, H, window, sinks)
-    qp, q_ld = _strided(q, "q", q.dtype, (R, H, D), dev)
+    c, B, Hk = _cache(k_pages, v_pages, table, lens, dtype, dev)
+    R, H, _ = shape
+    shape = (R, H, D)
+    if window or sinks:
+        _int32(window, sinks)
+    qp, q_ld = _strided(q, "q", dtype, shape, dev)
     wp, wn = _work(work, dev)
-    _check(lib.kda_attn_rows(qp, q_ld, c, _ptr(offsets, "offsets", torch.int32, (B + 1,), dev),
-                             _ptr(o, "o", q.dtype, (R, H, D), dev), R, B, H, Hk,
+    _check(lib.kda_attn_rows(qp, q_ld, c, _at(offsets, "offsets", torch.int32, (B + 1,), dev),
+                             _at(o, "o", dtype, shape, dev), R, B, H, Hk,
                              D ** -0.5 if scale is None else scale, window, sinks, dt, wp, wn, st))
 
 
@@ -898,24 +911,31 @@ def kda_accept_sampled(logits, offsets, drafts, u, out, probs=None, temp=None, p
     dev, st = _place(logits, stream)
     if logits.dim() != 2:
         raise ValueError("logits must be a [R][V] tensor")
-    R, V = logits.shape
-    _int32(R, V)
+    R, V = shape = logits.shape
+    if R > 0x7FFFFFFF or V > 0x7FFFFFFF:
+        _int32(R, V)   # (other calls' tensors would not fit a GPU first)
     dt = _row_dtype(logits, "logits")
     f32 = torch.float32
-    for t, n in ((logits, "logits"), (probs, "probs")):
-        if t is None:
-            continue
-        if t.shape != (R, V) or t.device != dev or (V > 1 and t.stride(1) != 1):
-            raise ValueError(f"{n} must be [{R}][{V}] on {dev} with contiguous rows")
-    if probs is not None and probs.dtype != f32:
-        raise TypeError(f"probs must be float32, got {probs.dtype}")
+    ld, one = logits.stride()
+    if one != 1 and V > 1:
+        raise ValueError("logits rows must be contiguous")
+    qp, q_ld = None, V
+    if probs is not None:
+        if probs.dtype is not f32:
+            raise TypeError(f"probs must be float32, got {probs.dtype}")
+        if probs.shape != shape or probs.get_device() != dev.index:
+            raise ValueError(f"probs must be {tuple(shape)} on {dev}, is {tuple(probs.shape)} on {probs.device}")
+        q_ld, one = probs.stride()
+        if one != 1 and V > 1:
+            raise ValueError("probs rows must be contiguous")
+        qp = probs.data_ptr()
     B = offsets.shape[0] - 1 if offsets.dim() == 1 else -1
+    rows = (R,)
     wp, wn = _work(work, dev)
     _check(lib.kda_accept_sampled(
-        logits.data_ptr(), logits.stride(0), dt, None if probs is None else probs.data_ptr(),
-        V if probs is None else probs.stride(0), _ptr(offsets, "offsets", torch.int32, (B + 1,), dev),
-        _ids(drafts, "drafts", (R,), dev), _ptr(u, "u", f32, (R,), dev), _ptr(temp, "temp", f32, (B,), dev),
-        _ids(out, "out", (B, 2), dev), _ptr(p_draft, "p_draft", f32, (R,), dev), R, B, V, wp, wn, st))
+        logits.data_ptr(), ld, dt, qp, q_ld, _at(offsets, "offsets", torch.int32, (B + 1,), dev),
+        _ids(drafts, "drafts", rows, dev), _at(u, "u", f32, rows, dev), _at(temp, "temp", f32, (B,), dev),
+        _ids(out, "out", (B, 2), dev), _at(p_draft, "p_draft", f32, rows, dev), R, B, V, wp, wn, st))
 
 
 def kda_abi_version() -> int:

@@ -15,6 +15,12 @@ from tests.test_abi_host import Bufs, ERR_ALIAS, ERR_ALIGN, ERR_ARG, ERR_RANGE, 
 from tests.test_ops_host import _refused, _up
 
 
+class _Cache(ctypes.Structure):   # kda_cache
+    _fields_ = ([(n, ctypes.c_void_p) for n in ("k", "v", "table", "lens")] +
+                [(n, ctypes.c_longlong) for n in ("page_stride", "row_stride", "head_stride")] +
+                [(n, ctypes.c_int) for n in ("pages", "page_rows", "seq_pages")])
+
+
 @pytest.fixture(scope="module")
 def lib():
     if not os.path.exists(kda.lib_path()):
@@ -32,7 +38,7 @@ def _cache(b, **kw):
     a = dict(k=b["k"], v=b["v"], table=b["ptrs"], lens=b["s_in"], page_stride=16 * 2 * 128, row_stride=2 * 128,
              head_stride=128, pages=4, page_rows=16, seq_pages=5)
     a.update({n: v for n, v in kw.items() if n in a})
-    return kda._Cache(*(a[n].value if isinstance(a[n], ctypes.c_void_p) else a[n] for n, _ in kda._Cache._fields_))
+    return _Cache(*(a[n].value if isinstance(a[n], ctypes.c_void_p) else a[n] for n, _ in _Cache._fields_))
 
 
 def _append(lib, b, **kw):
@@ -189,6 +195,13 @@ def test_sampled_refusals(lib, b):
     assert _sampled(lib, b, R=0, x=None, d=None, u=None, probs=None, p=None, work=None, bytes=0) == OK
     for bad in ((-1, 1, 1), (1, 0, 1), (1, 1, 0), (1, 5000, 1)):
         assert lib.kda_accept_sampled_work_bytes(*bad) == -1
+
+
+def test_python_binding_packs_the_caches_description():
+    data = kda._pack_cache(1 << 40, 2, 3, 4, 5, 1 << 35, 7, 8, 9, 10)
+    assert len(data) == ctypes.sizeof(_Cache)
+    c = _Cache.from_buffer_copy(data)
+    assert [getattr(c, n) for n, _ in _Cache._fields_] == [1 << 40, 2, 3, 4, 5, 1 << 35, 7, 8, 9, 10]
 
 
 def test_python_binding_refuses_what_it_sees(lib):
