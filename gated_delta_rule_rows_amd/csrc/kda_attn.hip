@@ -359,10 +359,10 @@ __device__ __forceinline__ int key_of(const Work& w, int t) {
     return (t < w.tiles.first ? t : t - w.tiles.first + w.tiles.from) * KT;
 }
 
-// The table entry of the lane's key of tile t; -1: none.
-template <int KT>
+// The table entry of tile t (WHOLE: a tile lies in one page) or of the lane's key of it; -1: none.
+template <int KT, bool WHOLE>
 __device__ __forceinline__ int entry_of(const AttnArgs& a, const Work& w, int t) {
-    const int key = key_of<KT>(w, t) + static_cast<int>(threadIdx.x & 63) % KT;
+    const int key = key_of<KT>(w, t) + (WHOLE ? 0 : static_cast<int>(threadIdx.x & 63) % KT);
     return t < w.t1 && key < w.keys ? a.c.table[static_cast<long long>(w.f.b) * a.c.seq_pages + (key >> a.c.page_shift)] : -1;
 }
 
@@ -531,26 +531,52 @@ struct Columns {
     }
 };
 
+template <int KT>
+constexpr uint64_t kAll = KT == 64 ? ~0ull : (1ull << KT) - 1;
+
+// Where a tile lies: the byte offset (head 0) of its first row (WHOLE) or of the row of the lane's key, and
+// which of its rows exist.  What does not is read as the cache's first rows: no row sees it.
+struct Place {
+    long long off;
+    uint64_t there;
+};
+
+template <int KT, int ES, bool WHOLE>
+__device__ __forceinline__ Place place_of(const AttnArgs& a, const Work& w, int t, int entry) {
+    const int key0 = key_of<KT>(w, t);
+    if constexpr (WHOLE) {
+        const long long at = cache_at(a.c, __builtin_amdgcn_readfirstlane(entry), key0);
+        const int n = w.keys - key0;
+        return at < 0 ? Place{0, 0} : Place{at * ES, n >= KT ? kAll<KT> : (1ull << (n & 63)) - 1};
+    } else {
+        const long long at = cache_at(a.c, entry, key0 + static_cast<int>(threadIdx.x & 63) % KT);
+        return Place{at < 0 ? 0 : at * ES, __ballot(at >= 0) & kAll<KT>};
+    }
+}
+
 // Rows of a tile that a thread brings to LDS: 16 bytes of row row0 + j * kRowsAtOnce in load j.
-template <typename Sh, bool BF16>
+template <typename Sh, bool BF16, bool WHOLE>
 struct Loader {
     struct Rows {
         u32x4 r[Sh::kLoads];
     };
     int piece, row0;
-    const char* base;   // K's or V's, of the key head and piece
+    const char* base;     // K's or V's, of the key head
+    long long step;       // WHOLE: bytes from load to load
+    uint32_t mine;        // bytes to the thread's piece of the tile's (WHOLE) or of any row
 
     __device__ __forceinline__ Loader(const void* p, const CacheView& c, int kh)
         : piece(threadIdx.x % Sh::kPieces), row0(threadIdx.x / Sh::kPieces),
-          base(static_cast<const char*>(p) + kh * c.head_stride * Sh::kEs + piece * 16) {}
+          base(static_cast<const char*>(p) + kh * c.head_stride * Sh::kEs), step(Sh::kRowsAtOnce * c.row_stride * Sh::kEs),
+          mine((WHOLE ? row0 * static_cast<uint32_t>(c.row_stride) * Sh::kEs : 0) + piece * 16) {}
 
-    // off: byte offset of the lane's key's row; -1: none, read as the cache's first row (no row sees it).
     __device__ __forceinline__ Rows load(long long off) const {
-        const long long from = off >= 0 ? off : 0;
         Rows u;
 #pragma unroll
-        for (int j = 0; j < Sh::kLoads; ++j)
-            u.r[j] = *reinterpret_cast<const u32x4*>(base + __shfl(from, row0 + j * Sh::kRowsAtOnce));
+        for (int j = 0; j < Sh::kLoads; ++j) {
+            const char* at = base + (WHOLE ? off + j * step : __shfl(off, row0 + j * Sh::kRowsAtOnce));
+            u.r[j] = *reinterpret_cast<const u32x4*>(at + mine);
+        }
         return u;
     }
 
@@ -575,21 +601,11 @@ struct Loader {
     }
 };
 
-// Byte offset of the row of the lane's key; -1: none.
-template <int KT, int ES>
-__device__ __forceinline__ long long offset_of(const AttnArgs& a, const Work& w, int t, int entry) {
-    const long long at = cache_at(a.c, entry, key_of<KT>(w, t) + static_cast<int>(threadIdx.x & 63) % KT);
-    return at < 0 ? -1 : at * ES;
-}
-
-template <int KT>
-constexpr uint64_t kAll = KT == 64 ? ~0ull : (1ull << KT) - 1;
-
 // Waits for all loads: what a loop only reads would else be waited for in every turn, with what the turn loads.
 __device__ __forceinline__ void arrived() { __builtin_amdgcn_s_waitcnt(0x0F70); }
 
 // 128 columns: four waves share the tiles of keys, two of which lie in LDS.
-template <bool BF16, bool SPLIT>
+template <bool BF16, bool SPLIT, bool WHOLE>
 __global__ void __launch_bounds__(256, 2) attn_wide_kernel(AttnArgs a, Plan p) {
     using Sh = Shape<BF16, 4>;
     constexpr int KT = Sh::kKeys, NB = Sh::kBlocks, PK = Sh::kPitchK, PV = Sh::kPitchV, ROWS = 64 / Sh::kPieces;
@@ -604,15 +620,15 @@ __global__ void __launch_bounds__(256, 2) attn_wide_kernel(AttnArgs a, Plan p) {
     Columns<BF16> x;
     x.begin(a, p, w, c0);
     const float c = a.scale * kLog2e;
-    const Loader<Sh, BF16> from_k(a.c.k, a.c, w.kh), from_v(a.c.v, a.c, w.kh);
+    const Loader<Sh, BF16, WHOLE> from_k(a.c.k, a.c, w.kh), from_v(a.c.v, a.c, w.kh);
     const int key_place = (lane & 31) * PK + (lane >> 5) * 16, value_at = KT * PK + value_place<BF16, PV>();
-    typename Loader<Sh, BF16>::Rows nk, nv;
+    typename Loader<Sh, BF16, WHOLE>::Rows nk, nv;
     uint64_t there = 0, next_there = 0;   // the tile's rows that exist
     const auto fetch = [&](int t, int entry) {
-        const long long off = offset_of<KT, Sh::kEs>(a, w, t, entry);
-        next_there = __ballot(off >= 0) & kAll<KT>;
-        nk = from_k.load(off);
-        nv = from_v.load(off);
+        const Place at = place_of<KT, Sh::kEs, WHOLE>(a, w, t, entry);
+        next_there = at.there;
+        nk = from_k.load(at.off);
+        nv = from_v.load(at.off);
     };
     const auto uneven = [&](int t) { return there != kAll<KT> || partly<KT>(a, key_of<KT>(w, t), w.lo, w.hi); };
     const auto keep = [&](int t, int buf) {
@@ -624,10 +640,10 @@ __global__ void __launch_bounds__(256, 2) attn_wide_kernel(AttnArgs a, Plan p) {
         from_k.template store<PK>(nk, tiles[buf]);
         from_v.template store<PV>(nv, tiles[buf] + KT * PK);
     };
-    int entry = entry_of<KT>(a, w, w.t0);
+    int entry = entry_of<KT, WHOLE>(a, w, w.t0);
     if (w.t0 < w.t1) {
         fetch(w.t0, entry);
-        entry = entry_of<KT>(a, w, w.t0 + 1);
+        entry = entry_of<KT, WHOLE>(a, w, w.t0 + 1);
         keep(w.t0, 0);
     }
     __syncthreads();
@@ -638,7 +654,7 @@ __global__ void __launch_bounds__(256, 2) attn_wide_kernel(AttnArgs a, Plan p) {
         const bool any_masked = uneven(t);
         if (t + 1 < w.t1) {
             fetch(t + 1, entry);
-            entry = entry_of<KT>(a, w, t + 2);
+            entry = entry_of<KT, WHOLE>(a, w, t + 2);
         }
         if (row_lo < w.rows && key0 <= wave_hi) {
             f32x16 s[NB];
@@ -664,7 +680,7 @@ __global__ void __launch_bounds__(256, 2) attn_wide_kernel(AttnArgs a, Plan p) {
 
 // 32 columns: a wave by itself, many a CU.  K and V of a tile take turns in one region of LDS and in the
 // registers that hold what is on its way: V comes while the scores are computed, the next K behind them.
-template <bool BF16, bool SPLIT>
+template <bool BF16, bool SPLIT, bool WHOLE>
 __global__ void __launch_bounds__(64, 2) attn_narrow_kernel(AttnArgs a, Plan p) {
     using Sh = Shape<BF16, 1>;
     constexpr int KT = Sh::kKeys, PK = Sh::kPitchK, PV = Sh::kPitchV;
@@ -673,11 +689,11 @@ __global__ void __launch_bounds__(64, 2) attn_narrow_kernel(AttnArgs a, Plan p) 
     const int lane = threadIdx.x & 63;
     const Work w = work_of<KT, SPLIT>(a, p);
     if (w.f.b < 0) return;
-    const Loader<Sh, BF16> from_k(a.c.k, a.c, w.kh), from_v(a.c.v, a.c, w.kh);
-    long long off = offset_of<KT, Sh::kEs>(a, w, w.t0, entry_of<KT>(a, w, w.t0));
-    int entry = entry_of<KT>(a, w, w.t0 + 1);
-    typename Loader<Sh, BF16>::Rows u;
-    if (w.t0 < w.t1) u = from_k.load(off);
+    const Loader<Sh, BF16, WHOLE> from_k(a.c.k, a.c, w.kh), from_v(a.c.v, a.c, w.kh);
+    Place at = place_of<KT, Sh::kEs, WHOLE>(a, w, w.t0, entry_of<KT, WHOLE>(a, w, w.t0));
+    int entry = entry_of<KT, WHOLE>(a, w, w.t0 + 1);
+    typename Loader<Sh, BF16, WHOLE>::Rows u;
+    if (w.t0 < w.t1) u = from_k.load(at.off);
     Columns<BF16> x;
     x.begin(a, p, w, 0);
     const float c = a.scale * kLog2e;
@@ -689,12 +705,12 @@ __global__ void __launch_bounds__(64, 2) attn_narrow_kernel(AttnArgs a, Plan p) 
     };
     if (w.t0 < w.t1) {
         from_k.template store<PK>(u, tile);
-        u = from_v.load(off);
+        u = from_v.load(at.off);
     }
     arrived();
     for (int t = w.t0; t < w.t1; ++t) {
         const int key0 = key_of<KT>(w, t);
-        const uint64_t there = __ballot(off >= 0) & kAll<KT>;
+        const uint64_t there = at.there;
         const bool masked = there != kAll<KT> || partly<KT>(a, key0, w.lo, w.hi);
         order();
         f32x16 s[1] = {x.scores(tile + key_place)};
@@ -708,9 +724,9 @@ __global__ void __launch_bounds__(64, 2) attn_narrow_kernel(AttnArgs a, Plan p) 
         }
         from_v.template store<PV>(u, tile);
         if (t + 1 < w.t1) {
-            off = offset_of<KT, Sh::kEs>(a, w, t + 1, entry);
-            u = from_k.load(off);
-            entry = entry_of<KT>(a, w, t + 2);
+            at = place_of<KT, Sh::kEs, WHOLE>(a, w, t + 1, entry);
+            u = from_k.load(at.off);
+            entry = entry_of<KT, WHOLE>(a, w, t + 2);
         }
         x.weights(s, c);
         order();
@@ -723,7 +739,7 @@ __global__ void __launch_bounds__(64, 2) attn_narrow_kernel(AttnArgs a, Plan p) 
         order();
         if (t + 1 < w.t1) {
             from_k.template store<PK>(u, tile);
-            u = from_v.load(off);
+            u = from_v.load(at.off);
         }
     }
     x.template finish<SPLIT>(a, p, w, 0);
@@ -809,23 +825,34 @@ __global__ void __launch_bounds__(kJoinThreads) attn_join_kernel(AttnArgs a, Pla
 // Four waves a tile where a sequence fills more than one wave's columns on average.
 bool is_wide(int R, int B, int H, int Hk) { return static_cast<long long>(R) * (H / Hk) > static_cast<long long>(B) * kColumns; }
 
+template <bool BF16, bool WIDE, bool WHOLE>
+void start(const AttnArgs& a, const Plan& p, unsigned grid, hipStream_t stream) {
+    if constexpr (WIDE) {
+        if (p.parts)
+            attn_wide_kernel<BF16, true, WHOLE><<<dim3(grid), dim3(256), 0, stream>>>(a, p);
+        else
+            attn_wide_kernel<BF16, false, WHOLE><<<dim3(grid), dim3(256), 0, stream>>>(a, p);
+    } else {
+        if (p.parts)
+            attn_narrow_kernel<BF16, true, WHOLE><<<dim3(grid), dim3(64), 0, stream>>>(a, p);
+        else
+            attn_narrow_kernel<BF16, false, WHOLE><<<dim3(grid), dim3(64), 0, stream>>>(a, p);
+    }
+}
+
 template <bool BF16, bool WIDE>
 hipError_t launch(const AttnArgs& a, hipStream_t stream) {
     Plan p = plan_of(a.R, a.B, a.H, a.Hk, WIDE);
     const int n_heads = a.Hk * p.groups;
     if (static_cast<long long>(a.c.seq_pages) << a.c.page_shift <= kSplitKeys) p.parts = 0;
-    const dim3 grid(static_cast<unsigned>(p.parts + p.slots) * n_heads), block(WIDE ? 256 : 64);
-    if (p.parts == 0) {
-        if constexpr (WIDE)
-            attn_wide_kernel<BF16, false><<<grid, block, 0, stream>>>(a, p);
-        else
-            attn_narrow_kernel<BF16, false><<<grid, block, 0, stream>>>(a, p);
-        return hipGetLastError();
-    }
-    if constexpr (WIDE)
-        attn_wide_kernel<BF16, true><<<grid, block, 0, stream>>>(a, p);
+    const unsigned grid = static_cast<unsigned>(p.parts + p.slots) * n_heads;
+    // Pages of whole tiles need one entry a tile, and no address of a row of its own (rows within 2^31 bytes).
+    constexpr int KT = Shape<BF16, WIDE ? 4 : 1>::kKeys, ES = BF16 ? 2 : 4;
+    if (1 << a.c.page_shift >= KT && a.c.row_stride < (1ll << 31) / (KT * ES))
+        start<BF16, WIDE, true>(a, p, grid, stream);
     else
-        attn_narrow_kernel<BF16, true><<<grid, block, 0, stream>>>(a, p);
+        start<BF16, WIDE, false>(a, p, grid, stream);
+    if (p.parts == 0) return hipGetLastError();
     const hipError_t e = hipGetLastError();
     if (e != hipSuccess) return e;
     // Columns of many splits take four waves each.  Of few, a wave each, and some of them a workgroup
