@@ -126,8 +126,7 @@ __device__ __forceinline__ Item find_item(const AttnArgs& a, const Plan& p, int 
     const auto row = [&](int b) { return min(max(a.offsets[b], 0), a.R); };
     int most = 0;
     for (int b = from; b < to; ++b) most = max(most, row(b));
-    int before = __shfl_up(running_max(most), 1);
-    if (lane == 0) before = 0;
+    const int before = lane_before(running_max(most), 0);
     // Calls back for each of the lane's sequences: its rows, tiles of columns and tiles of keys.
     const auto visit = [&](auto&& with) {
         int run = before;
@@ -155,17 +154,11 @@ __device__ __forceinline__ Item find_item(const AttnArgs& a, const Plan& p, int 
     };
     long long units = 0;
     again([&](int, int, int, int across, int along) { units += static_cast<long long>(across) * along; });
-#pragma unroll
-    for (int d = 32; d >= 1; d >>= 1) units += __shfl_xor(units, d);
+    units = of_lane(running_sum(units), 63);
     const int unit = max(kLeastTiles, static_cast<int>(min((units + p.parts - 1) / p.parts, 1ll << 30)));
     int mine = 0;
     again([&](int, int, int, int across, int along) { mine += across * max(1, div_up(along, unit)); });
-    int upto = mine;
-#pragma unroll
-    for (int d = 1; d < 64; d <<= 1) {
-        const int y = __shfl_up(upto, d);
-        if (lane >= d) upto += y;
-    }
+    const int upto = running_sum(mine);
     Item f{-1, 0, 0, 0, 1, 0, 0};
     const uint64_t mask = __ballot(item >= upto - mine && item < upto);
     if (mask == 0) return f;

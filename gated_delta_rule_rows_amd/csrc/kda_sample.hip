@@ -89,16 +89,10 @@ __device__ __forceinline__ double scale_of(const SampledArgs& a, int b) {
     return t > 0.f && t < kInf ? 1.0 / t : 0.0;
 }
 
-__device__ __forceinline__ double wave_sum(double x) {
-#pragma unroll
-    for (int d = 32; d >= 1; d >>= 1) x += __shfl_xor(x, d);
-    return x;
-}
+__device__ __forceinline__ double wave_sum(double x) { return of_lane(running_sum(x), 63); }
 
 __device__ __forceinline__ float wave_max(float x) {
-#pragma unroll
-    for (int d = 32; d >= 1; d >>= 1) x = fmaxf(x, __shfl_xor(x, d));
-    return x;
+    return of_lane(running(x, -kInf, [](float a, float b) { return fmaxf(a, b); }), 63);
 }
 
 // s moved to a maximum m >= s.m.
@@ -256,17 +250,6 @@ __device__ __forceinline__ void by_kind(int kind, F&& f) {
 
 __device__ __forceinline__ int piece_tokens(const SampledArgs& a, const Split& w) { return (a.V + w.pieces - 1) / w.pieces; }
 
-// Inclusive running sum over the lanes.
-__device__ __forceinline__ double running_sum(double x) {
-    const int lane = threadIdx.x & 63;
-#pragma unroll
-    for (int d = 1; d < 64; d <<= 1) {
-        const double y = __shfl_up(x, d);
-        if (lane >= d) x += y;
-    }
-    return x;
-}
-
 // The token of a session.
 template <bool BF16>
 __global__ void __launch_bounds__(kTokenThreads) sample_token_kernel(SampledArgs a, Split w) {
@@ -289,14 +272,14 @@ __global__ void __launch_bounds__(kTokenThreads) sample_token_kernel(SampledArgs
     // the piece: the first whose running sum passes the place (every wave finds it)
     if (f.drafted && __ballot(mass.w > 0.0) == 0) f.drafted = 0;
     const double mine = f.drafted ? mass.w : mass.p, upto = running_sum(mine);
-    const double place = f.u * __shfl(upto, 63);
+    const double place = f.u * of_lane(upto, 63);
     uint64_t mask = __ballot(mine > 0.0 && upto > place);
     if (mask == 0) {   // a place at or behind the end: the last piece with weight
         mask = __ballot(mine > 0.0);
         mask = mask ? 1ull << (63 - __builtin_clzll(mask)) : 1ull;
     }
     const int piece = __builtin_ctzll(mask);
-    double at = __shfl(upto - mine, piece);
+    double at = of_lane(upto - mine, piece);
     // the token in it: sums of each 64 tokens, their running sums, and those of the tokens where the
     // place lies
     const Weights weights = weights_of<BF16>(a, f);
@@ -319,7 +302,7 @@ __global__ void __launch_bounds__(kTokenThreads) sample_token_kernel(SampledArgs
         const uint64_t parts = __ballot(part > 0.0), passed = __ballot(part > 0.0 && run > place);
         const int found = passed ? __builtin_ctzll(passed) : parts ? 63 - __builtin_clzll(parts) : -1;
         if (found >= 0 && found % WAVES == wave) {
-            const double before = __shfl(run - part, found);
+            const double before = of_lane(run - part, found);
             double mine64 = 0.0;
 #pragma unroll
             for (int i = 0; i < N; ++i)
@@ -332,7 +315,7 @@ __global__ void __launch_bounds__(kTokenThreads) sample_token_kernel(SampledArgs
         }
         __syncthreads();
         if (token < a.V) break;
-        at = __shfl(run, 63);
+        at = of_lane(run, 63);
     }
     if (tid == 0) {
         a.out[2 * b] = f.j;

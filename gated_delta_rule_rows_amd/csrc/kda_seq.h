@@ -22,15 +22,62 @@ struct Part {
     int last;
 };
 
-// Inclusive running maximum over the lanes.
-__device__ __forceinline__ int running_max(int x) {
-    const int lane = threadIdx.x & 63;
-#pragma unroll
-    for (int d = 1; d < 64; d <<= 1) {
-        const int y = __shfl_up(x, d);
-        if (lane >= d) x = max(x, y);
+// Inclusive running folds over the lanes of a wave, f(before, mine), without LDS: within rows of 16 lanes by
+// shifts, then over the rows.  A lane that a step does not reach gets `none`.
+template <int CTRL, int ROWS>
+__device__ __forceinline__ int lane_step(int none, int x) {
+    return __builtin_amdgcn_update_dpp(none, x, CTRL, ROWS, 0xF, false);
+}
+
+template <int CTRL, int ROWS>
+__device__ __forceinline__ float lane_step(float none, float x) {
+    return __builtin_bit_cast(float, lane_step<CTRL, ROWS>(__builtin_bit_cast(int, none), __builtin_bit_cast(int, x)));
+}
+
+template <int CTRL, int ROWS, typename T64>
+__device__ __forceinline__ T64 lane_step(T64 none, T64 x) {
+    static_assert(sizeof(T64) == 8, "two words");
+    const long long n = __builtin_bit_cast(long long, none), y = __builtin_bit_cast(long long, x);
+    const uint32_t lo = lane_step<CTRL, ROWS>(static_cast<int>(n), static_cast<int>(y));
+    const uint32_t hi = lane_step<CTRL, ROWS>(static_cast<int>(n >> 32), static_cast<int>(y >> 32));
+    return __builtin_bit_cast(T64, static_cast<long long>(static_cast<unsigned long long>(hi) << 32 | lo));
+}
+
+template <typename T, typename F>
+__device__ __forceinline__ T running(T x, T none, F&& f) {
+    x = f(lane_step<0x111, 0xF>(none, x), x);   // row_shr:1, 2, 4, 8
+    x = f(lane_step<0x112, 0xF>(none, x), x);
+    x = f(lane_step<0x114, 0xF>(none, x), x);
+    x = f(lane_step<0x118, 0xF>(none, x), x);
+    x = f(lane_step<0x142, 0xA>(none, x), x);   // row_bcast:15 into rows 1 and 3
+    return f(lane_step<0x143, 0xC>(none, x), x);   // row_bcast:31 into rows 2 and 3
+}
+
+// The value of one lane in all.
+template <typename T>
+__device__ __forceinline__ T of_lane(T x, int lane) {
+    if constexpr (sizeof(T) == 4) {
+        return __builtin_bit_cast(T, __builtin_amdgcn_readlane(__builtin_bit_cast(int, x), lane));
+    } else {
+        const long long y = __builtin_bit_cast(long long, x);
+        const uint32_t lo = __builtin_amdgcn_readlane(static_cast<int>(y), lane), hi = __builtin_amdgcn_readlane(static_cast<int>(y >> 32), lane);
+        return __builtin_bit_cast(T, static_cast<long long>(static_cast<unsigned long long>(hi) << 32 | lo));
     }
-    return x;
+}
+
+template <typename T>
+__device__ __forceinline__ T running_sum(T x) {
+    return running(x, T(0), [](T a, T b) { return a + b; });
+}
+
+__device__ __forceinline__ int running_max(int x) {
+    return running(x, -2147483647 - 1, [](int a, int b) { return max(a, b); });
+}
+
+// The value of the lane before; `first` in lane 0.
+__device__ __forceinline__ int lane_before(int x, int first) {
+    const int y = __shfl_up(x, 1);
+    return (threadIdx.x & 63) == 0 ? first : y;
 }
 
 // The sequence of a slot: the last one whose slots begin at or before it.  The
@@ -57,8 +104,7 @@ __device__ __forceinline__ Part find_part(const Args& a, int part_rows, int slot
         int x = 0;
         for (int b = from; b < to; ++b) x = max(x, row(b));
         const int upto = running_max(x);
-        int ahead = __shfl_up(upto, 1);
-        if (lane == 0) ahead = 0;
+        const int ahead = lane_before(upto, 0);
         const uint64_t mask = __ballot(from < to && max(ahead, row(min(from, a.B - 1))) / part_rows + from <= slot);
         if (mask == 0) return f;
         const int at = 63 - __builtin_clzll(mask);
@@ -83,9 +129,7 @@ template <typename Args>
 __device__ __forceinline__ void sequence(const Args& a, int b, int& first, int& last) {
     int x = 0;
     for (int i = threadIdx.x & 63; i <= b; i += 64) x = max(x, min(max(a.offsets[i], 0), a.R));
-#pragma unroll
-    for (int m = 32; m >= 1; m >>= 1) x = max(x, __shfl_xor(x, m));
-    first = __builtin_amdgcn_readfirstlane(x);
+    first = of_lane(running_max(x), 63);
     last = min(max(a.offsets[b + 1], first), a.R);
 }
 
