@@ -270,10 +270,11 @@ __device__ __forceinline__ uint32_t part_finite(u32x4& u) {
     return bad;
 }
 
-// O^T += V^T P^T over a tile; v: the lane's place in its V.  P is rounded to bf16 for a bf16 cache, by
-// half a step of 2^-8 at most; l sums it unrounded.
-template <bool BF16, int NB, int PITCH>
-__device__ __forceinline__ void add_values(f32x16 (&acc)[4], const f32x16 (&s)[NB], const char* v) {
+// O^T += V^T P^T over a tile.  at(row, d): where the lane reads V from row `row` on (bf16: by four_keys; f32:
+// a float), channels of block d.  P is rounded to bf16 for a bf16 cache, by half a step of 2^-8 at most; l sums
+// it unrounded.
+template <bool BF16, int NB, typename At>
+__device__ __forceinline__ void add_values(f32x16 (&acc)[4], const f32x16 (&s)[NB], At&& at) {
     if constexpr (BF16) {
 #pragma unroll
         for (int b = 0; b < NB; ++b)
@@ -283,8 +284,7 @@ __device__ __forceinline__ void add_values(f32x16 (&acc)[4], const f32x16 (&s)[N
                 const uint4 w = make_uint4(p(0), p(2), p(4), p(6));
 #pragma unroll
                 for (int d = 0; d < 4; ++d) {
-                    const char* at = v + (32 * b + 16 * step) * PITCH + 64 * d;
-                    const uint2 x = four_keys(at), y = four_keys(at + 8 * PITCH);
+                    const uint2 x = four_keys(at(32 * b + 16 * step, d)), y = four_keys(at(32 * b + 16 * step + 8, d));
                     acc[d] = mfma(make_uint4(x.x, x.y, y.x, y.y), w, acc[d]);
                 }
             }
@@ -293,7 +293,7 @@ __device__ __forceinline__ void add_values(f32x16 (&acc)[4], const f32x16 (&s)[N
         for (int r = 0; r < 16; ++r)
 #pragma unroll
             for (int d = 0; d < 4; ++d)
-                acc[d] = mfma(*reinterpret_cast<const float*>(v + (8 * (r >> 2) + (r & 3)) * PITCH + 128 * d), s[0][r], acc[d]);
+                acc[d] = mfma(*reinterpret_cast<const float*>(at(8 * (r >> 2) + (r & 3), d)), s[0][r], acc[d]);
     }
 }
 
@@ -407,24 +407,40 @@ struct Columns {
         l = 0.f;
     }
 
-    // S^T of 32 keys; k: the lane's place in their K, rows PITCH bytes apart.
-    __device__ __forceinline__ f32x16 scores(const char* k) const {
-        f32x16 s;
+    // S^T of 32 NB keys; read(b, i): 16 bytes of the lane's key of block b, pieces 2 i + half.  The blocks'
+    // products alternate (each waits for the one before it in its block), K is read some products ahead.
+    template <int NB, typename Read>
+    __device__ __forceinline__ void scores(f32x16 (&s)[NB], Read&& read) const {
+        constexpr int N = NB * kQ, AHEAD = 4;
+        uint4 u[AHEAD];
 #pragma unroll
-        for (int r = 0; r < 16; ++r) s[r] = 0.f;
+        for (int i = 0; i < AHEAD; ++i) u[i] = read(i % NB, i / NB);
 #pragma unroll
-        for (int x = 0; x < kQ; ++x) {
-            const uint4 u = *reinterpret_cast<const uint4*>(k + 32 * x);
+        for (int b = 0; b < NB; ++b)
+#pragma unroll
+            for (int r = 0; r < 16; ++r) s[b][r] = 0.f;
+#pragma unroll
+        for (int i = 0; i < N; ++i) {
+            const uint4 w = u[i % AHEAD], y = q[i / NB];
+            f32x16& z = s[i % NB];
+            if (i + AHEAD < N) u[i % AHEAD] = read((i + AHEAD) % NB, (i + AHEAD) / NB);
             if constexpr (BF16) {
-                s = mfma(u, q[x], s);
+                z = mfma(w, y, z);
             } else {
-                s = mfma(real(u.x), real(q[x].x), s);
-                s = mfma(real(u.y), real(q[x].y), s);
-                s = mfma(real(u.z), real(q[x].z), s);
-                s = mfma(real(u.w), real(q[x].w), s);
+                z = mfma(real(w.x), real(y.x), z);
+                z = mfma(real(w.y), real(y.y), z);
+                z = mfma(real(w.z), real(y.z), z);
+                z = mfma(real(w.w), real(y.w), z);
             }
         }
-        return s;
+        if constexpr (BF16 && NB > 1) {   // in this order
+            __builtin_amdgcn_sched_group_barrier(0x100, AHEAD, 0);
+#pragma unroll
+            for (int i = 0; i < N; ++i) {
+                __builtin_amdgcn_sched_group_barrier(0x008, 1, 0);
+                if (i + AHEAD < N) __builtin_amdgcn_sched_group_barrier(0x100, 1, 0);
+            }
+        }
     }
 
     // Scores of keys that the column does not see (bits of `seen`) to -inf.
@@ -597,15 +613,29 @@ struct Loader {
 // Waits for all loads: what a loop only reads would else be waited for in every turn, with what the turn loads.
 __device__ __forceinline__ void arrived() { __builtin_amdgcn_s_waitcnt(0x0F70); }
 
+// The tiles of the wide kernel in LDS, row by row as they are loaded there: piece c of row r lies at
+// c ^ turn(r), so that the 16-byte reads of K (16 or 8 rows), and those of V (four rows of 64 bytes, or
+// rows 4 apart of 128 bytes) lie on all banks.
+template <bool BF16>
+__device__ __forceinline__ int turn_k(int row) { return BF16 ? row & 15 : row & 7; }
+template <bool BF16>
+__device__ __forceinline__ int turn_v(int row) { return BF16 ? (row & 3) << 2 : (row & 4) << 1; }
+
+// 16 bytes a lane from global memory to LDS, lane after lane from `to` (the same in all lanes) on.
+__device__ __forceinline__ void to_lds(const char* from, char* to) {
+    __builtin_amdgcn_global_load_lds((const __attribute__((address_space(1))) void*)from, (__attribute__((address_space(3))) void*)to, 16, 0, 0);
+}
+
 // 128 columns: four waves share the tiles of keys, two of which lie in LDS.
 template <bool BF16, bool SPLIT, bool WHOLE>
 __global__ void __launch_bounds__(256, 2) attn_wide_kernel(AttnArgs a, Plan p) {
     using Sh = Shape<BF16, 4>;
-    constexpr int KT = Sh::kKeys, NB = Sh::kBlocks, PK = Sh::kPitchK, PV = Sh::kPitchV, ROWS = 64 / Sh::kPieces;
-    __shared__ __align__(16) char tiles[2][Sh::kTile];
-    __shared__ uint32_t spoiled[2][4];   // whether the wave's rows of V are in odd
-    __shared__ uint8_t odd[2][KT * Sh::kPieces];
-    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, c0 = wave * kColumns;
+    constexpr int KT = Sh::kKeys, NB = Sh::kBlocks, ES = Sh::kEs, ROW = kD * ES, PIECES = Sh::kPieces, BYTES = KT * ROW;
+    // (arrays of their own: what is on its way to one does not hold up the reads of another)
+    __shared__ __align__(16) char k0[BYTES], v0[BYTES], k1[BYTES], v1[BYTES];
+    __shared__ uint32_t spoiled[4];      // whether the wave found values that are not finite: odd says which
+    __shared__ uint8_t odd[KT * PIECES];
+    const int lane = threadIdx.x & 63, half = lane >> 5, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), c0 = wave * kColumns;
     const Work w = work_of<KT, SPLIT>(a, p);
     if (w.f.b < 0) return;
     // the wave's positions
@@ -613,60 +643,86 @@ __global__ void __launch_bounds__(256, 2) attn_wide_kernel(AttnArgs a, Plan p) {
     Columns<BF16> x;
     x.begin(a, p, w, c0);
     const float c = a.scale * kLog2e;
-    const Loader<Sh, BF16, WHOLE> from_k(a.c.k, a.c, w.kh), from_v(a.c.v, a.c, w.kh);
-    const int key_place = (lane & 31) * PK + (lane >> 5) * 16, value_at = KT * PK + value_place<BF16, PV>();
-    typename Loader<Sh, BF16, WHOLE>::Rows nk, nv;
-    uint64_t there = 0, next_there = 0;   // the tile's rows that exist
-    const auto fetch = [&](int t, int entry) {
-        const Place at = place_of<KT, Sh::kEs, WHOLE>(a, w, t, entry);
-        next_there = at.there;
-        nk = from_k.load(at.off);
-        nv = from_v.load(at.off);
-    };
-    const auto uneven = [&](int t) { return there != kAll<KT> || partly<KT>(a, key_of<KT>(w, t), w.lo, w.hi); };
-    const auto keep = [&](int t, int buf) {
-        there = next_there;
-        if (uneven(t)) {
-            const bool any = from_v.part(nv, odd[buf]);
-            if (lane == 0) spoiled[buf][wave] = any;
+    // what the thread brings: place `piece` of rows row0 + j * kRowsAtOnce, which has another piece
+    const int piece = threadIdx.x % PIECES, row0 = threadIdx.x / PIECES;
+    const int piece_k = piece ^ turn_k<BF16>(row0), piece_v = piece ^ turn_v<BF16>(row0);
+    const long long step = Sh::kRowsAtOnce * a.c.row_stride * ES;
+    const uint32_t mine = WHOLE ? row0 * static_cast<uint32_t>(a.c.row_stride) * ES : 0;
+    const char* base_k = static_cast<const char*>(a.c.k) + w.kh * a.c.head_stride * ES;
+    const char* base_v = static_cast<const char*>(a.c.v) + w.kh * a.c.head_stride * ES;
+    const auto fetch = [&](const Place& at, char* k, char* v) {
+#pragma unroll
+        for (int j = 0; j < Sh::kLoads; ++j) {
+            const long long off = WHOLE ? at.off + j * step : __shfl(at.off, row0 + j * Sh::kRowsAtOnce);
+            const int to = (j * 4 + wave) * 1024;
+            to_lds(base_k + off + (mine + piece_k * 16), k + to);
+            to_lds(base_v + off + (mine + piece_v * 16), v + to);
         }
-        from_k.template store<PK>(nk, tiles[buf]);
-        from_v.template store<PV>(nv, tiles[buf] + KT * PK);
     };
+    // where the lane reads
+    const int key_at = (lane & 31) * ROW + ((half ^ turn_k<BF16>(lane & 31)) * 16);
+    const int i16 = lane & 15, r0 = BF16 ? 4 * half + (i16 >> 2) : 4 * half;
+    const int value_at = BF16 ? r0 * ROW + ((2 * (lane >> 4 & 1) + (i16 >> 1 & 1)) ^ turn_v<BF16>(r0)) * 16 + (i16 & 1) * 8
+                              : r0 * ROW + (((lane & 31) >> 2) ^ turn_v<BF16>(r0)) * 16 + (lane & 3) * 4;
+    uint64_t there = 0, next_there = 0;   // the tile's rows that exist
     int entry = entry_of<KT, WHOLE>(a, w, w.t0);
-    if (w.t0 < w.t1) {
-        fetch(w.t0, entry);
-        entry = entry_of<KT, WHOLE>(a, w, w.t0 + 1);
-        keep(w.t0, 0);
-    }
-    __syncthreads();
-    arrived();
-    for (int t = w.t0; t < w.t1; ++t) {
-        const int buf = (t - w.t0) & 1, key0 = key_of<KT>(w, t);
-        const uint64_t now = there;
-        const bool any_masked = uneven(t);
+    const auto turn = [&](int t, char* k, char* v, char* next_k, char* next_v) {
+        const int key0 = key_of<KT>(w, t);
+        const bool uneven = there != kAll<KT> || partly<KT>(a, key0, w.lo, w.hi);
         if (t + 1 < w.t1) {
-            fetch(t + 1, entry);
+            const Place at = place_of<KT, ES, WHOLE>(a, w, t + 1, entry);
+            next_there = at.there;
+            fetch(at, next_k, next_v);
             entry = entry_of<KT, WHOLE>(a, w, t + 2);
+        }
+        // Some row does not see all keys: 0 x NaN would carry a NaN or an infinity of V into rows that do not
+        // see it, so it is made 0, odd says which channels of which key it was, and the rows that see it get
+        // a NaN afterwards.
+        if (uneven) {
+            bool any = false;
+#pragma unroll
+            for (int j = 0; j < Sh::kLoads; ++j) {
+                const int row = row0 + j * Sh::kRowsAtOnce;
+                u32x4* at = reinterpret_cast<u32x4*>(v + row * ROW + piece * 16);
+                u32x4 u = *at;
+                const uint32_t bad = part_finite<BF16>(u);
+                if (bad) *at = u;
+                odd[row * PIECES + piece_v] = static_cast<uint8_t>(bad);
+                any |= bad != 0;
+            }
+            const bool some = __ballot(any) != 0;
+            if (lane == 0) spoiled[wave] = some;
+            __syncthreads();
         }
         if (row_lo < w.rows && key0 <= wave_hi) {
             f32x16 s[NB];
+            x.template scores<NB>(s, [&](int b, int i) { return *reinterpret_cast<const uint4*>(k + (key_at ^ (i * 32)) + b * 32 * ROW); });
+            if (there != kAll<KT> || partly<KT>(a, key0, wave_lo, wave_hi))
 #pragma unroll
-            for (int b = 0; b < NB; ++b) s[b] = x.scores(tiles[buf] + key_place + 32 * b * PK);
-            if (now != kAll<KT> || partly<KT>(a, key0, wave_lo, wave_hi))
-#pragma unroll
-                for (int b = 0; b < NB; ++b) x.mask(s[b], seen_by(a, static_cast<uint32_t>(now >> 32 * b), x.pos, key0 + 32 * b));
+                for (int b = 0; b < NB; ++b) x.mask(s[b], seen_by(a, static_cast<uint32_t>(there >> 32 * b), x.pos, key0 + 32 * b));
             x.weights(s, c);
-            add_values<BF16, NB, PV>(x.acc, s, tiles[buf] + value_at);
-            if (any_masked && (spoiled[buf][0] | spoiled[buf][1] | spoiled[buf][2] | spoiled[buf][3])) {
+            add_values<BF16, NB>(x.acc, s, [&](int row, int d) { return v + (value_at ^ (d * (BF16 ? 64 : 128))) + row * ROW; });
+            if (uneven && (spoiled[0] | spoiled[1] | spoiled[2] | spoiled[3])) {
 #pragma unroll 1
                 for (int i = 0; i < KT; ++i)
-                    if (spoiled[buf][i / ROWS % 4] && seen_by(a, static_cast<uint32_t>(now >> (i & 32)), x.pos, key0 + (i & 32)) >> (i & 31) & 1)
-                        x.spoil(odd[buf] + i * Sh::kPieces);
+                    if (seen_by(a, static_cast<uint32_t>(there >> (i & 32)), x.pos, key0 + (i & 32)) >> (i & 31) & 1) x.spoil(odd + i * PIECES);
             }
         }
-        if (t + 1 < w.t1) keep(t + 1, buf ^ 1);
+        there = next_there;
+        arrived();
         __syncthreads();
+    };
+    if (w.t0 < w.t1) {
+        const Place at = place_of<KT, ES, WHOLE>(a, w, w.t0, entry);
+        there = at.there;
+        fetch(at, k0, v0);
+        entry = entry_of<KT, WHOLE>(a, w, w.t0 + 1);
+    }
+    arrived();
+    __syncthreads();
+    for (int t = w.t0; t < w.t1; t += 2) {
+        turn(t, k0, v0, k1, v1);
+        if (t + 1 < w.t1) turn(t + 1, k1, v1, k0, v0);
     }
     x.template finish<SPLIT>(a, p, w, c0);
 }
@@ -706,7 +762,8 @@ __global__ void __launch_bounds__(64, 2) attn_narrow_kernel(AttnArgs a, Plan p) 
         const uint64_t there = at.there;
         const bool masked = there != kAll<KT> || partly<KT>(a, key0, w.lo, w.hi);
         order();
-        f32x16 s[1] = {x.scores(tile + key_place)};
+        f32x16 s[1];
+        x.template scores<1>(s, [&](int, int i) { return *reinterpret_cast<const uint4*>(tile + key_place + 32 * i); });
         order();
         bool odds = false;
         uint32_t seen = 0;
@@ -723,7 +780,7 @@ __global__ void __launch_bounds__(64, 2) attn_narrow_kernel(AttnArgs a, Plan p) 
         }
         x.weights(s, c);
         order();
-        add_values<BF16, 1, PV>(x.acc, s, tile + value_at);
+        add_values<BF16, 1>(x.acc, s, [&](int row, int d) { return tile + value_at + row * PV + d * (BF16 ? 64 : 128); });
         if (odds) {
 #pragma unroll 1
             for (int i = 0; i < KT; ++i)
