@@ -696,10 +696,12 @@ __global__ void __launch_bounds__(256, 2) attn_wide_kernel(AttnArgs a, Plan p) {
         }
         if (row_lo < w.rows && key0 <= wave_hi) {
             f32x16 s[NB];
+            __builtin_amdgcn_s_setprio(1);   // before the other wave's weights
             x.template scores<NB>(s, [&](int b, int i) { return *reinterpret_cast<const uint4*>(k + (key_at ^ (i * 32)) + b * 32 * ROW); });
             if (there != kAll<KT> || partly<KT>(a, key0, wave_lo, wave_hi))
 #pragma unroll
                 for (int b = 0; b < NB; ++b) x.mask(s[b], seen_by(a, static_cast<uint32_t>(there >> 32 * b), x.pos, key0 + 32 * b));
+            __builtin_amdgcn_s_setprio(0);
             x.weights(s, c);
             add_values<BF16, NB>(x.acc, s, [&](int row, int d) { return v + (value_at ^ (d * (BF16 ? 64 : 128))) + row * ROW; });
             if (uneven && (spoiled[0] | spoiled[1] | spoiled[2] | spoiled[3])) {
@@ -799,16 +801,15 @@ __global__ void __launch_bounds__(64, 2) attn_narrow_kernel(AttnArgs a, Plan p) 
 // has two channels.
 template <bool BF16, int TEAM>
 __global__ void __launch_bounds__(kJoinThreads) attn_join_kernel(AttnArgs a, Plan p, int columns, int per) {
-    constexpr int WAVES = kJoinThreads / 64, AHEAD = TEAM > 1 ? 4 : 8;
+    constexpr int WAVES = kJoinThreads / 64, AHEAD = 8;
     __shared__ float2 sums[WAVES][64];
     __shared__ float2 ml[WAVES];
     const int n_heads = a.Hk * p.groups, hd = blockIdx.x % n_heads, slot = blockIdx.x / n_heads;
     const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, mate = wave % TEAM;
-    const Part f = find_part(a, p.rows, slot);
-    if (f.b < 0) return;
     const Partials w(a.work, p, n_heads);
-    const int2 tile = w.tiles[slot];
-    if (tile.y <= 1) return;
+    const int2 tile = w.tiles[slot];   // (anything, where the slot is empty)
+    const Part f = find_part(a, p.rows, slot);
+    if (f.b < 0 || tile.y <= 1) return;
     const int first = f.first + f.index * p.rows, kh = hd / p.groups, G = a.H / a.Hk, g0 = hd % p.groups * p.heads;
     const long long step = static_cast<long long>(n_heads) * p.cols;
     const int begin = blockIdx.y * per, end = min(begin + per, columns);
