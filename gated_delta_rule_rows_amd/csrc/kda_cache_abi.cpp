@@ -3,7 +3,6 @@
 
 #include <hip/hip_runtime.h>
 
-#include <climits>
 #include <cmath>
 #include <cstdint>
 #include <utility>
@@ -71,9 +70,13 @@ int check_cache(const char* fn, const kda_cache* c, int B, int Hk, unsigned es, 
     if (c->pages < 1) return refuse(KDA_ERR_RANGE, "%s: cache.pages=%d, need >= 1", fn, c->pages);
     if (c->page_rows < 1 || (c->page_rows & (c->page_rows - 1)) != 0 || c->page_rows > KDA_PAGE_ROWS_MAX)
         return refuse(KDA_ERR_RANGE, "%s: cache.page_rows=%d is no power of two in 1..%d", fn, c->page_rows, KDA_PAGE_ROWS_MAX);
-    if (c->seq_pages < 1 || static_cast<long long>(c->seq_pages) * c->page_rows > INT_MAX)
-        return refuse(KDA_ERR_RANGE, "%s: cache.seq_pages=%d: need 1 .. 2^31-1 rows in a sequence", fn, c->seq_pages);
-    Axis axes[3] = {{c->page_stride, c->pages}, {c->row_stride, c->page_rows}, {c->head_stride, Hk}};
+    if (c->seq_pages < 1 || static_cast<long long>(c->seq_pages) * c->page_rows > 1ll << 30)
+        return refuse(KDA_ERR_RANGE, "%s: cache.seq_pages=%d: need 1 .. 2^30 rows in a sequence", fn, c->seq_pages);
+    // (one page, row or head has no stride)
+    Axis axes[3] = {{c->pages > 1 ? c->page_stride : 0, c->pages},
+                    {c->page_rows > 1 ? c->row_stride : 0, c->page_rows},
+                    {Hk > 1 ? c->head_stride : 0, Hk}};
+    v->page_stride = axes[0].stride; v->row_stride = axes[1].stride; v->head_stride = axes[2].stride;
     long long last = kD;
     for (const Axis& x : axes) {
         if (x.stride < 0 || x.stride > kStrideMax || (x.count > 1 && x.stride > kStrideMax / (x.count - 1)))
@@ -94,7 +97,6 @@ int check_cache(const char* fn, const kda_cache* c, int B, int Hk, unsigned es, 
     int rc;
     if ((rc = check_spans(fn, spans, 4))) return rc;
     v->k = c->k; v->v = c->v; v->table = c->table; v->lens = c->lens;
-    v->page_stride = c->page_stride; v->row_stride = c->row_stride; v->head_stride = c->head_stride;
     v->pages = c->pages;
     v->page_shift = __builtin_ctz(static_cast<unsigned>(c->page_rows));
     v->seq_pages = c->seq_pages;

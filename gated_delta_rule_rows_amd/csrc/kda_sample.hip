@@ -82,11 +82,11 @@ __device__ __forceinline__ const void* row_at(const SampledArgs& a, long long r)
     return static_cast<const char*>(a.logits) + r * a.ld * (BF16 ? 2 : 4);
 }
 
-// 1 / T of a session; 0 where T is no positive finite number.
+// 1 / T of a session; 0 where T is no finite number of 1e-30 at least (its reciprocal has to be one in f32).
 __device__ __forceinline__ double scale_of(const SampledArgs& a, int b) {
     if (!a.temp) return 1.0;
     const float t = a.temp[b];
-    return t > 0.f && t < kInf ? 1.0 / t : 0.0;
+    return t >= 1e-30f && t < kInf ? 1.0 / t : 0.0;
 }
 
 __device__ __forceinline__ double wave_sum(double x) { return of_lane(running_sum(x), 63); }

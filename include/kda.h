@@ -533,7 +533,8 @@ long long kda_logprobs_work_bytes(int t, int V, int n_top);
  *               zero.)  A rollback is a smaller length: glm_spec.rs (0.123.0),
  *               module doc ROLLBACK, truncates the attention layers' rows so.
  *   pages     : pages in k and v, >= 1.   page_rows : a power of two up to
- *               KDA_PAGE_ROWS_MAX.   seq_pages * page_rows <= 2^31 - 1.
+ *               KDA_PAGE_ROWS_MAX.   seq_pages * page_rows <= 2^30.  (A stride of one
+ *               page, row or head is not read.)
  */
 typedef struct {
     void* k;
@@ -630,8 +631,8 @@ long long kda_attn_rows_work_bytes(int R, int B, int H, int Hk);
  *               were), or NULL.
  *   A row that holds a NaN or +inf, or whose logits are all -inf, has no
  *   distribution: no draft is accepted there, its p_draft is NaN, and if the walk ends
- *   there the token is KDA_NO_TOKEN.  A temperature that is no positive finite
- *   number: j = 0, KDA_NO_TOKEN and NaN.
+ *   there the token is KDA_NO_TOKEN.  A temperature that is no finite number of
+ *   1e-30 at least: j = 0, KDA_NO_TOKEN and NaN.
  *   Weights and running sums are f64, and so is the sum of a row's exponentials,
  *   which are f32: p is good to about 1e-6 of itself.
  *   work      : kda_accept_sampled_work_bytes(R, B, V) bytes, 16-byte aligned, in

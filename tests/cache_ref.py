@@ -108,7 +108,7 @@ def accept_ref(logits, offsets, drafts, u, probs=None, temp=None):
             margin.append(math.inf)
             continue
         t = 1.0 if temp is None else float(temp[b])
-        good_t = t > 0 and math.isfinite(t)
+        good_t = t >= 1e-30 and math.isfinite(t)
         ps = []
         for r in range(first, last):
             x = x64[r]

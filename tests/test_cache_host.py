@@ -75,7 +75,7 @@ def test_cache_refusals(lib, b, call):
     for rows in (0, -16, 3, 48, 2 * _header_constant("KDA_PAGE_ROWS_MAX")):
         no(ERR_RANGE, "page_rows", page_rows=rows)
     no(ERR_RANGE, "seq_pages=0", seq_pages=0)
-    no(ERR_RANGE, "seq_pages", seq_pages=1 << 27)                       # 2^31 rows
+    no(ERR_RANGE, "seq_pages", seq_pages=(1 << 26) + 1)                 # over 2^30 rows
     no(ERR_RANGE, "negative", page_stride=-4096)
     no(ERR_RANGE, "too large", page_stride=(1 << 40) + 4)
     no(ERR_RANGE, "too large", page_stride=1 << 39)
@@ -122,6 +122,10 @@ def test_append_refusals(lib, b):
     assert _append(lib, b, R=0, nk=None, nv=None, v=_up(b["k"], 256 * 4), row_stride=512, page_stride=8192) == OK
     assert _append(lib, b, R=0, nk=None, nv=None, v=_up(b["k"], 128 * 4), head_stride=256, row_stride=512, page_stride=8192) == OK
     assert _append(lib, b, R=0, nk=None, nv=None, head_stride=16 * 128, row_stride=128) == OK
+    # one page, row or head has no stride
+    assert _append(lib, b, R=0, nk=None, nv=None, pages=1, page_stride=-7) == OK
+    assert _append(lib, b, R=0, nk=None, nv=None, Hk=1, head_stride=3, k_ld=128, v_ld=128) == OK
+    assert _append(lib, b, R=0, nk=None, nv=None, page_rows=1, row_stride=-1, page_stride=256) == OK
 
 
 def test_attn_refusals(lib, b):

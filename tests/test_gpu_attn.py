@@ -186,6 +186,60 @@ def test_attn_spoiled_rows_reach_only_those_that_see_them(dt, bad, n, length, wi
 
 
 @pytest.mark.parametrize("dt", TYPES)
+@pytest.mark.parametrize("n", [1, 15, 90])
+def test_attn_a_query_that_is_not_finite_spoils_its_row_and_head_alone(dt, n):
+    gen = torch.Generator().manual_seed(n)
+    k, v, table = make_cache(gen, [300], 16, 2, dt)
+    q = torch.randn(n, 4, D, generator=gen).to(dt).cuda()
+    clean, o = (torch.empty(n, 4, D, dtype=dt, device="cuda") for _ in range(2))
+    _call(q, k, v, table, [300], [0, n], clean)
+    for bad in (math.nan, math.inf):
+        x = q.clone()
+        x[n // 2, 2, 9] = bad
+        _call(x, k, v, table, [300], [0, n], o)
+        hit = torch.zeros(n, 4, dtype=torch.bool, device="cuda")
+        hit[n // 2, 2] = True
+        assert torch.isnan(o[hit]).all() and torch.equal(o[~hit], clean[~hit])
+
+
+def test_binding_refuses_what_it_sees_of_device_tensors():
+    gen = torch.Generator().manual_seed(1)
+    k, v, table = make_cache(gen, [20, 30], 16, 2, torch.float32)
+    lens = torch.tensor([20, 30], dtype=torch.int32, device="cuda")
+    offsets = torch.tensor([0, 3, 5], dtype=torch.int32, device="cuda")
+    q, o, new = (torch.zeros(5, h, D, device="cuda") for h in (4, 4, 2))
+    work = kda.attn_workspace(5, 2, 4, 2)
+
+    def attn(q=q, k=k, v=v, table=table, lens=lens, offsets=offsets, o=o, **kw):
+        kda.kda_attn_rows(q, k, v, table, lens, offsets, o, work=work, **kw)
+
+    def append(new_k=new, new_v=new, k=k, v=v, table=table, lens=lens, offsets=offsets):
+        kda.kda_cache_append(new_k, new_v, k, v, table, lens, offsets)
+
+    attn()
+    append()
+    for call in (attn, append):
+        for kw in (dict(k=k[0]), dict(k=k[:2]), dict(v=v.transpose(1, 2).contiguous().transpose(1, 2)), dict(k=k[..., :64]),
+                   dict(k=k.repeat_interleave(2, 3)[..., ::2], v=v.repeat_interleave(2, 3)[..., ::2]), dict(k=k.cpu()),
+                   dict(table=table[0]), dict(table=table[:, ::2]), dict(table=table.cpu()), dict(lens=lens[:1]),
+                   dict(offsets=offsets[:2])):
+            with pytest.raises((ValueError, kda.KdaError)):
+                call(**kw)
+        for kw in (dict(k=k.bfloat16(), v=v.bfloat16()), dict(table=table.long()), dict(lens=lens.long()), dict(offsets=offsets.long())):
+            with pytest.raises(TypeError):
+                call(**kw)
+    with pytest.raises(TypeError):
+        attn(q=q.half(), o=o.half(), k=k.half(), v=v.half())
+    for kw in (dict(o=o[:4]), dict(q=q[:, :, ::2]), dict(q=q[:, :3], o=o[:, :3].contiguous()), dict(q=q.transpose(0, 1).contiguous().transpose(0, 1)),
+               dict(o=torch.zeros(5, 8, D, device="cuda")[:, ::2]), dict(window=-1), dict(sinks=1), dict(scale=0.0), dict(window=2**31)):
+        with pytest.raises((ValueError, kda.KdaError)):
+            attn(**kw)
+    for kw in (dict(new_v=new[:4]), dict(new_k=torch.zeros(5, 2, 2 * D, device="cuda")[..., ::2]), dict(new_k=k.view(-1, 2, D)[:5])):
+        with pytest.raises((ValueError, kda.KdaError)):
+            append(**kw)
+
+
+@pytest.mark.parametrize("dt", TYPES)
 def test_attn_scores_of_any_size(dt):
     # weights that underflow but for one key, a score of -inf, scores that only the maximum keeps finite
     gen = torch.Generator().manual_seed(4)

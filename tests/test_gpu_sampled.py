@@ -112,8 +112,8 @@ def test_sampled_rows_without_a_distribution():
     out = _check(x, offsets, drafts, u, probs)
     assert [int(y) for y in out[:, 0]] == [1, 0, 2, 0, 1]
     assert [int(y) for y in out[:4, 1]] == [-1, -1, -1, -1] and int(out[4, 1]) >= 0
-    temp = torch.tensor([1.0, 0.0, -1.0, math.nan, math.inf], device="cuda")
-    _check(x, offsets, drafts, u, probs, temp)
+    for temp in ([1.0, 0.0, -1.0, math.nan, math.inf], [1e-29, 1e-31, 3e38, 1e-40, 1e30]):
+        _check(x, offsets, drafts, u, probs, torch.tensor(temp, device="cuda"))
 
 
 def test_sampled_borders():
