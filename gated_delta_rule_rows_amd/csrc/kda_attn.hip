@@ -40,10 +40,11 @@ constexpr float kInf = __builtin_inff();
 constexpr float kLog2e = 1.44269504088896340736f;
 constexpr float kSlack = 8.0f;        // the carried maximum may lag by this much (base 2)
 constexpr int kColumns = 32;          // columns of a wave
-constexpr int kTargetNarrow = 2048;   // workgroups that fill the chip: one wave each
+constexpr int kTargetNarrow = 2048;   // workgroups that run side by side: one wave each
 constexpr int kTargetWide = 512;      // four waves each
 constexpr int kLeastTiles = 1;        // a split has this many tiles at least
-constexpr int kSplitKeys = 256;       // a cache of no more keys a sequence is never split
+constexpr int kSplitKeys = 128;       // a cache of no more keys a sequence is never split
+constexpr int kNarrowColumns = 96;    // of a sequence, up to which f32 rows take the narrow kernel
 constexpr int kAppendThreads = 256;
 constexpr int kJoinThreads = 256;
 constexpr int kManySplits = 32;       // of a column: joined by four waves
@@ -190,14 +191,9 @@ __device__ __forceinline__ Item find_item(const AttnArgs& a, const Plan& p, int 
 template <bool BF16, int WAVES>
 struct Shape {
     static constexpr int kEs = BF16 ? 2 : 4;
-    static constexpr int kKeys = BF16 && WAVES == 4 ? 64 : 32;
+    static constexpr int kKeys = BF16 ? 64 : 32;
     static constexpr int kBlocks = kKeys / 32;
     static constexpr int kPieces = kD * kEs / 16;              // 16-byte pieces of a row
-    // Pitches of the rows in LDS.  K: 16 rows of a 16-byte read lie on all banks.  V: four rows of 64
-    // bytes (bf16), or rows 4 apart of 128 bytes (f32).
-    static constexpr int kPitchK = kD * kEs + 16;
-    static constexpr int kPitchV = kD * kEs + (BF16 ? 64 : 32);
-    static constexpr int kTile = kKeys * (kPitchK + kPitchV);  // K, then V
     static constexpr int kThreads = WAVES * 64;
     static constexpr int kRowsAtOnce = kThreads / kPieces;     // rows that a load of all threads covers
     static constexpr int kLoads = kKeys / kRowsAtOnce;         // 16-byte loads a thread, for K and for V
@@ -295,15 +291,6 @@ __device__ __forceinline__ void add_values(f32x16 (&acc)[4], const f32x16 (&s)[N
             for (int d = 0; d < 4; ++d)
                 acc[d] = mfma(*reinterpret_cast<const float*>(at(8 * (r >> 2) + (r & 3), d)), s[0][r], acc[d]);
     }
-}
-
-// Where a lane reads V: bf16, by four_keys, rows 4 half + (i >> 2), channels 16 (lane >> 4 & 1) + 4 (i & 3)
-// on; f32, row 4 half, channel col.
-template <bool BF16, int PITCH>
-__device__ __forceinline__ int value_place() {
-    const int lane = threadIdx.x & 63, i = lane & 15;
-    if constexpr (BF16) return (4 * (lane >> 5) + (i >> 2)) * PITCH + 32 * (lane >> 4 & 1) + 8 * (i & 3);
-    return 4 * (lane >> 5) * PITCH + 4 * (lane & 31);
 }
 
 // What a workgroup computes: rows x heads columns, keys of tiles t0 .. t1-1.
@@ -564,7 +551,7 @@ __device__ __forceinline__ Place place_of(const AttnArgs& a, const Work& w, int 
 }
 
 // Rows of a tile that a thread brings to LDS: 16 bytes of row row0 + j * kRowsAtOnce in load j.
-template <typename Sh, bool BF16, bool WHOLE>
+template <typename Sh, bool WHOLE>
 struct Loader {
     struct Rows {
         u32x4 r[Sh::kLoads];
@@ -602,7 +589,7 @@ struct Loader {
     __device__ __forceinline__ bool part(Rows& u, uint8_t* odd) const {
         uint32_t bad[Sh::kLoads], any = 0;
 #pragma unroll
-        for (int j = 0; j < Sh::kLoads; ++j) any |= bad[j] = part_finite<BF16>(u.r[j]);
+        for (int j = 0; j < Sh::kLoads; ++j) any |= bad[j] = part_finite<false>(u.r[j]);
         if (__ballot(any != 0) == 0) return false;
 #pragma unroll
         for (int j = 0; j < Sh::kLoads; ++j) odd[(row0 + j * Sh::kRowsAtOnce) * Sh::kPieces + piece] = static_cast<uint8_t>(bad[j]);
@@ -729,26 +716,27 @@ __global__ void __launch_bounds__(256, 2) attn_wide_kernel(AttnArgs a, Plan p) {
     x.template finish<SPLIT>(a, p, w, c0);
 }
 
-// 32 columns: a wave by itself, many a CU.  K and V of a tile take turns in one region of LDS and in the
-// registers that hold what is on its way: V comes while the scores are computed, the next K behind them.
-template <bool BF16, bool SPLIT, bool WHOLE>
+// 32 columns of f32: a wave by itself, eight a CU.  K and V of a tile take turns in one region of LDS and in
+// the registers that hold what is on its way: V comes while the scores are computed, the next K behind them.
+template <bool SPLIT, bool WHOLE>
 __global__ void __launch_bounds__(64, 2) attn_narrow_kernel(AttnArgs a, Plan p) {
-    using Sh = Shape<BF16, 1>;
-    constexpr int KT = Sh::kKeys, PK = Sh::kPitchK, PV = Sh::kPitchV;
-    __shared__ __align__(16) char tile[KT * (PK > PV ? PK : PV)];
+    using Sh = Shape<false, 1>;
+    // Pitches of the rows in LDS.  K: 16 rows of a 16-byte read lie on all banks; V: rows 4 apart of 128 bytes.
+    constexpr int KT = Sh::kKeys, PK = kD * 4 + 16, PV = kD * 4 + 32;
+    __shared__ __align__(16) char tile[KT * PV];
     __shared__ uint8_t odd[KT * Sh::kPieces];
     const int lane = threadIdx.x & 63;
     const Work w = work_of<KT, SPLIT>(a, p);
     if (w.f.b < 0) return;
-    const Loader<Sh, BF16, WHOLE> from_k(a.c.k, a.c, w.kh), from_v(a.c.v, a.c, w.kh);
+    const Loader<Sh, WHOLE> from_k(a.c.k, a.c, w.kh), from_v(a.c.v, a.c, w.kh);
     Place at = place_of<KT, Sh::kEs, WHOLE>(a, w, w.t0, entry_of<KT, WHOLE>(a, w, w.t0));
     int entry = entry_of<KT, WHOLE>(a, w, w.t0 + 1);
-    typename Loader<Sh, BF16, WHOLE>::Rows u;
+    typename Loader<Sh, WHOLE>::Rows u;
     if (w.t0 < w.t1) u = from_k.load(at.off);
-    Columns<BF16> x;
+    Columns<false> x;
     x.begin(a, p, w, 0);
     const float c = a.scale * kLog2e;
-    const int key_place = (lane & 31) * PK + (lane >> 5) * 16, value_at = value_place<BF16, PV>();
+    const int key_place = (lane & 31) * PK + (lane >> 5) * 16, value_at = 4 * (lane >> 5) * PV + 4 * (lane & 31);
     // (one wave: its LDS accesses are done in order)
     const auto order = [] {
         __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
@@ -782,7 +770,7 @@ __global__ void __launch_bounds__(64, 2) attn_narrow_kernel(AttnArgs a, Plan p) 
         }
         x.weights(s, c);
         order();
-        add_values<BF16, 1>(x.acc, s, [&](int row, int d) { return tile + value_at + row * PV + d * (BF16 ? 64 : 128); });
+        add_values<false, 1>(x.acc, s, [&](int row, int d) { return tile + value_at + row * PV + d * 128; });
         if (odds) {
 #pragma unroll 1
             for (int i = 0; i < KT; ++i)
@@ -873,8 +861,15 @@ __global__ void __launch_bounds__(kJoinThreads) attn_join_kernel(AttnArgs a, Pla
     }
 }
 
-// Four waves a tile where a sequence fills more than one wave's columns on average.
-bool is_wide(int R, int B, int H, int Hk) { return static_cast<long long>(R) * (H / Hk) > static_cast<long long>(B) * kColumns; }
+// The narrow kernel takes f32 rows of up to 96 columns a sequence on average: its matrix products are the
+// bound there, and a tile of 32 columns has fewer that do not exist.  8 sequences of 8,192 keys x 8 key heads,
+// 32 columns each: 126 us against the wide kernel's 172; 96 columns 262 against 311; 120 columns 346 against
+// 314.  bf16 is bound by memory there, and the wide kernel holds more loads on their way with fewer
+// registers: one token of 15 sessions x 8,192 keys x 64 heads 98 us against 103, of one with 65,536 keys 24
+// against 39, 32 columns 62 against 76; there is no narrow kernel for it.
+bool is_wide(int R, int B, int H, int Hk, bool bf16) {
+    return bf16 || static_cast<long long>(R) * (H / Hk) > static_cast<long long>(B) * kNarrowColumns;
+}
 
 template <bool BF16, bool WIDE, bool WHOLE>
 void start(const AttnArgs& a, const Plan& p, unsigned grid, hipStream_t stream) {
@@ -885,9 +880,9 @@ void start(const AttnArgs& a, const Plan& p, unsigned grid, hipStream_t stream) 
             attn_wide_kernel<BF16, false, WHOLE><<<dim3(grid), dim3(256), 0, stream>>>(a, p);
     } else {
         if (p.parts)
-            attn_narrow_kernel<BF16, true, WHOLE><<<dim3(grid), dim3(64), 0, stream>>>(a, p);
+            attn_narrow_kernel<true, WHOLE><<<dim3(grid), dim3(64), 0, stream>>>(a, p);
         else
-            attn_narrow_kernel<BF16, false, WHOLE><<<dim3(grid), dim3(64), 0, stream>>>(a, p);
+            attn_narrow_kernel<false, WHOLE><<<dim3(grid), dim3(64), 0, stream>>>(a, p);
     }
 }
 
@@ -895,9 +890,13 @@ template <bool BF16, bool WIDE>
 hipError_t launch(const AttnArgs& a, hipStream_t stream) {
     Plan p = plan_of(a.R, a.B, a.H, a.Hk, WIDE);
     const int n_heads = a.Hk * p.groups;
+    // A short cache in one launch: one token, 8 heads, 120 keys 9.6 us a call, 12.5 with the join; 248 keys
+    // 12.6 and 12.4.
     if (static_cast<long long>(a.c.seq_pages) << a.c.page_shift <= kSplitKeys) p.parts = 0;
     const unsigned grid = static_cast<unsigned>(p.parts + p.slots) * n_heads;
-    // Pages of whole tiles need one entry a tile, and no address of a row of its own (rows within 2^31 bytes).
+    // Pages of whole tiles need one entry a tile, and no address of a row of its own (rows within 2^31 bytes):
+    // a prompt of 2,048 rows x 64 heads bf16 102 us, row by row 110; 8 verify rounds of 15 rows over 4,096 keys
+    // x 16 heads f32 117 and 129.
     constexpr int KT = Shape<BF16, WIDE ? 4 : 1>::kKeys, ES = BF16 ? 2 : 4;
     if (1 << a.c.page_shift >= KT && a.c.row_stride < (1ll << 31) / (KT * ES))
         start<BF16, WIDE, true>(a, p, grid, stream);
@@ -907,7 +906,9 @@ hipError_t launch(const AttnArgs& a, hipStream_t stream) {
     const hipError_t e = hipGetLastError();
     if (e != hipSuccess) return e;
     // Columns of many splits take four waves each.  Of few, a wave each, and some of them a workgroup
-    // where there are many (it begins with a search for its rows).
+    // where there are many (it begins with a search for its rows).  Whole calls with four waves and with one:
+    // one token over 65,536 keys, 8 heads (256 splits) 39 and 103 us; of 4 sessions over 16,384 (50) 62 and 66;
+    // of 15 over 8,192 (17) 110 and 104; ragged chunks (4) 106 and 65.
     const int columns = (a.R < p.rows ? a.R : p.rows) * p.heads;
     const unsigned tiles = static_cast<unsigned>(p.slots) * n_heads;
     if (p.parts > kManySplits * p.slots) {
@@ -935,8 +936,13 @@ hipError_t launch_append(const AppendArgs& a, bool bf16, hipStream_t stream) {
 }
 
 long long attn_workgroups(int R, int B, int H, int Hk) {
-    const Plan p = plan_of(R, B, H, Hk, is_wide(R, B, H, Hk));
-    return (static_cast<long long>(p.slots) + p.parts) * Hk * p.groups;
+    long long most = 0;
+    for (const bool bf16 : {false, true}) {
+        const Plan p = plan_of(R, B, H, Hk, is_wide(R, B, H, Hk, bf16));
+        const long long n = (static_cast<long long>(p.slots) + p.parts) * Hk * p.groups;
+        if (n > most) most = n;
+    }
+    return most;
 }
 
 // Grows with R and B, though the division of a call does not.
@@ -953,8 +959,8 @@ long long attn_work_bytes(int R, int B, int H, int Hk) {
 }
 
 hipError_t launch_attn(const AttnArgs& a, bool bf16, hipStream_t stream) {
-    if (is_wide(a.R, a.B, a.H, a.Hk)) return bf16 ? launch<true, true>(a, stream) : launch<false, true>(a, stream);
-    return bf16 ? launch<true, false>(a, stream) : launch<false, false>(a, stream);
+    if (bf16) return launch<true, true>(a, stream);
+    return is_wide(a.R, a.B, a.H, a.Hk, false) ? launch<false, true>(a, stream) : launch<false, false>(a, stream);
 }
 
 }  // namespace kda
