@@ -30,14 +30,16 @@ namespace {
 
 constexpr float kInf = __builtin_inff();
 constexpr double kLog2e = 1.44269504088896340736;
-constexpr float kSlack = 4.0f;       // the carried maximum may lag by this much
+constexpr float kSlack = 6.0f;       // the carried reference may lag by this much (base 2)
 constexpr int kThreads = 256;
 constexpr int kMostParts = 64;       // of a row: a lane joins a part
 constexpr int kChunk = 4096;         // tokens of a piece, if that makes no more than 64 pieces
 constexpr int kAcceptThreads = 512;
 constexpr int kTokenThreads = 512;
 
-// m, and z relative to it; z is NaN where a value is NaN or +inf.
+// m, about the largest x, and z = sum 2^{(x - m) by}, by = log2(e) / T in f32; z is NaN where a value is NaN
+// or +inf.  (Taken as x by - c in one operation a power would be cheaper, but where x / T is large the rounding
+// of c alone would pass f32's range.)
 struct Stat {
     double z;
     float m;
@@ -47,9 +49,9 @@ struct Stat {
 // A session's row j.
 struct Found {
     double z;
-    double scale;  // 1 / T; 0: no token
     double u;      // of the session's last row
     float m;
+    float by;      // 0: no token
     int row;       // -1: the session has no rows
     int j;
     int drafted;   // weights max(p - q, 0) unless these are all 0; else p
@@ -82,11 +84,10 @@ __device__ __forceinline__ const void* row_at(const SampledArgs& a, long long r)
     return static_cast<const char*>(a.logits) + r * a.ld * (BF16 ? 2 : 4);
 }
 
-// 1 / T of a session; 0 where T is no finite number of 1e-30 at least (its reciprocal has to be one in f32).
-__device__ __forceinline__ double scale_of(const SampledArgs& a, int b) {
-    if (!a.temp) return 1.0;
-    const float t = a.temp[b];
-    return t >= 1e-30f && t < kInf ? 1.0 / t : 0.0;
+// log2(e) / T of a session; 0 where T is no finite number of 1e-30 at least (it has to be one in f32).
+__device__ __forceinline__ float by_of(const SampledArgs& a, int b) {
+    const float t = a.temp ? a.temp[b] : 1.f;
+    return t >= 1e-30f && t < kInf ? static_cast<float>(kLog2e / t) : 0.f;
 }
 
 __device__ __forceinline__ double wave_sum(double x) { return of_lane(running_sum(x), 63); }
@@ -95,28 +96,27 @@ __device__ __forceinline__ float wave_max(float x) {
     return of_lane(running(x, -kInf, [](float a, float b) { return fmaxf(a, b); }), 63);
 }
 
-// s moved to a maximum m >= s.m.
-__device__ __forceinline__ double moved(Stat s, float m, double scale) {
-    return s.m == -kInf ? s.z : s.z * exp((static_cast<double>(s.m) - m) * scale);
+// s's z at a reference m >= s.m.
+__device__ __forceinline__ double moved(Stat s, float m, float by) {
+    return s.m == -kInf ? s.z : s.z * exp2((static_cast<double>(s.m) - m) * by);
 }
 
 // Adds E values of a lane.
 template <int E>
-__device__ __forceinline__ void take(Stat& s, const float (&x)[E], double scale) {
+__device__ __forceinline__ void take(Stat& s, const float (&x)[E], float by) {
     float top = x[0];
 #pragma unroll
     for (int e = 1; e < E; ++e) top = fmaxf(top, x[e]);
-    const float rate = static_cast<float>(scale), by = static_cast<float>(scale * kLog2e);
-    if (__ballot((top - s.m) * rate > kSlack || s.m == -kInf)) {
+    if (__ballot(((top - s.m) * by > kSlack) | (s.m == -kInf))) {
         const float m = fmaxf(s.m, top);
-        s.z = moved(s, m, scale);
+        s.z = moved(s, m, by);
         s.m = m;
     }
     const float base = s.m == -kInf ? 0.f : s.m;
-    float z = 0.f;
+    float z[4] = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
-    for (int e = 0; e < E; ++e) z += __builtin_amdgcn_exp2f((x[e] - base) * by);
-    s.z += z;
+    for (int e = 0; e < E; ++e) z[e & 3] += __builtin_amdgcn_exp2f((x[e] - base) * by);
+    s.z += (z[0] + z[1]) + (z[2] + z[3]);
 }
 
 template <bool BF16>
@@ -125,8 +125,8 @@ __global__ void __launch_bounds__(kThreads) sample_stats_kernel(SampledArgs a, S
     const int part = blockIdx.x % w.parts;
     const Part f = find_part(a, 1, blockIdx.x / w.parts);
     if (f.b < 0) return;
-    const double scale = scale_of(a, f.b);
-    if (scale == 0.0) return;
+    const float by = by_of(a, f.b);
+    if (by == 0.f) return;
     const long long r = f.first + f.index;
     const void* row = row_at<BF16>(a, r);
     const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
@@ -152,29 +152,28 @@ __global__ void __launch_bounds__(kThreads) sample_stats_kernel(SampledArgs a, S
 #pragma unroll
         for (int k = 0; k < U; ++k) u[k] = next[k];
         if (i0 + U * kThreads < end) fetch(i0 + U * kThreads, next);
+        float x[U * E];
 #pragma unroll
         for (int k = 0; k < U; ++k) {
-            if (i0 + k * kThreads + (tid & ~63) >= end) break;
             const uint32_t v[4] = {u[k].x, u[k].y, u[k].z, u[k].w};
-            float x[E];
 #pragma unroll
             for (int e = 0; e < E; ++e) {
                 if constexpr (BF16)
-                    x[e] = __builtin_bit_cast(float, e & 1 ? v[e >> 1] & 0xFFFF0000u : v[e >> 1] << 16);
+                    x[k * E + e] = __builtin_bit_cast(float, e & 1 ? v[e >> 1] & 0xFFFF0000u : v[e >> 1] << 16);
                 else
-                    x[e] = __builtin_bit_cast(float, v[e]);
+                    x[k * E + e] = __builtin_bit_cast(float, v[e]);
             }
-            take<E>(s, x, scale);
         }
+        take<U * E>(s, x, by);
     }
     if (wave == 0) {
         const bool first = part == 0 && lane < head, last = part == w.parts - 1 && lane < tail;
         const float x[2] = {first ? logit<BF16>(row, lane) : -kInf, last ? logit<BF16>(row, a.V - tail + lane) : -kInf};
-        take<2>(s, x, scale);
+        take<2>(s, x, by);
     }
     __shared__ Stat waves[kThreads / 64];
     const float m = wave_max(s.m);
-    const double z = wave_sum(moved(s, m, scale));
+    const double z = wave_sum(moved(s, m, by));
     if (lane == 0) waves[wave] = Stat{z, m, 0};
     __syncthreads();
     if (tid == 0) {
@@ -183,18 +182,18 @@ __global__ void __launch_bounds__(kThreads) sample_stats_kernel(SampledArgs a, S
         for (int i = 1; i < kThreads / 64; ++i) top = fmaxf(top, waves[i].m);
         double sum = 0.0;
 #pragma unroll
-        for (int i = 0; i < kThreads / 64; ++i) sum += moved(waves[i], top, scale);
+        for (int i = 0; i < kThreads / 64; ++i) sum += moved(waves[i], top, by);
         w.stats[r * w.parts + part] = Stat{sum, top, 0};
     }
 }
 
 // m and z of row r, in every lane.
-__device__ __forceinline__ Stat row_stat(const Split& w, long long r, double scale) {
+__device__ __forceinline__ Stat row_stat(const Split& w, long long r, float by) {
     const int lane = threadIdx.x & 63;
     Stat s{0.0, -kInf, 0};
     if (lane < w.parts) s = w.stats[r * w.parts + lane];
     const float m = wave_max(s.m);
-    return Stat{wave_sum(moved(s, m, scale)), m, 0};
+    return Stat{wave_sum(moved(s, m, by)), m, 0};
 }
 
 // Weights of a row, times z.
@@ -213,8 +212,8 @@ __device__ __forceinline__ int kind_of(const SampledArgs& a, const Found& f) { r
 
 template <bool BF16>
 __device__ __forceinline__ Weights weights_of(const SampledArgs& a, const Found& f) {
-    return Weights{row_at<BF16>(a, f.row), a.probs ? a.probs + f.row * a.probs_ld : nullptr, f.z, f.m,
-                   static_cast<float>(f.scale * kLog2e), a.probs ? KDA_NO_TOKEN : a.drafts[f.row]};
+    return Weights{row_at<BF16>(a, f.row), a.probs ? a.probs + f.row * a.probs_ld : nullptr, f.z, f.m, f.by,
+                   a.probs ? KDA_NO_TOKEN : a.drafts[f.row]};
 }
 
 // Weights w and e = p z of tokens v0, v0 + step, ... below end (> v0 - step N); 0 behind it.
@@ -262,7 +261,7 @@ __global__ void __launch_bounds__(kTokenThreads) sample_token_kernel(SampledArgs
     Mass mass{0.0, 0.0};
     if (lane < w.pieces) mass = w.mass[b * w.pieces + lane];
     if (f.row < 0) return;
-    if (f.scale == 0.0) {
+    if (f.by == 0.f) {
         if (tid == 0) {
             a.out[2 * b] = f.j;
             a.out[2 * b + 1] = KDA_NO_TOKEN;
@@ -338,19 +337,20 @@ __global__ void __launch_bounds__(kAcceptThreads) sample_accept_kernel(SampledAr
         if (group == 0 && tid == 0) w.found[b].row = -1;
         return;
     }
-    const double scale = scale_of(a, b), u_last = a.u[last - 1];
-    if (tid == 0) stop = scale == 0.0 ? 0 : n - 1;
+    const double u_last = a.u[last - 1];
+    const float by = by_of(a, b);
+    if (tid == 0) stop = by == 0.f ? 0 : n - 1;
     __syncthreads();
     for (int i = wave; i < n - 1; i += WAVES) {
         const long long r = first + i;
         double p = __builtin_nan("");
-        if (scale != 0.0) {
+        if (by != 0.f) {
             const uint32_t d = a.drafts[r];
             const bool real = d < static_cast<uint32_t>(a.V);
             const float x = real ? logit<BF16>(row_at<BF16>(a, r), d) : -kInf;
             const double q = a.probs && real ? a.probs[r * a.probs_ld + d] : 1.0, u = a.u[r];
-            const Stat s = row_stat(w, r, scale);
-            if (s.m != -kInf) p = exp((static_cast<double>(x) - s.m) * scale) / s.z;
+            const Stat s = row_stat(w, r, by);
+            if (s.m != -kInf) p = exp2((static_cast<double>(x) - s.m) * by) / s.z;
             if (lane == 0 && !(u * q < p)) atomicMin(&stop, i);
         }
         if (lane == 0 && group == 0 && a.p_draft) a.p_draft[r] = static_cast<float>(p);
@@ -359,16 +359,16 @@ __global__ void __launch_bounds__(kAcceptThreads) sample_accept_kernel(SampledAr
     if (wave == 0) {
         const int j = stop;
         Stat s{0.0, -kInf, 0};
-        if (scale != 0.0) s = row_stat(w, first + j, scale);
+        if (by != 0.f) s = row_stat(w, first + j, by);
         const bool bad = s.m == -kInf || !(s.z < __builtin_inf());
         if (lane == 0) {
-            shared = Found{s.z, bad ? 0.0 : scale, u_last, s.m, first + j, j, j < n - 1};
+            shared = Found{s.z, u_last, s.m, bad ? 0.f : by, first + j, j, j < n - 1};
             if (group == 0) w.found[b] = shared;
         }
     }
     __syncthreads();
     const Found f = shared;
-    if (f.scale == 0.0) return;
+    if (f.by == 0.f) return;
     const Weights weights = weights_of<BF16>(a, f);
     const int kind = kind_of(a, f);
     const int each = piece_tokens(a, w);
