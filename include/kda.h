@@ -32,7 +32,8 @@
  *     Faults inside a kernel surface at the caller's next synchronization.
  *   - Row inputs (q, k, v, g, beta) are all f32 (KDA_IN_F32) or all bf16
  *     (KDA_IN_BF16, widened exactly by bits << 16 as dflash.rs, memra-engine
- *     0.98.0, fn bf16_to_f32, does).  State and outputs are always f32.
+ *     0.98.0, fn bf16_to_f32, does).  State and outputs are always f32 (but for
+ *     kda_attn_rows and the cache that it reads, which are in in_dtype).
  *   - Inputs must be finite; NaN/Inf are not checked on the hot path.
  *   - Results are deterministic: for a given input every entry point gives
  *     the same bits on every call, and a T-row scan gives the same bits as T
