@@ -100,7 +100,7 @@ struct Plan {
     int heads;       // query heads of a part
     int rows;        // rows of a tile
     int slots;       // tiles of columns, at most
-    int parts;       // workgroups a (key head, part) that the keys are split for; 0: not split
+    int parts;       // workgroups a (key head, part) beside those of the tiles, for which the keys are split; 0: not split
 };
 
 __host__ __device__ inline int div_up(int a, int b) { return (a + b - 1) / b; }
@@ -117,7 +117,7 @@ Plan plan_of(int R, int B, int H, int Hk, bool wide) {
     const int target = wide ? kTargetWide : kTargetNarrow;
     // parts + slots workgroups at most: as many as run side by side
     const int side = target / (Hk * p.groups);
-    p.parts = n >= target ? 0 : side > p.slots ? side - p.slots : 1;
+    p.parts = n < target && side > p.slots ? side - p.slots : 0;
     return p;
 }
 
@@ -133,7 +133,7 @@ struct Item {
 };
 
 // The items of all sequences, one after the other: (tile of columns, split).
-// Every wave runs it by itself; B < 64 * 64.
+// Every wave runs it by itself; up to 64 sequences a lane.
 __device__ __forceinline__ Item find_item(const AttnArgs& a, const Plan& p, int kt, int item) {
     const int lane = threadIdx.x & 63;
     const int capacity = a.c.seq_pages << a.c.page_shift;
