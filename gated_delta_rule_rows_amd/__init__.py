@@ -794,7 +794,8 @@ def attn_workspace(R: int, B: int, H: int, Hk: int, device=None) -> torch.Tensor
 
 
 def accept_sampled_workspace(R: int, B: int, V: int, device=None) -> torch.Tensor:
-    """Scratch for a kda_accept_sampled call of R rows of V logits in B sessions."""
+    """Scratch for kda_accept_sampled calls of up to R rows of up to V logits in up to B sessions
+    (uint8, contents irrelevant).  Calls that may run at the same time need their own."""
     return _workspace(_work_bytes(load().kda_accept_sampled_work_bytes, R, B, V), device)
 
 

@@ -411,13 +411,18 @@ __global__ void __launch_bounds__(kAcceptThreads) sample_accept_kernel(SampledAr
     }
 }
 
-// Enough workgroups to fill the chip, each with four loads a lane at least.
+constexpr int kFill = 2048;   // workgroups that fill the chip
+
+// Parts of a row that leave each four loads a lane at least.
+int most_parts(int V, int es) {
+    const long long loads = (static_cast<long long>(V) * es + 15) / 16, p = (loads + 4 * kThreads - 1) / (4 * kThreads);
+    return static_cast<int>(p < kMostParts ? p : kMostParts);
+}
+
+// Of them as many as fill the chip.
 int parts_of(int R, int V, int es) {
-    const long long loads = (static_cast<long long>(V) * es + 15) / 16;
-    long long p = (loads + 4 * kThreads - 1) / (4 * kThreads);
-    const long long fill = (2048 + R - 1) / R;
-    p = p < fill ? p : fill;
-    return static_cast<int>(p > kMostParts ? kMostParts : p);
+    const int p = most_parts(V, es), fill = (kFill + R - 1) / R;
+    return p < fill ? p : fill;
 }
 
 int pieces_of(int V) {
@@ -452,9 +457,11 @@ hipError_t launch(const SampledArgs& a, hipStream_t stream) {
 
 }  // namespace
 
+// Grows with R, B and V, though the parts of a row become fewer with R: R rows have R * most_parts() statistics at
+// most, and R * ceil(kFill / R) < kFill + R.  (f32 rows are the longer ones: never fewer parts than bf16 rows.)
 long long sampled_work_bytes(int R, int B, int V) {
-    // f32 rows are the longer ones: never fewer parts than bf16 rows
-    return static_cast<long long>(R) * parts_of(R, V, 4) * static_cast<long long>(sizeof(Stat)) +
+    const long long all = static_cast<long long>(R) * most_parts(V, 4), fill = static_cast<long long>(R) + kFill - 1;
+    return (all < fill ? all : fill) * static_cast<long long>(sizeof(Stat)) +
            static_cast<long long>(B) * (pieces_of(V) * static_cast<long long>(sizeof(Mass)) + static_cast<long long>(sizeof(Found)));
 }
 

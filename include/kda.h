@@ -646,7 +646,7 @@ int kda_accept_sampled(const void* logits, long long ld, int in_dtype, const flo
                        long long probs_ld, const int32_t* offsets, const uint32_t* drafts,
                        const float* u, const float* temp, uint32_t* out, float* p_draft, int R,
                        int B, int V, void* work, long long work_bytes, void* stream);
-/* Workspace bytes of kda_accept_sampled; -1 on a bad count. */
+/* Workspace bytes of kda_accept_sampled (they never shrink as R, B or V grow); -1 on a bad count. */
 long long kda_accept_sampled_work_bytes(int R, int B, int V);
 
 /* Message for the last nonzero status returned on the calling thread. */

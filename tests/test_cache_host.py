@@ -223,3 +223,22 @@ def test_python_binding_refuses_what_it_sees(lib):
         kda.attn_workspace(1 << 32, 1, 8, 1, device="cpu")
     with pytest.raises(kda.KdaError):
         kda.accept_sampled_workspace(1, 1, 1 << 31, device="cpu")
+
+
+def test_sampled_workspace_never_shrinks(lib):
+    """One buffer of a loop's largest round serves every smaller one."""
+    size = lib.kda_accept_sampled_work_bytes
+    for B in (1, 15, 64, 4096):
+        for V in (1, 7, 4096, 4097, 50001, 150000, 300007, 1 << 20, 1 << 30):
+            last = 0
+            for R in range(1, 4200, 1 if V == 150000 else 37):
+                n = size(R, B, V)
+                assert n >= last > -1
+                last = n
+            # what a call itself lays out, part by part of its rows: min(ceil(2048 / R), 64, whole parts of 4096 f32 logits)
+            for R in (1, 2, 3, 31, 32, 33, 63, 511, 512, 2047, 2048, 2049, 4096):
+                parts = min(-(-2048 // R), 64, -(-V // 4096))
+                assert size(R, B, V) >= R * parts * 16
+    for R in (1, 15, 511, 512, 5000):
+        for B, V in ((1, 1000), (64, 150000)):
+            assert size(R, B, V) <= min(size(R, B + 1, V), size(R, B, V + 1), size(R, B, 2 * V))

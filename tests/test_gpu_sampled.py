@@ -194,3 +194,17 @@ def test_sampled_without_rows():
                            torch.empty(0, dtype=torch.int32, device="cuda"), torch.empty(0, device="cuda"), out)
     torch.cuda.synchronize()
     assert (out == 3).all()
+
+
+@pytest.mark.parametrize("dt", [torch.float32, torch.bfloat16])
+def test_sampled_rounds_of_fewer_rows_share_the_largest_ones_workspace(dt):
+    V, B = 20011, 64
+    work = kda.accept_sampled_workspace(B * 8, B, V)
+    for rows in ([8] * B, [8] * 63 + [7], [8, 6] * 32, [1] * B, [9, 1, 0, 15, 3], [7], [1], [2, 2, 2]):
+        x, offsets, drafts, u, probs = _inputs(rows, V, dt, sum(rows))
+        n = offsets[-1]
+        x, drafts, u, probs = x[:n], drafts[:n], u[:n], probs[:n]
+        want, want_p = _call(x, offsets, drafts, u, probs)
+        work.fill_(0xFF)
+        got, got_p = _call(x, offsets, drafts, u, probs, work=work)
+        assert torch.equal(got, want) and torch.equal(got_p, want_p)
