@@ -12,8 +12,12 @@
 // finds the piece that holds the place, and the token in it.  (As the work of the
 // second's last workgroup the third's cost more than a launch: release and acquire
 // over the chip's eight L2 caches, 28 us for 15 rows of 50,001 against 18.)
-// The exponentials are f32; their sums, p - q (which cancels) and the running
-// sums (which decide between two tokens near their border) are f64.
+// The exponentials of whole rows are f32; their sums, a draft's p, p - q (which
+// cancels) and the running sums (which decide between two tokens near their border)
+// are f64.  An f32 exponential is off by three roundings of its argument (log2(e) / T,
+// x - m and their product), 3 (m - x) / T half steps, and its own; the sum of a row by
+// the mean of that, and the mean of (m - x) / T under p is ln V at most: it is the row's
+// entropy less the logarithm of a sum of 1 at least.
 //
 // On an MI355X, calls in a loop: 64 sessions x 8 rows of 150,000 bf16 58 us (38 at
 // the 5.1 TB/s of a large copy): the logits 36 us, 4.3 TB/s, bound by VALU (0.90),
@@ -42,7 +46,7 @@ constexpr int kChunk = 4096;         // tokens of a piece, if that makes no more
 constexpr int kAcceptThreads = 512;
 constexpr int kTokenThreads = 512;
 
-// m, about the largest x, and z = sum 2^{(x - m) by}, by = log2(e) / T in f32; z is NaN where a value is NaN
+// m, about the largest x, and z = sum 2^{(x - m) by}, by = log2(e) / T; z is NaN where a value is NaN
 // or +inf.  (Taken as x by - c in one operation a power would be cheaper, but where x / T is large the rounding
 // of c alone would pass f32's range.)
 struct Stat {
@@ -55,8 +59,8 @@ struct Stat {
 struct Found {
     double z;
     double u;      // of the session's last row
+    double by;     // 0: no token
     float m;
-    float by;      // 0: no token
     int row;       // -1: the session has no rows
     int j;
     int drafted;   // weights max(p - q, 0) unless these are all 0; else p
@@ -90,9 +94,9 @@ __device__ __forceinline__ const void* row_at(const SampledArgs& a, long long r)
 }
 
 // log2(e) / T of a session; 0 where T is no finite number of 1e-30 at least (it has to be one in f32).
-__device__ __forceinline__ float by_of(const SampledArgs& a, int b) {
+__device__ __forceinline__ double by_of(const SampledArgs& a, int b) {
     const float t = a.temp ? a.temp[b] : 1.f;
-    return t >= 1e-30f && t < kInf ? static_cast<float>(kLog2e / t) : 0.f;
+    return t >= 1e-30f && t < kInf ? kLog2e / t : 0.0;
 }
 
 __device__ __forceinline__ double wave_sum(double x) { return of_lane(running_sum(x), 63); }
@@ -102,17 +106,18 @@ __device__ __forceinline__ float wave_max(float x) {
 }
 
 // s's z at a reference m >= s.m.
-__device__ __forceinline__ double moved(Stat s, float m, float by) {
+__device__ __forceinline__ double moved(Stat s, float m, double by) {
     return s.m == -kInf ? s.z : s.z * exp2((static_cast<double>(s.m) - m) * by);
 }
 
 // Adds E values of a lane.
 template <int E>
-__device__ __forceinline__ void take(Stat& s, const float (&x)[E], float by) {
+__device__ __forceinline__ void take(Stat& s, const float (&x)[E], double by) {
+    const float by32 = static_cast<float>(by);
     float top = x[0];
 #pragma unroll
     for (int e = 1; e < E; ++e) top = fmaxf(top, x[e]);
-    if (__ballot(((top - s.m) * by > kSlack) | (s.m == -kInf))) {
+    if (__ballot(((top - s.m) * by32 > kSlack) | (s.m == -kInf))) {
         const float m = fmaxf(s.m, top);
         s.z = moved(s, m, by);
         s.m = m;
@@ -120,7 +125,7 @@ __device__ __forceinline__ void take(Stat& s, const float (&x)[E], float by) {
     const float base = s.m == -kInf ? 0.f : s.m;
     float z[4] = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
-    for (int e = 0; e < E; ++e) z[e & 3] += __builtin_amdgcn_exp2f((x[e] - base) * by);
+    for (int e = 0; e < E; ++e) z[e & 3] += __builtin_amdgcn_exp2f((x[e] - base) * by32);
     s.z += (z[0] + z[1]) + (z[2] + z[3]);
 }
 
@@ -130,8 +135,8 @@ __global__ void __launch_bounds__(kThreads) sample_stats_kernel(SampledArgs a, S
     const int part = blockIdx.x % w.parts;
     const Part f = find_part(a, 1, blockIdx.x / w.parts);
     if (f.b < 0) return;
-    const float by = by_of(a, f.b);
-    if (by == 0.f) return;
+    const double by = by_of(a, f.b);
+    if (by == 0.0) return;
     const long long r = f.first + f.index;
     const void* row = row_at<BF16>(a, r);
     const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
@@ -193,7 +198,7 @@ __global__ void __launch_bounds__(kThreads) sample_stats_kernel(SampledArgs a, S
 }
 
 // m and z of row r, in every lane.
-__device__ __forceinline__ Stat row_stat(const Split& w, long long r, float by) {
+__device__ __forceinline__ Stat row_stat(const Split& w, long long r, double by) {
     const int lane = threadIdx.x & 63;
     Stat s{0.0, -kInf, 0};
     if (lane < w.parts) s = w.stats[r * w.parts + lane];
@@ -217,7 +222,7 @@ __device__ __forceinline__ int kind_of(const SampledArgs& a, const Found& f) { r
 
 template <bool BF16>
 __device__ __forceinline__ Weights weights_of(const SampledArgs& a, const Found& f) {
-    return Weights{row_at<BF16>(a, f.row), a.probs ? a.probs + f.row * a.probs_ld : nullptr, f.z, f.m, f.by,
+    return Weights{row_at<BF16>(a, f.row), a.probs ? a.probs + f.row * a.probs_ld : nullptr, f.z, f.m, static_cast<float>(f.by),
                    a.probs ? KDA_NO_TOKEN : a.drafts[f.row]};
 }
 
@@ -266,7 +271,7 @@ __global__ void __launch_bounds__(kTokenThreads) sample_token_kernel(SampledArgs
     Mass mass{0.0, 0.0};
     if (lane < w.pieces) mass = w.mass[b * w.pieces + lane];
     if (f.row < 0) return;
-    if (f.by == 0.f) {
+    if (f.by == 0.0) {
         if (tid == 0) {
             a.out[2 * b] = f.j;
             a.out[2 * b + 1] = KDA_NO_TOKEN;
@@ -343,13 +348,13 @@ __global__ void __launch_bounds__(kAcceptThreads) sample_accept_kernel(SampledAr
         return;
     }
     const double u_last = a.u[last - 1];
-    const float by = by_of(a, b);
-    if (tid == 0) stop = by == 0.f ? 0 : n - 1;
+    const double by = by_of(a, b);
+    if (tid == 0) stop = by == 0.0 ? 0 : n - 1;
     __syncthreads();
     for (int i = wave; i < n - 1; i += WAVES) {
         const long long r = first + i;
         double p = __builtin_nan("");
-        if (by != 0.f) {
+        if (by != 0.0) {
             const uint32_t d = a.drafts[r];
             const bool real = d < static_cast<uint32_t>(a.V);
             const float x = real ? logit<BF16>(row_at<BF16>(a, r), d) : -kInf;
@@ -364,16 +369,16 @@ __global__ void __launch_bounds__(kAcceptThreads) sample_accept_kernel(SampledAr
     if (wave == 0) {
         const int j = stop;
         Stat s{0.0, -kInf, 0};
-        if (by != 0.f) s = row_stat(w, first + j, by);
+        if (by != 0.0) s = row_stat(w, first + j, by);
         const bool bad = s.m == -kInf || !(s.z < __builtin_inf());
         if (lane == 0) {
-            shared = Found{s.z, u_last, s.m, bad ? 0.f : by, first + j, j, j < n - 1};
+            shared = Found{s.z, u_last, bad ? 0.0 : by, s.m, first + j, j, j < n - 1};
             if (group == 0) w.found[b] = shared;
         }
     }
     __syncthreads();
     const Found f = shared;
-    if (f.by == 0.f) return;
+    if (f.by == 0.0) return;
     const Weights weights = weights_of<BF16>(a, f);
     const int kind = kind_of(a, f);
     const int each = piece_tokens(a, w);

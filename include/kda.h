@@ -635,7 +635,10 @@ long long kda_attn_rows_work_bytes(int R, int B, int H, int Hk);
  *   there the token is KDA_NO_TOKEN.  A temperature that is no finite number of
  *   1e-30 at least: j = 0, KDA_NO_TOKEN and NaN.
  *   Weights and running sums are f64, and so is the sum of a row's exponentials,
- *   which are f32: p is good to about 1e-6 of itself.
+ *   which are f32.  A draft's p is off by (3 ln V + 26) 2^-24 of itself at most (3.7e-6
+ *   for V = 150,000; some 1e-7 as a rule), the weight of token v by
+ *   (3 ln V + 50 + 3 (max x - x_v) / T) 2^-24 of its p; a p below 2^-126 of the row's
+ *   largest may weigh 0.
  *   work      : kda_accept_sampled_work_bytes(R, B, V) bytes, 16-byte aligned, in
  *               any state on entry.  Calls that can run at the same time need
  *               different work buffers.

@@ -208,3 +208,25 @@ def test_sampled_rounds_of_fewer_rows_share_the_largest_ones_workspace(dt):
         work.fill_(0xFF)
         got, got_p = _call(x, offsets, drafts, u, probs, work=work)
         assert torch.equal(got, want) and torch.equal(got_p, want_p)
+
+
+@pytest.mark.parametrize("dt", [torch.float32, torch.bfloat16])
+@pytest.mark.parametrize("V", [2, 600])
+def test_sampled_probabilities_of_unlikely_drafts(dt, V):
+    """A draft far behind the likeliest token, at any temperature: p down to f32's smallest numbers."""
+    gen = torch.Generator().manual_seed(V)
+    B = 64
+    temp = 0.4 + 2 * torch.rand(B, generator=gen)
+    x = torch.randn(2 * B, V, generator=gen)
+    drafts = torch.randint(0, V, (2 * B,), generator=gen)
+    x[torch.arange(2 * B), drafts] = -(60 + 20 * torch.rand(2 * B, generator=gen)) * temp.repeat_interleave(2)
+    x, temp = x.to(dt).cuda(), temp.cuda()
+    offsets = list(range(0, 2 * B + 1, 2))
+    _, p = _call(x, offsets, drafts.to(torch.int32).cuda(), torch.rand(2 * B, generator=gen).cuda(), temp=temp)
+    _, want, _ = accept_ref(x, offsets, drafts, torch.zeros(2 * B), temp=temp)
+    for r, w in want.items():
+        assert w > 2.0**-126
+        # half steps of f32 (2^-24): the sum's exponentials, 3 (ln V + 6 ln 2) of their arguments in the mean (three
+        # roundings each; the reference that they are taken from may lag by 6 in base 2), 2 of their own,
+        # 10 of the additions of 32 of them; the quotient is f64 and rounded once
+        assert abs(float(p[r]) - w) <= (3 * (math.log(V) + 6 * math.log(2)) + 13) * 2.0**-24 * w, (r, float(p[r]) / w - 1)
