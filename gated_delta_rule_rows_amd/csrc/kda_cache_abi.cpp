@@ -3,7 +3,6 @@
 
 #include <hip/hip_runtime.h>
 
-#include <cmath>
 #include <cstdint>
 #include <utility>
 
@@ -17,6 +16,7 @@ using namespace kda;
 namespace {
 
 constexpr long long kStrideMax = 1ll << 40;     // elements
+constexpr float kScaleMax = 2e38f;              // times log2(e) it has to be finite in f32: scores are kept in base 2
 constexpr long long kGridMax = 1ll << 24;       // workgroups of 256 threads: 2^32 threads
 
 int check_packed(const char* fn, int R, int B) {
@@ -163,8 +163,9 @@ int kda_attn_rows(const void* q, long long q_ld, const kda_cache* cache, const i
     const char* fn = "kda_attn_rows";
     int rc;
     if ((rc = check_dtype(fn, in_dtype)) || (rc = check_heads(fn, H, Hk)) || (rc = check_packed(fn, R, B))) return rc;
-    if (!(scale > 0.f) || !std::isfinite(scale))
-        return refuse(KDA_ERR_RANGE, "%s: scale=%g is no positive finite number", fn, static_cast<double>(scale));
+    if (!(scale > 0.f) || !(scale <= kScaleMax))
+        return refuse(KDA_ERR_RANGE, "%s: scale=%g is no positive number up to %g", fn, static_cast<double>(scale),
+                      static_cast<double>(kScaleMax));
     if (window < 0) return refuse(KDA_ERR_RANGE, "%s: window=%d, need >= 0 (0: none)", fn, window);
     if (sinks < 0 || (sinks > 0 && window == 0))
         return refuse(KDA_ERR_RANGE, "%s: sinks=%d: need >= 0, and 0 without a window", fn, sinks);

@@ -581,7 +581,7 @@ int kda_cache_append(const void* k, long long k_ld, const void* v, long long v_l
  *   o         : [R][H][128] in in_dtype, contiguous.  (Not f32 for bf16 rows, as
  *               the scans' outputs are: it goes into a projection as it is.)  Rows that
  *               no sequence covers are not written.
- *   scale     : > 0, finite; 1/sqrt(128) as a rule.
+ *   scale     : > 0, up to 2e38; 1/sqrt(128) as a rule.
  *   window    : 0 for none; sinks >= 0, and 0 without a window.
  *   A row that sees no key gives 0.  A score of -inf counts as not seen; a NaN or
  *   +inf score makes NaN of its row's head.  A NaN or an infinity in a value makes

@@ -242,3 +242,11 @@ def test_sampled_workspace_never_shrinks(lib):
     for R in (1, 15, 511, 512, 5000):
         for B, V in ((1, 1000), (64, 150000)):
             assert size(R, B, V) <= min(size(R, B + 1, V), size(R, B, V + 1), size(R, B, 2 * V))
+
+
+def test_attn_scales_that_leave_f32_in_base_2(lib, b):
+    """2.4e38 log2(e) is an infinity in f32, and 0 times it a NaN."""
+    for scale in (2.4e38, 3.4e38):
+        _refused(lib, _attn(lib, b, R=0, q=None, o=None, scale=scale), ERR_RANGE, "scale")
+    for scale in (1e-45, 1e-38, 1.0, 1.9e38):
+        assert _attn(lib, b, R=0, q=None, o=None, scale=scale) == OK
