@@ -838,14 +838,14 @@ def _cache(k_pages, v_pages, table, lens, dtype, device):
         raise ValueError(f"k_pages and v_pages are on {k_pages.device} and {v_pages.device}, expected {device}")
     if strides[3] != 1:
         raise ValueError("the rows of a page must be contiguous")
-    of = table.shape
+    of = table.shape if table is not None else ()
     if len(of) != 2:
         raise ValueError("table must be a [B][pages of a sequence] tensor")
     pages, rows, Hk, _ = shape
     if pages > 0x7FFFFFFF or rows > 0x7FFFFFFF or of[1] > 0x7FFFFFFF:
         _int32(pages, rows, of[1])
     c = _pack_cache(k_pages.data_ptr(), v_pages.data_ptr(), _at(table, "table", torch.int32, of, device),
-                    _at(lens, "lens", torch.int32, of[:1], device), strides[0], strides[1], strides[2], pages, rows,
+                    _at(lens, "lens", torch.int32, of[:1], device) or 0, strides[0], strides[1], strides[2], pages, rows,
                     of[1])
     return c, of[0], Hk
 

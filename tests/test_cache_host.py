@@ -250,3 +250,18 @@ def test_attn_scales_that_leave_f32_in_base_2(lib, b):
         _refused(lib, _attn(lib, b, R=0, q=None, o=None, scale=scale), ERR_RANGE, "scale")
     for scale in (1e-45, 1e-38, 1.0, 1.9e38):
         assert _attn(lib, b, R=0, q=None, o=None, scale=scale) == OK
+
+
+class _Cpu:   # a device as the binding compares it: that of tensors on the CPU
+    index = -1
+
+
+def test_python_binding_refuses_a_cache_without_table_or_lengths(lib, b):
+    k, v = torch.zeros(2, 4, 16, 2, 128).unbind()
+    table = torch.zeros(3, 2, dtype=torch.int32)
+    with pytest.raises(ValueError, match="table"):
+        kda._cache(k, v, None, torch.zeros(3, dtype=torch.int32), torch.float32, _Cpu)
+    c, B, Hk = kda._cache(k, v, table, None, torch.float32, _Cpu)
+    _refused(lib, lib.kda_cache_append(b["q"], 256, b["g"], 256, c, b["s_out"], 6, B, Hk, 0, None), ERR_ARG, "cache.lens is NULL")
+    _refused(lib, lib.kda_attn_rows(b["q"], 512, c, b["s_out"], b["o"], 6, B, 4, Hk, 0.1, 0, 0, 0, b["snap"], 64 << 20, None),
+             ERR_ARG, "cache.lens is NULL")
