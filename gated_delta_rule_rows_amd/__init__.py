@@ -830,7 +830,8 @@ def _cache(k_pages, v_pages, table, lens, dtype, device):
     shape, strides, dev = k_pages.shape, k_pages.stride(), device.index
     if len(shape) != 4 or shape[3] != D:
         raise ValueError(f"k_pages must be [pages][rows][Hk][{D}], got {tuple(shape)}")
-    if v_pages.shape != shape or v_pages.stride() != strides:
+    if v_pages.shape != shape or (v_pages.stride() != strides and any(   # (one page, row or head has no stride)
+            n > 1 and x != y for n, x, y in zip(shape, strides, v_pages.stride()))):
         raise ValueError("k_pages and v_pages must have the same shape and strides")
     if k_pages.dtype is not dtype or v_pages.dtype is not dtype:
         raise TypeError(f"k_pages and v_pages must be {dtype}, got {k_pages.dtype} and {v_pages.dtype}")

@@ -265,3 +265,17 @@ def test_python_binding_refuses_a_cache_without_table_or_lengths(lib, b):
     _refused(lib, lib.kda_cache_append(b["q"], 256, b["g"], 256, c, b["s_out"], 6, B, Hk, 0, None), ERR_ARG, "cache.lens is NULL")
     _refused(lib, lib.kda_attn_rows(b["q"], 512, c, b["s_out"], b["o"], 6, B, 4, Hk, 0.1, 0, 0, 0, b["snap"], 64 << 20, None),
              ERR_ARG, "cache.lens is NULL")
+
+
+def test_python_binding_strides_of_one_page_row_or_head_are_free(lib, b):
+    table, lens = torch.zeros(3, 2, dtype=torch.int32), torch.zeros(3, dtype=torch.int32)
+    one_page = torch.zeros(1, 16, 2, 128), torch.zeros(1, 2, 16, 2, 128)[:, 1]
+    one_row = torch.zeros(4, 1, 2, 128), torch.zeros(4, 2, 1, 128).transpose(1, 2)
+    one_head = torch.zeros(4, 16, 1, 128), torch.zeros(4, 1, 16, 128).transpose(1, 2)
+    for k, v in (one_page, one_row, one_head):
+        assert k.stride() != v.stride()
+        for x, y in ((k, v), (v, k)):
+            c = kda._cache(x, y, table, lens, torch.float32, _Cpu)[0]
+            assert len(c) == ctypes.sizeof(_Cache)
+    with pytest.raises(ValueError, match="same shape and strides"):
+        kda._cache(torch.zeros(4, 16, 2, 128), torch.zeros(4, 2, 16, 128).transpose(1, 2), table, lens, torch.float32, _Cpu)
