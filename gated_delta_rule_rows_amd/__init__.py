@@ -843,8 +843,8 @@ def _cache(k_pages, v_pages, table, lens, dtype, device):
     if len(of) != 2:
         raise ValueError("table must be a [B][pages of a sequence] tensor")
     pages, rows, Hk, _ = shape
-    if pages > 0x7FFFFFFF or rows > 0x7FFFFFFF or of[1] > 0x7FFFFFFF:
-        _int32(pages, rows, of[1])
+    if pages > 0x7FFFFFFF or rows > 0x7FFFFFFF or of[0] > 0x7FFFFFFF or of[1] > 0x7FFFFFFF:
+        _int32(pages, rows, *of)
     c = _pack_cache(k_pages.data_ptr(), v_pages.data_ptr(), _at(table, "table", torch.int32, of, device),
                     _at(lens, "lens", torch.int32, of[:1], device) or 0, strides[0], strides[1], strides[2], pages, rows,
                     of[1])
@@ -864,6 +864,8 @@ def kda_cache_append(k, v, k_pages, v_pages, table, lens, offsets, stream=None) 
     dt = _row_dtype(k, "k")
     c, B, Hk = _cache(k_pages, v_pages, table, lens, dtype, dev)
     R = k.shape[0]
+    if R > 0x7FFFFFFF:   # (an expanded row)
+        _int32(R)
     shape = (R, Hk, D)
     kp, k_ld = _strided(k, "k", dtype, shape, dev)
     vp, v_ld = _strided(v, "v", dtype, shape, dev)
@@ -932,6 +934,8 @@ def kda_accept_sampled(logits, offsets, drafts, u, out, probs=None, temp=None, p
             raise ValueError("probs rows must be contiguous")
         qp = probs.data_ptr()
     B = offsets.shape[0] - 1 if offsets.dim() == 1 else -1
+    if B > 0x7FFFFFFF:
+        _int32(B)
     rows = (R,)
     wp, wn = _work(work, dev)
     _check(lib.kda_accept_sampled(

@@ -279,3 +279,9 @@ def test_python_binding_strides_of_one_page_row_or_head_are_free(lib, b):
             assert len(c) == ctypes.sizeof(_Cache)
     with pytest.raises(ValueError, match="same shape and strides"):
         kda._cache(torch.zeros(4, 16, 2, 128), torch.zeros(4, 2, 16, 128).transpose(1, 2), table, lens, torch.float32, _Cpu)
+
+
+def test_python_binding_refuses_more_sequences_than_a_c_int_counts(lib):
+    k, v = torch.zeros(2, 4, 16, 2, 128).unbind()
+    with pytest.raises(kda.KdaError, match="32 bits"):
+        kda._cache(k, v, torch.zeros(1 << 32, 0, dtype=torch.int32), torch.zeros(3, dtype=torch.int32), torch.float32, _Cpu)

@@ -431,3 +431,13 @@ def test_attn_and_append_without_rows():
     kda.kda_attn_rows(none, k, v, table, lens, offsets, none, work=kda.attn_workspace(0, 1, 2, 2))
     torch.cuda.synchronize()
     assert torch.equal(k, before)
+
+
+def test_append_refuses_more_rows_than_a_c_int_counts():
+    # 2^32 rows of one row in memory: as a C int they would be none at all
+    gen = torch.Generator().manual_seed(1)
+    k, v, table = make_cache(gen, [20], 16, 2, torch.float32)
+    rows = torch.zeros(1, 2, D, device="cuda").expand(2**32, 2, D)
+    lens, offsets = torch.tensor([20], dtype=torch.int32, device="cuda"), torch.zeros(2, dtype=torch.int32, device="cuda")
+    with pytest.raises(kda.KdaError):
+        kda.kda_cache_append(rows, rows, k, v, table, lens, offsets)
