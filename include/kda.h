@@ -583,10 +583,11 @@ int kda_cache_append(const void* k, long long k_ld, const void* v, long long v_l
  *               no sequence covers are not written.
  *   scale     : > 0, up to 2e38; 1/sqrt(128) as a rule.
  *   window    : 0 for none; sinks >= 0, and 0 without a window.
- *   A row that sees no key gives 0.  A score of -inf counts as not seen; a NaN or
- *   +inf score makes NaN of its row's head.  A NaN or an infinity in a value makes
- *   a NaN or an infinity of its channel for the rows that see it; what lies in keys and
- *   values that a row does not see has no effect on it.
+ *   A row that sees no key gives 0, and so does one whose scores are all -inf: such a
+ *   score has no weight.  A NaN or +inf score makes NaN of its row's head.  A NaN or an
+ *   infinity in a value makes a NaN or an infinity of its channel for the rows that see
+ *   it, whatever its weight, 0 as well; what lies in keys and values that a row does not
+ *   see has no effect on it.
  *   Sums are f32.  The weights of bf16 rows are rounded to bf16 for their product
  *   with the values.  Results are deterministic; they depend on R, B, H and Hk, and on
  *   the lengths of all sequences, only in how sums are divided.

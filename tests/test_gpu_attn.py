@@ -441,3 +441,35 @@ def test_append_refuses_more_rows_than_a_c_int_counts():
     lens, offsets = torch.tensor([20], dtype=torch.int32, device="cuda"), torch.zeros(2, dtype=torch.int32, device="cuda")
     with pytest.raises(kda.KdaError):
         kda.kda_cache_append(rows, rows, k, v, table, lens, offsets)
+
+
+@pytest.mark.parametrize("dt", TYPES)
+@pytest.mark.parametrize("bad", [math.nan, math.inf])
+@pytest.mark.parametrize("n", [1, 15, 120])
+def test_attn_a_score_of_minus_infinity_has_no_weight_but_its_value_is_seen(dt, bad, n):
+    gen = torch.Generator().manual_seed(n)
+    length, dead = 333, [3, 200, 332]
+    k, v, table = make_cache(gen, [length], 16, 1, dt)
+    q = torch.randn(n, 2, D, generator=gen).to(dt).cuda()
+    q[..., 0] = 1.0
+    for j in dead:
+        k[int(table[0, j // 16]), j % 16, 0, 0] = -math.inf
+    k_finite = torch.where(torch.isinf(k), 0.0, k)
+    o, spoiled = (torch.empty(n, 2, D, dtype=dt, device="cuda") for _ in range(2))
+    _call(q, k, v, table, [length], [0, n], o)
+    torch.cuda.synchronize()
+    p = torch.arange(length - n, length)
+    # the same as if the keys' pages were not there: a cache of pages of one row, these keys' entries -1
+    rows_k, rows_v = (x.reshape(-1, 1, 1, D) for x in (k_finite, v))
+    rows = torch.full((1, length), -1, dtype=torch.int32)
+    for j in range(length):
+        if j not in dead:
+            rows[0, j] = int(table[0, j // 16]) * 16 + j % 16
+    _check(q, rows_k, rows_v, rows.cuda(), [length], [0, n], o, o)
+    for j in dead:
+        w = v.clone()
+        w[int(table[0, j // 16]), j % 16, 0, 77] = bad
+        _call(q, k, w, table, [length], [0, n], spoiled)
+        hit = torch.zeros(n, 2, D, dtype=torch.bool)
+        hit[p >= j, :, 77] = True
+        assert not torch.isfinite(spoiled[hit.cuda()]).any() and torch.equal(spoiled[~hit.cuda()], o[~hit.cuda()])
