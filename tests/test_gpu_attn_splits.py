@@ -72,3 +72,67 @@ def test_every_share_of_the_keys_is_joined_once(dt, even, news, lens, H, Hk, pag
                 heads = (factors[r] == factor).nonzero()[:, 0]
                 want = result(scores[:sees], channel[:sees], factor, torch.ones(sees, dtype=torch.float64))
                 assert len(heads) == 0 or not off(o[r, heads], want, rel), (b, r, factor)
+
+
+def _plain(q, k, v, table, lens, offsets, scale, window, sinks):
+    """o in 64 bits with the sizes that attn_bound takes, a head at a time on the GPU."""
+    R, H, _ = q.shape
+    page, Hk = k.shape[1], k.shape[2]
+    out, size, count, dot = (torch.zeros(R, H, D, dtype=torch.float64), torch.zeros(R, H, D, dtype=torch.float64),
+                             torch.zeros(R, dtype=torch.float64), torch.zeros(R, H, dtype=torch.float64))
+    for b, length in enumerate(lens):
+        first, last = offsets[b], offsets[b + 1]
+        j = torch.arange(length, device="cuda")
+        p = torch.arange(length - (last - first), length, device="cuda")[:, None]
+        sees = (j <= p) & ((j > p - window) | (j < sinks) if window else torch.ones_like(j <= p))
+        count[first:last] = sees.sum(1).cpu()
+        at = table[b, j // page].long(), j % page
+        for h in range(H):
+            K, V = (x[at[0], at[1], h // (H // Hk)].double() for x in (k, v))
+            Q = q[first:last, h].double()
+            x = (Q @ K.T.contiguous()) * scale
+            w = torch.softmax(x.masked_fill(~sees, -math.inf), 1)
+            out[first:last, h] = (w @ V).cpu()
+            size[first:last, h] = (w @ V.abs()).cpu()
+            dot[first:last, h] = ((Q.abs() @ K.abs().T.contiguous()) * scale).masked_fill(~sees, 0.0).amax(1).cpu()
+    return out, size, count, dot
+
+
+# Tiles of columns that fill the chip by themselves, so that no key is split, with pages of whole tiles: bf16, f32 of
+# many columns (the wide kernel) and of few (the narrow one).
+@pytest.mark.parametrize("window,sinks", [(0, 0), (150, 5)])
+@pytest.mark.parametrize("dt,news,lens,H,Hk,page", [
+    (torch.bfloat16, [300, 1, 130], [700, 40, 130], 128, 128, 64),
+    (torch.bfloat16, [500], [500], 128, 64, 128),
+    (torch.bfloat16, [1100], [1100], 64, 8, 64),
+    (torch.float32, [300, 1, 130], [700, 40, 130], 128, 128, 32),
+    (torch.float32, [500], [500], 128, 64, 64),
+    (torch.float32, [60] * 6, [60, 200, 333, 61, 128, 64], 128, 128, 64),
+    (torch.float32, [15] * 20, [400 + 7 * i for i in range(20)], 192, 64, 256),
+])
+def test_nothing_split_over_pages_of_whole_tiles(dt, news, lens, H, Hk, page, window, sinks):
+    gen = torch.Generator().manual_seed(sum(news))
+    k, v, table = make_cache(gen, lens, page, Hk, dt)
+    q = torch.randn(sum(news), H, D, generator=gen).to(dt).cuda()
+    scale, offsets = 1.0 / math.sqrt(D), _ends(news)
+    o = _call(q, k, v, table, lens, offsets, scale, window, sinks)
+    want, size, count, dot = _plain(q, k, v, table, lens, offsets, scale, window, sinks)
+    assert ((o.double().cpu() - want).abs() <= attn_bound(want, size, count, dot, dt)).all()
+
+
+@pytest.mark.parametrize("dt", TYPES)
+@pytest.mark.parametrize("bad", [math.nan, math.inf])
+def test_nothing_split_spoiled_values_reach_only_rows_that_see_them(dt, bad):
+    """Whole tiles and tiles of the diagonal, without splits."""
+    gen = torch.Generator().manual_seed(3)
+    n, length, H = 400, 500, 128
+    k, v, table = make_cache(gen, [length], 64, H, dt)
+    q = torch.randn(n, H, D, generator=gen).to(dt).cuda()
+    clean = _call(q, k, v, table, [length], [0, n], 0.1)
+    for j in (length - 1, length - 130, length - n, 20):
+        spoiled = v.clone()
+        spoiled[int(table[0, j // 64]), j % 64, 5, 77] = bad
+        o = _call(q, k, spoiled, table, [length], [0, n], 0.1)
+        hit = torch.zeros_like(clean, dtype=torch.bool)
+        hit[max(0, j - (length - n)):, 5, 77] = True
+        assert not torch.isfinite(o[hit]).any() and torch.equal(o[~hit], clean[~hit])
