@@ -230,3 +230,63 @@ def test_sampled_probabilities_of_unlikely_drafts(dt, V):
         # roundings each; the reference that they are taken from may lag by 6 in base 2), 2 of their own,
         # 10 of the additions of 32 of them; the quotient is f64 and rounded once
         assert abs(float(p[r]) - w) <= (3 * (math.log(V) + 6 * math.log(2)) + 13) * 2.0**-24 * w, (r, float(p[r]) / w - 1)
+
+
+@pytest.mark.parametrize("dt", [torch.float32, torch.bfloat16])
+@pytest.mark.parametrize("V", [262144, 262145, 300007, 600011])
+def test_sampled_vocabularies_whose_pieces_are_several_chunks(dt, V):
+    """Rows are summed in 64 pieces at most and searched 4,096 tokens at a time: tokens on both sides of the borders of
+    pieces and chunks, each drawn by a number in the middle of its share; rows that live in one chunk alone."""
+    gen = torch.Generator().manual_seed(V)
+    each = -(-V // min(64, -(-V // 4096)))
+    live = set()
+    for piece in (0, 1, 31, (V - 1) // each):
+        begin, end = piece * each, min(piece * each + each, V)
+        live |= {begin, begin + 1, begin + 4095, begin + 4096, begin + 4097, begin + 8191, begin + 8192, end - 1} & set(range(begin, end))
+    live = sorted(live)
+    near = [v for v in live if each <= v < each + 4096]
+    rows = []   # (tokens alive, the one that is drawn)
+    rows += [(live, v) for v in live]
+    rows += [(near, v) for v in near]
+    rows += [([v], v) for v in live[::5]]
+    x = torch.full((len(rows), V), -math.inf)
+    for r, (some, _) in enumerate(rows):
+        x[r, some] = torch.randn(len(some), generator=gen)
+    x = x.to(dt)
+    p = torch.softmax(x.double(), 1)
+
+    def middle(weights, v):   # of v's share: some 0.1 % of the whole at least, against 1e-5 that the sums are off by
+        c = torch.cumsum(weights, 0)
+        share = weights[v] / c[-1]
+        assert share > 1e-3
+        return float((c[v] - weights[v] / 2) / c[-1])
+
+    drawn = [v for _, v in rows]
+    u = torch.tensor([middle(p[r], v) for r, v in enumerate(drawn)], dtype=torch.float32)
+    # a session a row: the token of the row
+    out, _ = _call(x.cuda(), list(range(len(rows) + 1)), torch.zeros(len(rows), dtype=torch.int32, device="cuda"), u.cuda(), want_p=False)
+    assert out.tolist() == [[0, v] for v in drawn]
+    # sessions of two rows whose draft is rejected: without it, and with what p leaves of q
+    two = x.repeat_interleave(2, 0)
+    offsets = list(range(0, 2 * len(rows) + 1, 2))
+    drafts, left = [], torch.zeros(2 * len(rows), V)
+    u_two, u_left = torch.full((2 * len(rows),), 0.999999), torch.full((2 * len(rows),), 0.999999)
+    for r, (some, v) in enumerate(rows):
+        d = some[0] if some[0] != v else some[-1]       # (a row of one token: nothing is left, p itself)
+        drafts += [d, d]
+        w = p[r].clone()
+        if len(some) > 1:
+            w[d] = 0.0
+        u_two[2 * r + 1] = middle(w, v)
+        # q takes a half of each other token's share and all of the draft's and more
+        left[2 * r] = (p[r] / 2).float()
+        left[2 * r, d] = 1.0
+        w = (p[r] - left[2 * r].double()).clamp(min=0.0)
+        if len(some) == 1:
+            w = p[r]
+        u_left[2 * r + 1] = middle(w, v)
+    drafts = torch.tensor(drafts, dtype=torch.int32, device="cuda")
+    for probs, numbers in ((None, u_two), (left.cuda(), u_left)):
+        out, _ = _call(two.cuda(), offsets, drafts, numbers.cuda(), probs, want_p=False)
+        # (where one token lives, p = 1 at the draft: accepted, and drawn again)
+        assert out.tolist() == [[int(len(some) == 1), v] for some, v in rows]
