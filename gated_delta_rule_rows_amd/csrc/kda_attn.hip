@@ -17,21 +17,28 @@
 //
 // Where the tiles of columns are too few to fill the chip, the keys of a tile
 // are split over workgroups, which leave O, m and l in the workspace for a
-// second launch.
+// second launch.  Where they fill it, nothing is split, however uneven the
+// sequences are: with 8 key heads bf16 from 64 tiles on (64 places; few shares
+// are left from some 50 on).
 //
 // On an MI355X, calls in a loop (what a call cannot do without, at the 5.1 TB/s of
 // a large copy or the 1,300 TFLOP/s of a large bf16 product, in brackets): a prompt
-// of 4,096 rows x 64 heads bf16 314-326 us (211), 15 verify rows x 64 heads over
-// 65,536 keys 74 us (53), one token of 15 sessions of 82,000 keys in all 74 us (66),
-// ragged chunks of 1,420 rows x 12 heads 63 us (28), verify rounds of 8 sessions
+// of 4,096 rows x 64 heads bf16 317-334 us (211), 15 verify rows x 64 heads over
+// 65,536 keys 74-76 us (53), one token of 15 sessions of 82,000 keys in all 74 us (66),
+// ragged chunks of 1,420 rows x 12 heads 63-65 us (28), verify rounds of 8 sessions
 // with a window of 1,024, 16 heads f32, 41 us (19), one token over 300 keys 10.7 us.
-// The prompt is at 0.43 MFMA and 0.41 VALU activity: two waves a SIMD, whose
-// products and softmax overlap in part.  Two waves of 64 columns do not fit the
+// The prompt is at 0.42 MFMA and 0.41 VALU activity: two waves a SIMD, whose
+// products and softmax overlap in part, and its tiles start in the order of their rows, so that
+// those with the most keys end alone: 160 tiles' times of a place where the
+// mean is 130 (computed, not measured apart).  Two waves of 64 columns do not fit the
 // registers, one a SIMD leaves every latency open (587 us against 360 then).  V is read
 // in 8-byte transposing reads at half of LDS's rate; turning it on its way to LDS
 // cost as much as that saves (360 against 357).  Tiles of 32 keys with three
 // workgroups a CU took 376 us against 350.
-// Batches of few columns are bound by memory: 4.5 TB/s over the steps.
+// Batches of few columns are bound by memory: 4.5 TB/s over the steps.  The windowed
+// rounds wait (0.33 MFMA, 0.12 VALU): two tiles a wave, behind the plan, a table entry and K.
+// A step of 64 sessions, one of 65,536 keys and 63 of 300, takes 1,320 us (68): its
+// longest sequence is read by one workgroup a key head.
 
 #include <hip/hip_runtime.h>
 
@@ -612,9 +619,8 @@ struct Loader {
             *reinterpret_cast<u32x4*>(to + row0 * PITCH + piece * 16 + j * Sh::kRowsAtOnce * PITCH) = u.r[j];
     }
 
-    // Of V, where some row does not see all keys: 0 x NaN would carry a NaN or an infinity into rows that
-    // do not see it, so it is made 0, odd says which channels of which key it was, and the rows that see
-    // it get a NaN afterwards.  Whether the wave brought any.
+    // Of V, where some row does not see all keys: what the wide kernel does in LDS, before the rows go
+    // there.  Whether the wave brought any.
     __device__ __forceinline__ bool part(Rows& u, uint8_t* odd) const {
         uint32_t bad[Sh::kLoads], any = 0;
 #pragma unroll
@@ -895,7 +901,8 @@ __global__ void __launch_bounds__(kJoinThreads) attn_join_kernel(AttnArgs a, Pla
 // 32 columns each: 126 us against the wide kernel's 172; 96 columns 262 against 311; 120 columns 346 against
 // 314.  bf16 is bound by memory there, and the wide kernel holds more loads on their way with fewer
 // registers: one token of 15 sessions x 8,192 keys x 64 heads 98 us against 103, of one with 65,536 keys 24
-// against 39, 32 columns 62 against 76; there is no narrow kernel for it.
+// against 39, 32 columns 62 against 76; there is no narrow kernel for it.  (The average is all that the host
+// knows: a long chunk beside many single tokens is read in tiles of 32 columns too.)
 bool is_wide(int R, int B, int H, int Hk, bool bf16) {
     return bf16 || static_cast<long long>(R) * (H / Hk) > static_cast<long long>(B) * kNarrowColumns;
 }

@@ -20,7 +20,7 @@
 // entropy less the logarithm of a sum of 1 at least.
 //
 // On an MI355X, calls in a loop: 64 sessions x 8 rows of 150,000 bf16 58 us (38 at
-// the 5.1 TB/s of a large copy): the logits 36 us, 4.3 TB/s, bound by VALU (0.90),
+// the 5.1 TB/s of a large copy): the logits 36 us, 4.3 TB/s, bound by VALU (0.8-0.9),
 // the sums of row j 19 us, the token 5.  One round of 15 rows of 150,000 f32 17 us, a
 // token for each of 15 sessions 14 us: three launches of 4 to 8 us, latency.
 

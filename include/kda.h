@@ -588,11 +588,16 @@ int kda_cache_append(const void* k, long long k_ld, const void* v, long long v_l
  *   infinity in a value makes a NaN or an infinity of its channel for the rows that see
  *   it, whatever its weight, 0 as well; what lies in keys and values that a row does not
  *   see has no effect on it.
- *   Sums are f32.  The weights of bf16 rows are rounded to bf16 for their product
- *   with the values.  Results are deterministic; they depend on R, B, H and Hk, and on
+ *   Sums are f32, of weights up to 2^9 before they are divided by the sum of these: a
+ *   row's |values| may add up to 2^118.  The weights of bf16 rows are rounded to bf16 for
+ *   their product with the values.  Results are deterministic; they depend on R, B, H and Hk, and on
  *   the lengths of all sequences, only in how sums are divided.
+ *   A tile is the rows of a sequence that make 128 columns with the heads of a key
+ *   head (32 columns for few f32 rows).  Keys are divided among workgroups while B + R /
+ *   rows of a tile is below 512 / Hk (2048 / Hk); beyond, one workgroup a key head reads all
+ *   keys of a tile, and a batch takes as long as its longest sequence: 65,536 keys 1.3 ms.
  *   work      : kda_attn_rows_work_bytes(R, B, H, Hk) bytes, 16-byte aligned, in any
- *               state on entry.  Calls that can run at the same time need
+ *               state on entry (34 MB and more, for one token too).  Calls that can run at the same time need
  *               different work buffers.
  *   0 <= R <= KDA_PROMPT_ROWS_MAX, 1 <= B <= KDA_PROMPT_SEQS_MAX, Hk divides H <= 65535,
  *   as long as the grid holds them (refused beyond).  With R = 0 nothing is enqueued.
